@@ -76,6 +76,7 @@ typedef enum { SFI_F32 = 0, SFI_BF16 = 1 } sfi_dtype;
 #define SFI_DEV_WAIT_TIMEOUT   0x4u  /* a pipeline wait gave up */
 #define SFI_DEV_ITEMS_OVERFLOW 0x8u  /* more work items than the workspace holds */
 #define SFI_DEV_REFINE         0x10u /* a refinement met an inconsistent candidate list */
+#define SFI_DEV_NO_PAGES       0x20u /* too few free pages, or no room in the page table's row */
 
 typedef void* sfi_stream; /* a cudaStream_t */
 
@@ -303,6 +304,59 @@ sfi_status sfi_fast_attn_noalloc(const sfi_layout* layout, const sfi_params* par
                                  const void* q, const void* k, const void* v,
                                  const int32_t* idx, const int32_t* count, float* out,
                                  sfi_stream stream);
+
+/* ---------------------------------------------------------------- prompt attention */
+
+/* Causal attention over whole prompts, packed one after another (no
+ * counterpart on the pages, whose path starts at the filled cache): what
+ * produces a prompt's hidden states before its K and V rows go to a cache.
+ *
+ * Sequence b holds the query rows [cu_q[b], cu_q[b + 1]) of q and the key rows
+ * [cu_k[b], cu_k[b + 1]) of k and v; with n_q and n_k of them, query row i
+ * sits at position i + n_k - n_q and attends to the key rows j <= i + n_k - n_q
+ * (n_k = n_q: a whole prompt; n_k > n_q: the next chunk of a prompt whose
+ * earlier rows are in k and v already).  For query head h (KV head g):
+ *   s_j = q_{i,h} . k_{j,g} / sqrt(d),  out[i][h] = sum_j softmax(s)_j v_{j,g},
+ *   lse_out[i][h] = ln sum_j exp(s_j)                       (if not NULL).
+ * A row that sees no key (n_k < n_q, or n_k = 0) gets out = 0 and
+ * lse = -infinity.  Rows outside every sequence (behind cu_q[B], before
+ * cu_q[0]) are left untouched, and what lies in k and v outside a sequence's
+ * rows never reaches its outputs, NaN included.  Within a sequence V must be
+ * finite: a non-finite V row may also spoil rows at most 127 positions before
+ * its own (a K row only reaches the rows that attend to it).
+ *  - bf16 only.  out is bf16 too, unlike the decode calls' fp32: it is the
+ *    next matrix product's input.  Scores, softmax and sums are fp32, the
+ *    probabilities are rounded to bf16 for the product with V.  lse is fp32
+ *    [total_q][H_q].
+ *  - Row t of q starts q_stride elements after row t - 1 and holds H_q heads
+ *    of d elements one after another (0: H_q * d, nothing between); the same
+ *    for k, v (H_kv heads) and out.  Strides are at least a row and
+ *    multiples of 8 elements; the four pointers are 16-byte aligned.
+ *  - Any group size G = H_q / H_kv from 1 to 16; head_dim 64 or 128.
+ *  - cu_q and cu_k are ascending; an entry pair that descends or leaves
+ *    [0, total_q] ([0, total_k]) sets SFI_DEV_LEN_OVER_CAP and that sequence's
+ *    rows are not computed.
+ *  - total_q = 0 is a call that does nothing; total_k = 0 (k and v may then be
+ *    NULL) gives every row no key.
+ * The workspace (sfi_prefill_attn_workspace_size, 0 for invalid arguments)
+ * follows the shared rules, and so do the waits (sfi_set_wait_limit). */
+typedef struct {
+  int32_t batch;
+  int32_t n_q_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t dtype;   /* SFI_BF16 */
+  int32_t total_q; /* rows of q, out and lse_out */
+  int32_t total_k; /* rows of k and v */
+  int64_t q_stride, k_stride, v_stride, out_stride; /* elements; 0: rows without gaps */
+  const int32_t* cu_q; /* device [B + 1] */
+  const int32_t* cu_k; /* device [B + 1] */
+} sfi_packed_layout;
+
+size_t sfi_prefill_attn_workspace_size(const sfi_packed_layout* layout);
+sfi_status sfi_prefill_attn(const sfi_packed_layout* layout, const void* q, const void* k,
+                            const void* v, void* out, float* lse_out, void* ws, size_t ws_bytes,
+                            sfi_stream stream);
 
 /* ---------------------------------------------------------------- decode driver */
 

@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int32, c_size_t, c_uint32, c_void_p
+from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 from typing import Optional, Sequence
 
 import torch
@@ -25,7 +25,7 @@ SFI_OK, SFI_ERR_INVALID_ARG, SFI_ERR_UNSUPPORTED, SFI_ERR_CAPACITY, SFI_ERR_WORK
 SFI_F32, SFI_BF16 = 0, 1
 SFI_SELECT_FUSED, SFI_SELECT_LOGIT_SUM_SEQ, SFI_SELECT_LOGIT_SUM_HEAD = 0, 1, 2
 SFI_DEV_LEN_OVER_CAP, SFI_DEV_BAD_INDEX, SFI_DEV_WAIT_TIMEOUT, SFI_DEV_ITEMS_OVERFLOW = 1, 2, 4, 8
-SFI_DEV_REFINE = 16
+SFI_DEV_REFINE, SFI_DEV_NO_PAGES = 16, 32
 
 
 class sfi_layout(ctypes.Structure):
@@ -48,6 +48,14 @@ class sfi_ctx_desc(ctypes.Structure):
                 ("head_dim", c_int32), ("dtype", c_int32), ("max_len", c_int32),
                 ("n_layers", c_int32), ("params", sfi_params), ("budget", c_int32),
                 ("async_select", c_int32), ("refine", sfi_refine)]
+
+
+class sfi_packed_layout(ctypes.Structure):
+    _fields_ = [("batch", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32),
+                ("head_dim", c_int32), ("dtype", c_int32), ("total_q", c_int32),
+                ("total_k", c_int32), ("q_stride", c_int64), ("k_stride", c_int64),
+                ("v_stride", c_int64), ("out_stride", c_int64), ("cu_q", c_void_p),
+                ("cu_k", c_void_p)]
 
 
 _L = POINTER(sfi_layout)
@@ -75,6 +83,9 @@ EXPORTS = {
                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "sfi_fast_attn_noalloc": (c_int32, [_L, _P, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                         c_void_p, c_void_p]),
+    "sfi_prefill_attn_workspace_size": (c_size_t, [POINTER(sfi_packed_layout)]),
+    "sfi_prefill_attn": (c_int32, [POINTER(sfi_packed_layout), c_void_p, c_void_p, c_void_p,
+                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "sfi_ctx_create": (c_int32, [POINTER(sfi_ctx_desc), POINTER(c_void_p)]),
     "sfi_ctx_destroy": (c_int32, [c_void_p]),
     "sfi_decode_step": (c_int32, [c_void_p, c_int32, c_void_p, _L, c_void_p, c_void_p, c_void_p,
@@ -261,6 +272,80 @@ def sfi_fast_attn_noalloc(layout: Layout, prm: sfi_params, q, k, v, idx, count, 
     _check("sfi_fast_attn_noalloc", lib.sfi_fast_attn_noalloc(
         ctypes.byref(c), ctypes.byref(prm), _ptr(q), _ptr(k), _ptr(v), _ptr(idx), _ptr(count),
         _ptr(out), _stream(stream)))
+
+
+def _want(name: str, t: torch.Tensor, shape, dtype: torch.dtype, device: torch.device,
+          inner: int = 0) -> torch.Tensor:
+    """Refuse a tensor of another shape, type or device; its last ``inner`` dimensions must be
+    dense (0: all of them), and ``device`` must be the current one, where the kernels run."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} lies on {t.device}, the layout on {device}")
+    if not (t.is_contiguous() if inner == 0 else t.numel() == 0 or t[0].is_contiguous()):
+        raise ValueError(f"{name} must be dense{' behind its first dimension' if inner else ''}")
+    return t
+
+
+def _device_of(name: str, t: torch.Tensor) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name}: libsfi takes device tensors")
+    return t.device
+
+
+def _here(device: torch.device, stream) -> None:
+    """The kernels run on the current device, so the tensors and the stream must be its own."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors lie on {device}, but cuda:{torch.cuda.current_device()} is current")
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+
+
+class PackedLayout:
+    """Prompts packed one after another: sequence b's query rows are
+    cu_q[b]..cu_q[b + 1] of [total_q, H_q, d], its key rows cu_k[b]..cu_k[b + 1]
+    of [total_k, H_kv, d] (cu_*: int32 device tensors of batch + 1 entries)."""
+
+    def __init__(self, n_q_heads: int, n_kv_heads: int, head_dim: int, dtype: torch.dtype,
+                 cu_q: torch.Tensor, cu_k: torch.Tensor, total_q: int, total_k: int):
+        self.device = _device_of("cu_q", cu_q)
+        self.B = cu_q.numel() - 1
+        _want("cu_q", cu_q, (self.B + 1,), torch.int32, self.device)
+        _want("cu_k", cu_k, (self.B + 1,), torch.int32, self.device)
+        self.n_q_heads, self.n_kv_heads, self.head_dim, self.dtype = n_q_heads, n_kv_heads, head_dim, dtype
+        self.cu_q, self.cu_k = cu_q, cu_k
+        self.total_q, self.total_k = int(total_q), int(total_k)
+        self._c = sfi_packed_layout(self.B, n_q_heads, n_kv_heads, head_dim, dtype_code(dtype),
+                                    self.total_q, self.total_k, 0, 0, 0, 0, cu_q.data_ptr(),
+                                    cu_k.data_ptr())
+
+
+def prefill_workspace(layout: PackedLayout) -> torch.Tensor:
+    """A zero-filled workspace for sfi_prefill_attn."""
+    n = int(lib.sfi_prefill_attn_workspace_size(ctypes.byref(layout._c)))
+    if n == 0:
+        raise SfiError("sfi_prefill_attn_workspace_size", SFI_ERR_INVALID_ARG)
+    return torch.zeros(n, dtype=torch.uint8, device=layout.device)
+
+
+def sfi_prefill_attn(layout: PackedLayout, q, k, v, out, lse_out=None, ws=None, stream=None):
+    """q, out [total_q, H_q, d], k, v [total_k, H_kv, d], bf16, heads dense, any row stride (slices
+    of a joint projection); lse_out [total_q, H_q] fp32."""
+    L, c = layout, sfi_packed_layout.from_buffer_copy(layout._c)
+    _here(L.device, stream)
+    rq, rk = (L.total_q, L.n_q_heads, L.head_dim), (L.total_k, L.n_kv_heads, L.head_dim)
+    _want("q", q, rq, L.dtype, L.device, 2)
+    _want("k", k, rk, L.dtype, L.device, 2)
+    _want("v", v, rk, L.dtype, L.device, 2)
+    _want("out", out, rq, L.dtype, L.device, 2)
+    if lse_out is not None:
+        _want("lse_out", lse_out, rq[:2], torch.float32, L.device)
+    # (a row stride only means something where there is a second row)
+    c.q_stride, c.out_stride = (t.stride(0) if L.total_q > 1 else 0 for t in (q, out))
+    c.k_stride, c.v_stride = (t.stride(0) if L.total_k > 1 else 0 for t in (k, v))
+    _check("sfi_prefill_attn", lib.sfi_prefill_attn(
+        ctypes.byref(c), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse_out), _ptr(ws),
+        0 if ws is None else ws.numel(), _stream(stream)))
 
 
 def sfi_read_status(ws: torch.Tensor, stream=None) -> int:

@@ -339,6 +339,19 @@ bool encode_rows(CUtensorMap* m, const void* base, int D) {
 }
 }  // namespace
 
+bool encode_bf16_3d(CUtensorMap* m, const void* base, const uint64_t (&dims)[3],
+                    const uint64_t (&strides)[2], const uint32_t (&box)[3]) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
+  const cuuint64_t st[2] = {strides[0], strides[1]};
+  const cuuint32_t bx[3] = {box[0], box[1], box[2]};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), d, st, bx, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 void attach_tensor_maps(AttnArgs& a, const sfi_layout* L) {
   a.use_tma = 0;
   if (L->dtype != SFI_BF16) return;

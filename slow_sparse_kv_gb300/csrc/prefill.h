@@ -1,0 +1,29 @@
+// Kernel arguments of the prompt attention, shared by its C-ABI layer
+// (paged.cpp) and its kernel (prefill.cu).
+#pragma once
+
+#include "sfi_internal.h"
+
+namespace sfi {
+
+constexpr int kPrefillMaxGroup = 16;  // query heads per KV head, at most
+
+struct PrefillArgs {
+  // 3-D maps [row][head][d] of q, k and v, boxes of 64 elements of d with a
+  // 128-byte swizzle: G heads x 128 / G rows of q, 1 head x 128 rows of k and v
+  CUtensorMap tmq, tmk, tmv;
+  void* out;
+  float* lse;  // [total_q][H_q] or null
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int64_t out_stride;
+  int32_t B, H_q, H_kv, G, total_q, total_k;
+  int32_t tok;      // tokens per 128-row query tile: 128 / G
+  float scale_log2; // log2(e) / sqrt(d)
+  uint32_t* status;
+  long long wait_cycles;
+};
+
+cudaError_t launch_prefill(const PrefillArgs& a, int D, cudaStream_t st);
+
+}  // namespace sfi
