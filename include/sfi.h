@@ -358,6 +358,134 @@ sfi_status sfi_prefill_attn(const sfi_packed_layout* layout, const void* q, cons
                             const void* v, void* out, float* lse_out, void* ws, size_t ws_bytes,
                             sfi_stream stream);
 
+/* ---------------------------------------------------------------- paged cache */
+
+/* A KV cache in pages (no counterpart in the method's sources, which leave
+ * paged caches to the serving systems).  A pool holds n_pages pages; page x of
+ * k (and of v) starts page_stride elements after page x - 1 and is
+ * [H_kv][page_size][d] row-major, so K and V, or several layers, may share one
+ * allocation.  Sequence b's position i lies in row i % page_size of page
+ * page_table[b][i / page_size]; the sequence holds the first
+ * ceil(len[b] / page_size) entries of its row of the table, and the rest of the
+ * row is not read.
+ *  - page_size 1 to 1024 (any number; multiples of 16 load fastest),
+ *    max_pages * page_size <= 2^30, batch <= 1024, batch * n_kv_heads <= 4096,
+ *    n_pages <= 2^24, fewer than 2^31 rows of d elements from the pool's first to
+ *    its last.
+ *  - page_stride is a multiple of head_dim and at least a page (0: a page).
+ *    k and v are 16-byte aligned.
+ *  - Any group size G = H_q / H_kv from 1 to 16; head_dim 64 or 128; dtype
+ *    SFI_F32 or SFI_BF16.
+ *  - A len[b] outside [0, max_pages * page_size] sets SFI_DEV_LEN_OVER_CAP and
+ *    is taken as the nearer end (sfi_paged_attn) or leaves the sequence as it
+ *    is (the others); a page outside [0, n_pages) sets SFI_DEV_BAD_INDEX and is
+ *    read as page 0, and never written.
+ * One workspace (sfi_paged_workspace_size, 0 for invalid arguments) serves all
+ * calls of a geometry and follows the shared rules. */
+typedef struct {
+  int32_t batch;
+  int32_t n_q_heads; /* read by sfi_paged_attn only; a multiple of n_kv_heads */
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t dtype; /* sfi_dtype */
+  int32_t page_size;
+  int32_t n_pages;
+  int32_t max_pages;   /* entries in a row of the table */
+  int64_t page_stride; /* elements */
+  int32_t* page_table; /* device [B][max_pages] */
+  int32_t* len;        /* device [B] */
+} sfi_paged_layout;
+
+size_t sfi_paged_workspace_size(const sfi_paged_layout* layout);
+
+/* Attention of one new token per sequence over its whole paged cache:
+ *   out[b][h] = sum_{i < len[b]} softmax_i(q_h . k_{g,i} / sqrt(d)) v_{g,i},
+ *   lse_out[b][h] = ln sum_i exp(q_h . k_{g,i} / sqrt(d))    (if not NULL).
+ * len[b] includes the token, whose K and V are in the cache already
+ * (sfi_paged_append).  q: [B][H_q][d] (dtype), 16-byte aligned; out and lse_out
+ * fp32.  len[b] = 0 gives out = 0 and lse = -infinity.  Rows of a page at or
+ * past len[b] may hold anything.  One launch: all rows of all sequences are
+ * dealt evenly over the SMs, and the pieces of a split (sequence, KV head) are
+ * joined by whichever CTA finishes last, in a fixed order: the same call gives the
+ * same bits, but where a sequence is split, and so the order of its fp32 sums,
+ * depends on all lengths of the batch.  The waits for copies have the limit of
+ * sfi_set_wait_limit. */
+sfi_status sfi_paged_attn(const sfi_paged_layout* layout, const void* q, const void* k,
+                          const void* v, float* out, float* lse_out, void* ws, size_t ws_bytes,
+                          sfi_stream stream);
+
+/* Store new rows: sequence b's m = cu_new[b + 1] - cu_new[b] rows
+ * [cu_new[b], cu_new[b + 1]) of k_new and v_new ([total_new] rows of H_kv heads
+ * of d, k_stride and v_stride elements apart, 0: without gaps, else a multiple
+ * of 16 bytes and at least a row) become positions len[b] - m .. len[b] - 1;
+ * len[b] counts them already (sfi_pages_extend).  cu_new (device [B + 1]) may
+ * be NULL: one row per sequence, total_new = B.  A sequence whose rows leave
+ * [0, total_new] or outnumber len[b] is flagged (SFI_DEV_LEN_OVER_CAP) and left
+ * out; with cu_new NULL one with len[b] = 0 is an idle slot, whose row is not
+ * stored.  k_new and v_new are 16-byte aligned and apart from the pool. */
+sfi_status sfi_paged_append(const sfi_paged_layout* layout, int32_t total_new, const void* k_new,
+                            const void* v_new, int64_t k_stride, int64_t v_stride,
+                            const int32_t* cu_new, void* k, void* v, void* ws, size_t ws_bytes,
+                            sfi_stream stream);
+
+/* Page bookkeeping, on the device: ref[x] counts the table entries (and other
+ * holders, if the caller adds any) that hold page x; 0 is a free page.  New
+ * pages are the lowest free ones, in the order in which they are asked for.
+ * A full page may be shared; a sequence's last, partly filled page is its own.
+ * k and v are read by the calls that move rows (fork, compact, copy): the pool
+ * of layer j starts j * layer_stride elements (a multiple of head_dim) behind
+ * that of layer 0, and all layers use the same table.
+ * None of these calls may overlap another call on the same table, counts or
+ * pool. */
+typedef struct {
+  int32_t* ref; /* device [n_pages] */
+  void* k;
+  void* v;
+  int32_t n_layers;
+  int64_t layer_stride;
+} sfi_page_store;
+
+/* len[b] += n_new[b] (device [B]; NULL: 1 for every sequence that holds
+ * anything), with pages for the positions that need new ones.  Sequences are
+ * served in order; one that needs more pages than are left, or more entries
+ * than its row has, stays as it is and sets SFI_DEV_NO_PAGES; a negative n_new
+ * sets SFI_DEV_LEN_OVER_CAP. */
+sfi_status sfi_pages_extend(const sfi_paged_layout* layout, const sfi_page_store* store,
+                            const int32_t* n_new, void* ws, size_t ws_bytes, sfi_stream stream);
+
+/* For each pair i in order: sequence dst[i], which must be empty (len 0), becomes a
+ * copy of src[i]: it shares the full pages, and the rows of the last, partly
+ * filled one are copied, in every layer, to a new page.  src and dst are host
+ * arrays of n sequences; no dst twice and none that is a src too
+ * (SFI_ERR_INVALID_ARG).  A dst that is not empty sets SFI_DEV_BAD_INDEX, one
+ * for which no page is left SFI_DEV_NO_PAGES; both stay as they are. */
+sfi_status sfi_pages_fork(const sfi_paged_layout* layout, const sfi_page_store* store,
+                          const int32_t* src, const int32_t* dst, int32_t n, void* ws,
+                          size_t ws_bytes, sfi_stream stream);
+
+/* The listed sequences (host array of n, none twice) give up their pages: each
+ * entry's count falls by one, the entries become -1, len becomes 0.  A count that
+ * is 0 already stays 0 and sets SFI_DEV_BAD_INDEX. */
+sfi_status sfi_pages_free(const sfi_paged_layout* layout, const sfi_page_store* store,
+                          const int32_t* seqs, int32_t n, void* ws, size_t ws_bytes,
+                          sfi_stream stream);
+
+/* Close the holes: with n_live pages in use, the i-th used page at or past
+ * n_live moves to the i-th free one before it, in every layer, and the counts and
+ * the entries that sequences hold follow.  new_id (device [n_pages], may be
+ * NULL) gets each page's new place, -1 for a free one, for other holders. */
+sfi_status sfi_pages_compact(const sfi_paged_layout* layout, const sfi_page_store* store,
+                             int32_t* new_id, void* ws, size_t ws_bytes, sfi_stream stream);
+
+/* Copy whole pages, in every layer: page src[i] to page dst[i] (device arrays of
+ * n).  No dst may be another pair's dst or src (what such pages hold afterwards is
+ * not defined); src[i] = dst[i] is nothing to do.  A pair with a page outside
+ * [0, n_pages) is left out and sets SFI_DEV_BAD_INDEX.  Counts and tables stay
+ * as they are. */
+sfi_status sfi_pages_copy(const sfi_paged_layout* layout, const sfi_page_store* store,
+                          const int32_t* src, const int32_t* dst, int32_t n, void* ws,
+                          size_t ws_bytes, sfi_stream stream);
+
 /* ---------------------------------------------------------------- decode driver */
 
 typedef struct sfi_ctx sfi_ctx;

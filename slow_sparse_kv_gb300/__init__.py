@@ -58,8 +58,21 @@ class sfi_packed_layout(ctypes.Structure):
                 ("cu_k", c_void_p)]
 
 
+class sfi_paged_layout(ctypes.Structure):
+    _fields_ = [("batch", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32),
+                ("head_dim", c_int32), ("dtype", c_int32), ("page_size", c_int32),
+                ("n_pages", c_int32), ("max_pages", c_int32), ("page_stride", c_int64),
+                ("page_table", c_void_p), ("len", c_void_p)]
+
+
+class sfi_page_store(ctypes.Structure):
+    _fields_ = [("ref", c_void_p), ("k", c_void_p), ("v", c_void_p), ("n_layers", c_int32),
+                ("layer_stride", c_int64)]
+
+
 _L = POINTER(sfi_layout)
 _P = POINTER(sfi_params)
+_PL, _PS = POINTER(sfi_paged_layout), POINTER(sfi_page_store)
 # name -> (restype, argtypes); every function declared in include/sfi.h
 EXPORTS = {
     "sfi_last_error": (c_char_p, []),
@@ -86,6 +99,16 @@ EXPORTS = {
     "sfi_prefill_attn_workspace_size": (c_size_t, [POINTER(sfi_packed_layout)]),
     "sfi_prefill_attn": (c_int32, [POINTER(sfi_packed_layout), c_void_p, c_void_p, c_void_p,
                                    c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "sfi_paged_workspace_size": (c_size_t, [_PL]),
+    "sfi_paged_attn": (c_int32, [_PL, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                 c_size_t, c_void_p]),
+    "sfi_paged_append": (c_int32, [_PL, c_int32, c_void_p, c_void_p, c_int64, c_int64, c_void_p,
+                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "sfi_pages_extend": (c_int32, [_PL, _PS, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "sfi_pages_fork": (c_int32, [_PL, _PS, c_void_p, c_void_p, c_int32, c_void_p, c_size_t, c_void_p]),
+    "sfi_pages_free": (c_int32, [_PL, _PS, c_void_p, c_int32, c_void_p, c_size_t, c_void_p]),
+    "sfi_pages_compact": (c_int32, [_PL, _PS, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "sfi_pages_copy": (c_int32, [_PL, _PS, c_void_p, c_void_p, c_int32, c_void_p, c_size_t, c_void_p]),
     "sfi_ctx_create": (c_int32, [POINTER(sfi_ctx_desc), POINTER(c_void_p)]),
     "sfi_ctx_destroy": (c_int32, [c_void_p]),
     "sfi_decode_step": (c_int32, [c_void_p, c_int32, c_void_p, _L, c_void_p, c_void_p, c_void_p,
@@ -344,8 +367,179 @@ def sfi_prefill_attn(layout: PackedLayout, q, k, v, out, lse_out=None, ws=None, 
     c.q_stride, c.out_stride = (t.stride(0) if L.total_q > 1 else 0 for t in (q, out))
     c.k_stride, c.v_stride = (t.stride(0) if L.total_k > 1 else 0 for t in (k, v))
     _check("sfi_prefill_attn", lib.sfi_prefill_attn(
-        ctypes.byref(c), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse_out), _ptr(ws),
-        0 if ws is None else ws.numel(), _stream(stream)))
+        ctypes.byref(c), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse_out), *_ws(ws, L.device),
+        _stream(stream)))
+
+
+class PagedLayout:
+    """A KV cache in pages: sequence b's position i lies in row i % page_size of
+    page page_table[b, i // page_size] (page_table [B, max_pages], len [B], int32
+    device tensors, shared with the caller).  One layer's pool is
+    [n_pages, H_kv, page_size, d]; ``page_stride`` is the distance of its pages in
+    elements where they are not one after another (0: they are)."""
+
+    def __init__(self, n_q_heads: int, n_kv_heads: int, head_dim: int, dtype: torch.dtype,
+                 page_size: int, n_pages: int, page_table: torch.Tensor, len: torch.Tensor,
+                 page_stride: int = 0):
+        self.device = _device_of("page_table", page_table)
+        if page_table.dim() != 2:
+            raise ValueError("page_table: expected [batch, max_pages]")
+        self.B, self.max_pages = page_table.shape
+        _want("page_table", page_table, (self.B, self.max_pages), torch.int32, self.device)
+        _want("len", len, (self.B,), torch.int32, self.device)
+        self.n_q_heads, self.n_kv_heads, self.head_dim, self.dtype = n_q_heads, n_kv_heads, head_dim, dtype
+        self.page_size, self.n_pages, self.page_stride = page_size, n_pages, page_stride
+        self.page_table, self.len = page_table, len
+        self.c = sfi_paged_layout(self.B, n_q_heads, n_kv_heads, head_dim, dtype_code(dtype), page_size,
+                                  n_pages, self.max_pages, page_stride, page_table.data_ptr(),
+                                  len.data_ptr())
+
+    def _pool(self, name: str, t: torch.Tensor, layers: int = 0) -> torch.Tensor:
+        """Refuse a tensor that is not a pool ([layers,] n_pages, H_kv, page_size, d) of this layout."""
+        page = (self.n_pages, self.n_kv_heads, self.page_size, self.head_dim)
+        want = (layers,) + page if layers else page
+        if t.dtype != self.dtype or tuple(t.shape) != want or t.device != self.device:
+            raise ValueError(f"{name}: expected {self.dtype} {want} on {self.device}, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        d, p = self.head_dim, self.page_size
+        dense = self.n_kv_heads * p * d
+        strides = t.stride()[-4:]
+        if strides[1:] != (p * d, d, 1) and not t[(0,) * (t.dim() - 3)].is_contiguous():
+            raise ValueError(f"{name}: a page must be dense")
+        if self.n_pages > 1 and strides[0] != (self.page_stride or dense):
+            raise ValueError(f"{name}: pages lie {strides[0]} elements apart, the layout says "
+                             f"{self.page_stride or dense}")
+        return t
+
+
+class PageStore:
+    """The page counts ref [n_pages] (int32) and the pools k, v of the layers that the
+    bookkeeping moves: [n_pages, H_kv, page_size, d] or [layers, n_pages, H_kv, page_size, d]."""
+
+    def __init__(self, ref: torch.Tensor, k: torch.Tensor, v: torch.Tensor):
+        self.ref, self.k, self.v = ref, k, v
+        if k.shape != v.shape or k.stride() != v.stride() or k.dim() not in (4, 5):
+            raise ValueError("k and v must be pools of the same shape and strides")
+        self.layers = k.shape[0] if k.dim() == 5 else 0
+        self.c = sfi_page_store(_ptr(ref), _ptr(k), _ptr(v), max(1, self.layers),
+                                k.stride(0) if self.layers > 1 else 0)
+        self._for = None
+
+    def _check(self, layout: PagedLayout) -> "PageStore":
+        if self._for is not layout:
+            _want("ref", self.ref, (layout.n_pages,), torch.int32, layout.device)
+            layout._pool("k", self.k, self.layers)
+            layout._pool("v", self.v, self.layers)
+            self._for = layout
+        return self
+
+
+def paged_workspace(layout: PagedLayout) -> torch.Tensor:
+    """A zero-filled workspace for every paged call of this geometry."""
+    n = int(lib.sfi_paged_workspace_size(ctypes.byref(layout.c)))
+    if n == 0:
+        raise SfiError("sfi_paged_workspace_size", SFI_ERR_INVALID_ARG)
+    return torch.zeros(n, dtype=torch.uint8, device=layout.device)
+
+
+def _ws(ws, device: torch.device):
+    if ws is None:
+        return None, 0
+    if ws.device != device:
+        raise ValueError(f"the workspace lies on {ws.device}, the layout on {device}")
+    return _ptr(ws), ws.numel() * ws.element_size()
+
+
+def sfi_paged_attn(layout: PagedLayout, q, k, v, out, lse_out=None, ws=None, stream=None):
+    """q [B, H_q, d], k, v one layer's pools; out [B, H_q, d] and lse_out [B, H_q] fp32."""
+    L = layout
+    _here(L.device, stream)
+    rq = (L.B, L.n_q_heads, L.head_dim)
+    _want("q", q, rq, L.dtype, L.device)
+    L._pool("k", k)
+    L._pool("v", v)
+    _want("out", out, rq, torch.float32, L.device)
+    if lse_out is not None:
+        _want("lse_out", lse_out, rq[:2], torch.float32, L.device)
+    _check("sfi_paged_attn", lib.sfi_paged_attn(
+        ctypes.byref(L.c), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse_out), *_ws(ws, L.device),
+        _stream(stream)))
+
+
+def sfi_paged_append(layout: PagedLayout, k_new, v_new, k, v, cu_new=None, ws=None, stream=None):
+    """k_new, v_new [rows, H_kv, d] (heads dense, any row stride) into the pools k, v; cu_new
+    [B + 1] int32, or None: one row per sequence."""
+    L = layout
+    _here(L.device, stream)
+    new = (k_new.shape[0], L.n_kv_heads, L.head_dim)
+    _want("k_new", k_new, new, L.dtype, L.device, 2)
+    _want("v_new", v_new, new, L.dtype, L.device, 2)
+    L._pool("k", k)
+    L._pool("v", v)
+    if cu_new is not None:
+        _want("cu_new", cu_new, (L.B + 1,), torch.int32, L.device)
+    ks, vs = (t.stride(0) if new[0] > 1 else 0 for t in (k_new, v_new))
+    _check("sfi_paged_append", lib.sfi_paged_append(
+        ctypes.byref(L.c), new[0], _ptr(k_new), _ptr(v_new), ks, vs, _ptr(cu_new), _ptr(k), _ptr(v),
+        *_ws(ws, L.device), _stream(stream)))
+
+
+def _ids(v):
+    """A host list of sequences as a C array."""
+    v = [int(x) for x in v]
+    return (c_int32 * max(1, len(v)))(*v), len(v)
+
+
+def sfi_pages_extend(layout: PagedLayout, store: PageStore, n_new=None, ws=None, stream=None):
+    """Every sequence grows by n_new[b] positions (int32 [B] on the device; None: by one, if it
+    holds any), with new pages where it needs them."""
+    _here(layout.device, stream)
+    if n_new is not None:
+        _want("n_new", n_new, (layout.B,), torch.int32, layout.device)
+    _check("sfi_pages_extend", lib.sfi_pages_extend(
+        ctypes.byref(layout.c), ctypes.byref(store._check(layout).c), _ptr(n_new),
+        *_ws(ws, layout.device), _stream(stream)))
+
+
+def sfi_pages_fork(layout: PagedLayout, store: PageStore, src, dst, ws=None, stream=None):
+    """The empty sequences dst[i] become copies of src[i] (host lists)."""
+    _here(layout.device, stream)
+    (s, n), (d, m) = _ids(src), _ids(dst)
+    if n != m:
+        raise ValueError(f"{n} sources, but {m} destinations")
+    _check("sfi_pages_fork", lib.sfi_pages_fork(
+        ctypes.byref(layout.c), ctypes.byref(store._check(layout).c), s, d, n, *_ws(ws, layout.device),
+        _stream(stream)))
+
+
+def sfi_pages_free(layout: PagedLayout, store: PageStore, seqs, ws=None, stream=None):
+    """The listed sequences (host list) give up their pages."""
+    _here(layout.device, stream)
+    s, n = _ids(seqs)
+    _check("sfi_pages_free", lib.sfi_pages_free(
+        ctypes.byref(layout.c), ctypes.byref(store._check(layout).c), s, n, *_ws(ws, layout.device),
+        _stream(stream)))
+
+
+def sfi_pages_compact(layout: PagedLayout, store: PageStore, new_id=None, ws=None, stream=None):
+    """Used pages move to the lowest places; new_id (int32 [n_pages]) gets where each went."""
+    _here(layout.device, stream)
+    if new_id is not None:
+        _want("new_id", new_id, (layout.n_pages,), torch.int32, layout.device)
+    _check("sfi_pages_compact", lib.sfi_pages_compact(
+        ctypes.byref(layout.c), ctypes.byref(store._check(layout).c), _ptr(new_id),
+        *_ws(ws, layout.device), _stream(stream)))
+
+
+def sfi_pages_copy(layout: PagedLayout, store: PageStore, src, dst, ws=None, stream=None):
+    """Whole pages src[i] -> dst[i] in every layer (int32 device tensors)."""
+    _here(layout.device, stream)
+    n = src.numel()
+    _want("src", src, (n,), torch.int32, layout.device)
+    _want("dst", dst, (n,), torch.int32, layout.device)
+    _check("sfi_pages_copy", lib.sfi_pages_copy(
+        ctypes.byref(layout.c), ctypes.byref(store._check(layout).c), _ptr(src), _ptr(dst), n,
+        *_ws(ws, layout.device), _stream(stream)))
 
 
 def sfi_read_status(ws: torch.Tensor, stream=None) -> int:

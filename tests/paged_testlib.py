@@ -52,3 +52,28 @@ def close_lse(got, ref, size, d, what="lse"):
     fin = np.isfinite(ref)
     tol = score_error(size, d)[fin] + 2.0 ** -16 + 2.0 ** -21 * np.abs(ref[fin])
     close(got[fin], ref[fin], tol, what)
+
+
+def f32_tolerance(ref, scale, size, d, n, split):
+    """Elementwise bound for attention with an fp32 output over n positions.  Scores as above; exp2
+    off by 2^-22 twice (numerator and sum); sums in any order, off by one truncation of the sum
+    of magnitudes a step, at most n / 8 steps in a warp and 64 across warps and pieces (numerator
+    and sum); `split`: p as the sum of two bf16 terms, each off by eps / 2 of what is left."""
+    move = np.expm1(2 * score_error(size, d))[..., None] + 2.0 ** -21
+    move = move + 2 * (n / 8 + 64) * 2.0 ** -23
+    if split:
+        move = move + (torch.finfo(torch.bfloat16).eps / 2) ** 2
+    return move * (scale + np.abs(ref)) + 2.0 ** -126
+
+
+def pool_of(lens, page, extra, seed):
+    """A fragmented pool for these lengths: (n_pages, page table rows padded with -1)."""
+    need = [-(-n // page) for n in lens]
+    n_pages = sum(need) + extra
+    ids = np.random.RandomState(seed).permutation(n_pages)
+    width = max(need) + 1
+    table, at = np.full((len(lens), width), -1, np.int32), 0
+    for b, x in enumerate(need):
+        table[b, :x] = ids[at:at + x]
+        at += x
+    return n_pages, table
