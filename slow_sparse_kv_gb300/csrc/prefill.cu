@@ -44,7 +44,7 @@ struct Cfg {
 };
 
 struct Shared {
-  uint64_t q_full[2], s_full[2], p_ready[2], kv_full[6], kv_empty[6], drained;
+  uint64_t q_full[2], s_full[2], p_ready[2][2], kv_full[6], kv_empty[6], v_clean, drained;
   uint32_t tmem;
   volatile int abort;
   int b, tile;
@@ -82,6 +82,31 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+  return m;
+}
+
+// Two fp32 values in one 64-bit register, and the packed arithmetic on them.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ float lo(uint64_t p) { return __uint_as_float(uint32_t(p)); }
+__device__ __forceinline__ float hi(uint64_t p) { return __uint_as_float(uint32_t(p >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
 }
 
 // Keeps uses of registers that a tcgen05.ld fills behind its wait.
@@ -158,12 +183,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       for (int i = 0; i < 2; ++i) {
         mbar_init(smem_addr(&sh.q_full[i]), 1);
         mbar_init(smem_addr(&sh.s_full[i]), 1);
-        mbar_init(smem_addr(&sh.p_ready[i]), 128);
+        for (int h = 0; h < 2; ++h) mbar_init(smem_addr(&sh.p_ready[i][h]), 128);
       }
       for (int i = 0; i < C::STAGES; ++i) {
         mbar_init(smem_addr(&sh.kv_full[i]), 1);
         mbar_init(smem_addr(&sh.kv_empty[i]), 1);
       }
+      mbar_init(smem_addr(&sh.v_clean), 1);
       mbar_init(smem_addr(&sh.drained), 1);
       fence_mbar_init();
     }
@@ -203,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
               tma_load_3d(q_sm + i * C::TILE + h * (kRows * 128), &a.tmq, h * 64, g * a.G,
                           q0 + t0 + i * a.tok, bar);
           }
-          for (; issued < 2 * n && ok; ++issued) {
+          for (; issued < 2 * n; ++issued) {
             const int st = issued % C::STAGES, use = issued / C::STAGES;
             if (use > 0) ok = wait(smem_addr(&sh.kv_empty[st]), (use - 1) & 1, sh, a.status, a.wait_cycles);
             if (!ok) break;
@@ -214,94 +240,82 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
               tma_load_3d(kv_sm + st * C::TILE + h * (kKeys * 128), map, h * 64, g,
                           k0 + (issued >> 1) * kKeys, bar);
           }
-          // no copy may be in flight when the CTA exits (after a wait that
-          // gave up, some may never have been waited for)
-          for (int i = 0; i < 2; ++i)
-            if (n_it[i] > 0) mbar_wait(smem_addr(&sh.q_full[i]), 0);
-          for (int x = max(0, issued - C::STAGES); x < issued; ++x)
-            mbar_wait(smem_addr(&sh.kv_full[x % C::STAGES]), (x / C::STAGES) & 1);
         }
-        __syncwarp();
+        issued = __shfl_sync(kFull, issued, 0);
+        // no copy may be in flight when the CTA exits (after a wait that gave
+        // up, some may never have been waited for)
+        bool landed = true;
+        for (int i = 0; i < 2; ++i)
+          if (n_it[i] > 0) landed = mbar_wait(smem_addr(&sh.q_full[i]), 0) && landed;
+        for (int x = max(0, issued - C::STAGES); x < issued; ++x)
+          landed = mbar_wait(smem_addr(&sh.kv_full[x % C::STAGES]), (x / C::STAGES) & 1) && landed;
+        if (issued == 2 * n && n * kKeys > nk && __all_sync(kFull, landed)) {
+          // the rows of the last V block behind the sequence belong to nobody or
+          // to the next one: P is zero there, but 0 * NaN is not
+          const uint32_t v_sm = kv_sm + (2 * n - 1) % C::STAGES * C::TILE;
+          for (int y = (nk - (n - 1) * kKeys) * 8 + lane; y < kKeys * 8; y += 32)
+            for (int h = 0; h < C::HALVES; ++h)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v_sm + h * (kKeys * 128) + y * 16), "r"(0)
+                           : "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh.v_clean));
+        }
       } else if (warp == 9) {
-        // ---- products
-        constexpr uint32_t kIdS = tc5::idesc_bf16(kRows, kKeys, false);
-        constexpr uint32_t kIdO = tc5::idesc_bf16(kRows, D, true);
-        bool ok = true;
-        auto scores = [&](int i, int st) {  // S_i = Q_i K^T
-          if (lane == 0) {
-  #pragma unroll
+        // ---- products, all of them from one lane: a warp-wide vote or
+        // __syncwarp between MMAs costs more than their issue
+        if (tc5::elect()) {
+          constexpr uint32_t kIdS = tc5::idesc_bf16(kRows, kKeys, false);
+          constexpr uint32_t kIdO = tc5::idesc_bf16(kRows, D, true);
+          auto full = [&](int x) {  // block x of the ring (K_j: 2j, V_j: 2j + 1) has landed
+            return wait(smem_addr(&sh.kv_full[x % C::STAGES]), (x / C::STAGES) & 1, sh, a.status, a.wait_cycles);
+          };
+          auto release = [&](int x) { tc5::commit(smem_addr(&sh.kv_empty[x % C::STAGES])); };
+          auto scores = [&](int i, int x) {  // S_i = Q_i K^T
+            const uint64_t qd = tc5::desc_sw128(q_sm + i * C::TILE, 16, 1024);
+            const uint64_t kd = tc5::desc_sw128(kv_sm + (x % C::STAGES) * C::TILE, 16, 1024);
+#pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t at = (kk / 4) * (kRows * 128) + (kk % 4) * 32;
-              tc5::mma_ss(tmem + i * 128, tc5::desc_sw128(q_sm + i * C::TILE + at, 16, 1024),
-                          tc5::desc_sw128(kv_sm + st * C::TILE + at, 16, 1024), kIdS, kk > 0);
+              const uint32_t at = ((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4;
+              tc5::mma_ss(tmem + i * 128, qd + at, kd + at, kIdS, kk > 0);
             }
             tc5::commit(smem_addr(&sh.s_full[i]));
-          }
-          __syncwarp();
-        };
-        auto full = [&](int x) {  // block x of the ring (K_j: 2j, V_j: 2j + 1) has landed
-          return __all_sync(kFull, wait(smem_addr(&sh.kv_full[x % C::STAGES]), (x / C::STAGES) & 1, sh,
-                                        a.status, a.wait_cycles)) != 0;
-        };
-        auto release = [&](int x) {
-          if (lane == 0) tc5::commit(smem_addr(&sh.kv_empty[x % C::STAGES]));
-          __syncwarp();
-        };
-        if (n > 0) {
-          ok = full(0);
+          };
+          bool ok = n == 0 || full(0);
           for (int i = 0; i < 2 && ok; ++i) {
             if (n_it[i] == 0) continue;
-            ok = __all_sync(kFull, wait(smem_addr(&sh.q_full[i]), 0, sh, a.status, a.wait_cycles));
+            ok = wait(smem_addr(&sh.q_full[i]), 0, sh, a.status, a.wait_cycles);
             if (ok) scores(i, 0);
           }
-          if (ok) release(0);
-        }
-        for (int j = 0; j < n && ok; ++j) {
-          ok = full(2 * j + 1);
-          if (!ok) break;
-          const int sv = (2 * j + 1) % C::STAGES;
-          const uint32_t v_sm = kv_sm + sv * C::TILE;
-          const int rows = nk - j * kKeys;
-          if (rows < kKeys) {
-            // the rows behind the sequence belong to nobody or to the next one:
-            // P is zero there, but 0 * NaN is not
-            for (int x = rows * 8 + lane; x < kKeys * 8; x += 32)
-              for (int h = 0; h < C::HALVES; ++h)
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                 v_sm + h * (kKeys * 128) + x * 16),
-                             "r"(0)
-                             : "memory");
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-          }
-          bool more = false;
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (j >= n_it[i]) continue;
-            ok = __all_sync(kFull, wait(smem_addr(&sh.p_ready[i]), j & 1, sh, a.status, a.wait_cycles));
+          if (ok && n > 0) release(0);
+          for (int j = 0; j < n && ok; ++j) {
+            ok = (j + 1) * kKeys > nk ? wait(smem_addr(&sh.v_clean), 0, sh, a.status, a.wait_cycles) : full(2 * j + 1);
             if (!ok) break;
-            tc5::fence_after();
-            if (lane == 0) {
-  #pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk)
-                tc5::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + kk * 8,
-                            tc5::desc_sw128(v_sm + kk * 2048, kKeys * 128, 1024), kIdO, j > 0 || kk > 0);
-            }
-            __syncwarp();
-            if (j + 1 < n_it[i]) {
-              ok = full(2 * j + 2);
+            const uint64_t vd = tc5::desc_sw128(kv_sm + ((2 * j + 1) % C::STAGES) * C::TILE, kKeys * 128, 1024);
+            for (int i = 0; i < 2 && ok; ++i) {
+              if (j >= n_it[i]) continue;
+              for (int h = 0; h < 2; ++h) {  // O_i += P_i V, the halves of P as they come
+                ok = wait(smem_addr(&sh.p_ready[i][h]), j & 1, sh, a.status, a.wait_cycles);
+                if (!ok) break;
+                tc5::fence_after();
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 32; ++kk) {
+                  const int k16 = h * (kKeys / 32) + kk;
+                  tc5::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k16 * 8, vd + k16 * (2048 >> 4), kIdO, j > 0 || k16 > 0);
+                }
+              }
               if (!ok) break;
-              scores(i, (2 * j + 2) % C::STAGES);
-              more = true;
-            } else {
-              if (lane == 0) tc5::commit(smem_addr(&sh.s_full[i]));  // O_i is complete
-              __syncwarp();
+              if (j + 1 < n_it[i]) {
+                ok = full(2 * j + 2);
+                if (ok) scores(i, 2 * j + 2);
+              } else {
+                tc5::commit(smem_addr(&sh.s_full[i]));  // O_i is complete
+              }
             }
+            if (!ok) break;
+            release(2 * j + 1);
+            if (j + 1 < n) release(2 * j + 2);
           }
-          if (!ok) break;
-          release(2 * j + 1);
-          if (more) release(2 * j + 2);
-        }
-        if (lane == 0) {
           // the products in flight end before tensor memory is freed, whether or
           // not a softmax warp still waits for them
           tc5::commit(smem_addr(&sh.drained));
@@ -321,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const int open = max(0, min(off + t0 + i * a.tok + 1, nk));  // keys every valid row sees
       const uint32_t lanes = uint32_t(warp & 3) << 21;             // 32 * (warp % 4) in the lane field
       const uint32_t s_tm = tmem + i * 128 + lanes, o_tm = tmem + 256 + i * 128 + lanes;
-      const uint32_t s_bar = smem_addr(&sh.s_full[i]), p_bar = smem_addr(&sh.p_ready[i]);
+      const uint32_t s_bar = smem_addr(&sh.s_full[i]), p_bar = smem_addr(&sh.p_ready[i][0]);
       const float c = a.scale_log2;
       float m = -INFINITY, l = 0.f;
       bool ok = true;
@@ -341,8 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int x = 0; x < 128; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int x = 0; x < 128; x += 2)
+          mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+        const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
         if (j == 0) {
           m = top;
         } else {
@@ -364,21 +379,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             }
           }
         }
-        const float mc = m == -INFINITY ? 0.f : m * c;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float mc = m == -INFINITY ? 0.f : -m * c;
+        const uint64_t cc = pair(c, c), mm = pair(mc, mc);
+        uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int x = 0; x < 64; ++x) {
-          const float p0 = ex2(fmaf(__uint_as_float(s[2 * x]), c, -mc));
-          const float p1 = ex2(fmaf(__uint_as_float(s[2 * x + 1]), c, -mc));
-          sum[x & 3] += p0 + p1;
-          s[x] = pack_bf16x2(p0, p1);
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int x = 32 * h; x < 32 * h + 32; ++x) {
+            uint64_t y = pair(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
+            y = fma2(y, cc, mm);
+            const float p0 = ex2(lo(y)), p1 = ex2(hi(y));
+            sum[x & 3] = add2(sum[x & 3], pair(p0, p1));
+            s[x] = pack_bf16x2(p0, p1);
+          }
+          tc5::st32(s_tm + 32 * h, s + 32 * h);
+          tc5::wait_st();
+          tc5::fence_before();
+          mbar_arrive(p_bar + 8 * h);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tc5::st32(s_tm, s);
-        tc5::st32(s_tm + 32, s + 32);
-        tc5::wait_st();
-        tc5::fence_before();
-        mbar_arrive(p_bar);
+        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += lo(sum[0]) + hi(sum[0]);
       }
       if (ok && n_it[i] > 0)
         ok = __all_sync(kFull, wait(s_bar, n_it[i] & 1, sh, a.status, a.wait_cycles));

@@ -7,6 +7,17 @@
 namespace sfi {
 namespace tc5 {
 
+// True in one lane of a converged warp, the same one every time.  MMAs and commits are issued
+// under this predicate: the compiler then knows that one lane runs them and keeps their operands
+// in uniform registers (under lane == 0 each MMA took ~120 clocks to issue).
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Allocate `cols` tensor-memory columns (one warp, all lanes); the base
 // address is written to shared memory at `dst`.
 __device__ __forceinline__ void alloc(uint32_t dst, uint32_t cols) {

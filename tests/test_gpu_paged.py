@@ -217,8 +217,16 @@ def test_captured_calls_share_a_workspace(sfi):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_wait_limit(sfi, dtype):
-    """A one-clock limit: the waits give up, the status says so, nothing is left in flight."""
-    c = Cache(8, 2, 128, dtype, 16, [5000, 300])
+    """A one-clock limit: the waits give up, the status says so, nothing is left in flight.  The
+    cache is larger than L2, so that HBM is slower than the arithmetic and some wait is always
+    early (of a few thousand rows in L2, every tile has landed when its warp looks)."""
+    c = Cache(8, 2, 128, dtype, 16, [1])
+    c.lens = [8192] * 64
+    c.n_pages = 64 * 512
+    c.table = torch.randperm(c.n_pages, device="cuda").view(64, 512).int()
+    c.len = ints(c.lens)
+    c.q = normal((64, 8, 128), dtype, 1)
+    c.k, c.v = (torch.randn(c.n_pages, 2, 16, 128, device="cuda", dtype=dtype) for _ in range(2))
     lay = c.layout(sfi)
     good, _ = c.run(sfi)
     ws = sfi.paged_workspace(lay)
