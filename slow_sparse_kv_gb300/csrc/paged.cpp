@@ -14,6 +14,9 @@
 namespace sfi {
 namespace {
 
+// the status word, the counters of the tiles, and two numbers for each sequence
+constexpr size_t kPrefillWs = 512 + 8 * kMaxBatch;
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 bool misaligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
 
@@ -197,7 +200,7 @@ using namespace sfi;
 extern "C" {
 
 size_t sfi_prefill_attn_workspace_size(const sfi_packed_layout* L) {
-  return check_packed(L) == SFI_OK ? 256 : 0;  // the status word
+  return check_packed(L) == SFI_OK ? kPrefillWs : 0;
 }
 
 sfi_status sfi_prefill_attn(const sfi_packed_layout* L, const void* q, const void* k, const void* v, void* out,
@@ -210,7 +213,7 @@ sfi_status sfi_prefill_attn(const sfi_packed_layout* L, const void* q, const voi
   if ((s = row_stride("k_stride", L->k_stride, int64_t(L->n_kv_heads) * D, 8, &ks)) != SFI_OK) return s;
   if ((s = row_stride("v_stride", L->v_stride, int64_t(L->n_kv_heads) * D, 8, &vs)) != SFI_OK) return s;
   if ((s = row_stride("out_stride", L->out_stride, int64_t(L->n_q_heads) * D, 8, &os)) != SFI_OK) return s;
-  if ((s = check_workspace(ws, ws_bytes, 256)) != SFI_OK) return s;
+  if ((s = check_workspace(ws, ws_bytes, kPrefillWs)) != SFI_OK) return s;
   if (L->total_q == 0) return SFI_OK;
   if (!q || !out || (L->total_k > 0 && (!k || !v)))
     return fail(SFI_ERR_INVALID_ARG, "q, k, v and out must be set");
@@ -232,6 +235,9 @@ sfi_status sfi_prefill_attn(const sfi_packed_layout* L, const void* q, const voi
   a.tok = 128 / G;
   a.scale_log2 = float(1.4426950408889634 / std::sqrt(double(D)));
   a.status = static_cast<uint32_t*>(ws);
+  a.next = a.status + 64;
+  a.span = reinterpret_cast<int32_t*>(a.status + 128);
+  a.lvl = a.span + kMaxBatch;
   a.wait_cycles = wait_limit_cycles();
   bool ok = encode_heads(&a.tmq, q, D, L->n_q_heads, L->total_q, qs, G, a.tok);
   if (L->total_k > 0)  // without keys the kernel loads neither

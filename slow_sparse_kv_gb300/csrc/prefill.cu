@@ -1,9 +1,12 @@
 // Causal attention over packed prompts (bf16, grouped heads) on the
 // fifth-generation tensor cores.
 //
-// One CTA takes 2 x 128 query rows of one (sequence, KV head); a row is one
-// (token, query head of the group), so a tile holds 128 / G tokens times the G
-// heads that share the KV head, and K and V are read once for all of them.
+// One CTA to an SM takes tile after tile: 2 x 128 query rows of one (sequence,
+// KV head); a row is one (token, query head of the group), so a tile holds
+// 128 / G tokens times the G heads that share the KV head, and K and V are read
+// once for all of them.  The tiles come from a shared counter, the long ones
+// first; loads run ahead into the next tile, so that its first products start
+// while the last one's output is written.
 // For each block of 128 keys: S = Q K^T (tcgen05.mma from shared memory into
 // tensor memory), softmax statistics with one thread per row, P in bf16 over
 // S's columns in tensor memory, O += P V (P from tensor memory).  The two
@@ -26,13 +29,17 @@
 namespace sfi {
 namespace {
 
-constexpr int kThreads = 384;  // 2 softmax warpgroups; a load warp, an MMA warp and two idle ones
+constexpr int kThreads = 384;  // 2 softmax warpgroups; a load, an MMA, a scheduling and a cleaning warp
 // Registers a thread: launched with 168 (64512 in all); the softmax threads
 // hold a whole row of scores, the third warpgroup gives up what they take
-// (128 * (2 * 208 + 88) = 64512).
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+// (128 * (2 * 216 + 72) = 64512).
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kRows = 128;     // query rows per tile
 constexpr int kKeys = 128;     // keys per block
+// P of a block is handed over in parts, the first 64 keys, then twice 32: the
+// products start early and the scores behind them wait for a short last part.
+constexpr int kParts = 3;
+__host__ __device__ constexpr int part_end(int part) { return part == 0 ? 64 : part == 1 ? 96 : kKeys; }
 constexpr float kGrow = 8.0f;  // growth of the maximum (log2) that moves m
 
 template <int D>
@@ -40,16 +47,28 @@ struct Cfg {
   static constexpr int HALVES = D / 64;
   static constexpr uint32_t TILE = kRows * 128 * HALVES;  // bytes of a 128-row tile
   static constexpr int STAGES = D == 128 ? 4 : 6;         // K and V blocks in flight
-  static constexpr uint32_t SMEM = 1024 + (2 + STAGES) * TILE;
+  static constexpr uint32_t OUT = 8 * 32 * 128;           // 32 rows of 64 outputs for each softmax warp
+  static constexpr uint32_t SMEM = 1024 + (2 + STAGES) * TILE + OUT;
 };
 
+// A pair of 128-row tiles: 2 x 128 / G tokens of one (sequence, KV head).
+struct Tile {
+  int rows;    // tokens it has (0: no tile, the end)
+  int g;       // KV head
+  int q0;      // first query row
+  int k0, nk;  // the sequence's first key row and its number of keys
+  int seen;    // keys that the first token sees (may be negative: none, and none for some after it)
+  int n[2];    // key blocks of each half
+};
+
+constexpr int kTileReaders = 11;  // loads, MMAs, the cleaning warp, 8 softmax warps
+
 struct Shared {
-  uint64_t q_full[2], s_full[2], p_ready[2][2], kv_full[6], kv_empty[6], v_clean, drained;
+  uint64_t q_full[2], q_empty[2], s_full[2], o_full[2], p_ready[2][kParts], tile_full[2], tile_empty[2];
+  uint64_t kv_full[6], kv_empty[6], v_clean, drained;
+  Tile tile[2];
   uint32_t tmem;
   volatile int abort;
-  int b, tile;
-  int span[kMaxBatch];  // CTAs (tile pairs) of each sequence
-  int lvl[kMaxBatch];   // its first one's level
 };
 
 // Bounded wait; false (and the CTA's abort flag and the status bit set) after
@@ -109,6 +128,28 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
   return d;
 }
 
+// Part H of a block's probabilities: p = 2^(c s - c m) summed in fp32 (four
+// pairs of sums) and rounded to bf16 pairs in s's first half.
+template <int H>
+__device__ __forceinline__ void exp_part(uint32_t (&s)[kKeys], uint64_t cc, uint64_t mm, uint64_t (&sum)[4]) {
+#pragma unroll
+  for (int x = H ? part_end(H - 1) / 2 : 0; x < part_end(H) / 2; ++x) {
+    const uint64_t y = fma2(pair(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), cc, mm);
+    const float p0 = ex2(lo(y)), p1 = ex2(hi(y));
+    sum[x & 3] = add2(sum[x & 3], pair(p0, p1));
+    s[x] = pack_bf16x2(p0, p1);
+  }
+}
+
+// Store a part of P and tell the MMA lane.
+template <typename Store>
+__device__ __forceinline__ void hand_over(uint32_t bar, Store store) {
+  store();
+  tc5::wait_st();
+  tc5::fence_before();
+  mbar_arrive(bar);
+}
+
 // Keeps uses of registers that a tcgen05.ld fills behind its wait.
 template <int N>
 __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
@@ -116,13 +157,76 @@ __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// Tiles of a level tau or above, over all sequences (one warp): sequence b has
-// its tiles at levels lvl[b] .. lvl[b] + span[b] - 1.
-__device__ __forceinline__ int tiles_from(const Shared& sh, int B, int tau) {
-  int n = 0;
-  for (int b = threadIdx.x & 31; b < B; b += 32)
-    n += min(max(sh.lvl[b] + sh.span[b] - tau, 0), sh.span[b]);
-  return __reduce_add_sync(kFull, n);
+// Which tile has which rank (one warp).  Levels stand for the keys that a tile
+// sees, in units of its tokens: sequence b has its tiles at levels lvl[b] ..
+// lvl[b] + span[b] - 1.  Ranks go from the highest level down, so that the long
+// tiles start first; within a level by sequence, and the KV heads of a tile are
+// neighbours.  A CTA asks for growing ranks, so the walk goes on from where it
+// stood.
+struct Ranks {
+  const int* span;
+  const int* lvl;
+  int B;
+  int level, before, here;  // the level it stands at, tiles above it and on it
+
+  // tiles on levels tau and above
+  __device__ __forceinline__ int from(int tau) const {
+    int n = 0;
+    for (int b = threadIdx.x & 31; b < B; b += 32) n += min(max(lvl[b] + span[b] - tau, 0), span[b]);
+    return __reduce_add_sync(kFull, n);
+  }
+  __device__ __forceinline__ void top() {
+    int t = 0;
+    for (int b = threadIdx.x & 31; b < B; b += 32) t = max(t, span[b] > 0 ? lvl[b] + span[b] : 0);
+    level = __reduce_max_sync(kFull, t);
+    before = here = 0;
+  }
+  // sequence and tile of a rank below from(0)
+  __device__ __forceinline__ void find(int rank, int* seq, int* tile) {
+    const int lane = threadIdx.x & 31;
+    if (rank >= before + here) {
+      // the level with from(level + 1) <= rank < from(level), below this one
+      int lo = 0, hi = level;
+      if (level > 0 && from(level - 1) > rank) lo = level - 1;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (from(mid) > rank) lo = mid;
+        else hi = mid;
+      }
+      level = lo;
+      before = from(lo + 1);
+      here = from(lo) - before;
+    }
+    int left = rank - before;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      const int b = b0 + lane;
+      const uint32_t in = __ballot_sync(kFull, b < B && lvl[b] <= level && level < lvl[b] + span[b]);
+      if (left < __popc(in)) {
+        *seq = b0 + __fns(in, 0, left + 1);
+        *tile = level - lvl[*seq];
+        return;
+      }
+      left -= __popc(in);
+    }
+  }
+};
+
+__device__ __forceinline__ Tile make_tile(const PrefillArgs& a, int g, int seq, int tile) {
+  Tile t;
+  const int span = 2 * a.tok, first = tile * span;
+  const int q0 = a.cu_q[seq], nq = a.cu_q[seq + 1] - q0;
+  t.g = g;
+  t.k0 = a.cu_k[seq];
+  t.nk = a.cu_k[seq + 1] - t.k0;
+  t.q0 = q0 + first;
+  t.rows = min(span, nq - first);
+  t.seen = t.nk - nq + first + 1;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int tokens = min(t.rows, (i + 1) * a.tok);  // the half's last one sees seen + tokens - 1
+    t.n[i] = t.rows > i * a.tok ? (max(0, min(t.seen + tokens - 1, t.nk)) + kKeys - 1) / kKeys : 0;
+  }
+  return t;
 }
 
 template <int D>
@@ -132,62 +236,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   __shared__ Shared sh;
   const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = blockIdx.x % a.H_kv;
-  const int rank = blockIdx.x / a.H_kv;
-
-  // Which tile: levels stand for the keys that a tile sees (in units of its
-  // tokens); the CTAs take them from the highest down, so that the long ones
-  // start first.
   const int span_tok = 2 * a.tok;
+
   for (int b = tid; b < a.B; b += kThreads) {
     const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
     const bool ok = q0 >= 0 && q0 <= q1 && q1 <= a.total_q && k0 >= 0 && k0 <= k1 && k1 <= a.total_k;
     if (!ok && blockIdx.x == 0) set_status(a.status, SFI_DEV_LEN_OVER_CAP);
-    sh.span[b] = ok ? (q1 - q0 + span_tok - 1) / span_tok : 0;
-    sh.lvl[b] = ok ? max(0, (k1 - k0) - (q1 - q0)) / span_tok : 0;
+    // (every CTA writes the same values and reads its own)
+    a.span[b] = ok ? (q1 - q0 + span_tok - 1) / span_tok : 0;
+    a.lvl[b] = ok ? max(0, (k1 - k0) - (q1 - q0)) / span_tok : 0;
   }
-  if (tid == 0) {
-    sh.abort = 0;
-    sh.b = -1;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int top = 0;
-    for (int b = lane; b < a.B; b += 32) top = max(top, sh.span[b] > 0 ? sh.lvl[b] + sh.span[b] : 0);
-    top = __reduce_max_sync(kFull, top);
-    if (rank < tiles_from(sh, a.B, 0)) {
-      // the level with tiles_from(tau + 1) <= rank < tiles_from(tau)
-      int lo = 0, hi = top;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (tiles_from(sh, a.B, mid) > rank) lo = mid;
-        else hi = mid;
-      }
-      int left = rank - tiles_from(sh, a.B, lo + 1);
-      for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int b = b0 + lane;
-        const bool in = b < a.B && sh.lvl[b] <= lo && lo < sh.lvl[b] + sh.span[b];
-        const uint32_t m = __ballot_sync(kFull, in);
-        if (left < __popc(m)) {
-          if (in && __popc(m & ((1u << lane) - 1)) == left) {
-            sh.b = b;
-            sh.tile = lo - sh.lvl[b];
-          }
-          break;
-        }
-        left -= __popc(m);
-      }
-    }
-  } else if (warp == 9) {
+  if (warp == 9) {
     if (lane == 0) {
+      sh.abort = 0;
       for (int i = 0; i < 2; ++i) {
         mbar_init(smem_addr(&sh.q_full[i]), 1);
+        mbar_init(smem_addr(&sh.q_empty[i]), 1);
         mbar_init(smem_addr(&sh.s_full[i]), 1);
-        for (int h = 0; h < 2; ++h) mbar_init(smem_addr(&sh.p_ready[i][h]), 128);
+        mbar_init(smem_addr(&sh.o_full[i]), 1);
+        for (int h = 0; h < kParts; ++h) mbar_init(smem_addr(&sh.p_ready[i][h]), 128);
+        mbar_init(smem_addr(&sh.tile_full[i]), 1);
+        mbar_init(smem_addr(&sh.tile_empty[i]), kTileReaders);
       }
       for (int i = 0; i < C::STAGES; ++i) {
         mbar_init(smem_addr(&sh.kv_full[i]), 1);
-        mbar_init(smem_addr(&sh.kv_empty[i]), 1);
+        mbar_init(smem_addr(&sh.kv_empty[i]), 2);  // its last product, and the cleaning warp
       }
       mbar_init(smem_addr(&sh.v_clean), 1);
       mbar_init(smem_addr(&sh.drained), 1);
@@ -200,147 +273,218 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   __syncthreads();
   tc5::fence_after();
   const uint32_t tmem = sh.tmem;
+  const uint32_t q_sm = base, kv_sm = base + 2 * C::TILE;
+  auto stage = [&](int x) { return x % C::STAGES; };
+  auto wait_for = [&](uint64_t* bar, int use) {
+    return wait(smem_addr(bar), use & 1, sh, a.status, a.wait_cycles);
+  };
+  // The k-th tile of this CTA, once it is there; one without rows ends the walk.
+  auto take = [&](int k, Tile& t) {
+    if (!wait_for(&sh.tile_full[k & 1], k >> 1)) return false;
+    t = sh.tile[k & 1];
+    return true;
+  };
+  auto taken = [&](int k) { mbar_arrive(smem_addr(&sh.tile_empty[k & 1])); };
 
-  if (sh.b >= 0) {
-    const int b = sh.b;
-    const int q0 = a.cu_q[b], nq = a.cu_q[b + 1] - q0;
-    const int k0 = a.cu_k[b], nk = a.cu_k[b + 1] - k0;
-    const int off = nk - nq;
-    const int t0 = sh.tile * span_tok;
-    int n_it[2];  // key blocks of each tile
-    for (int i = 0; i < 2; ++i) {
-      const int first = t0 + i * a.tok, last = min(first + a.tok, nq);
-      n_it[i] = first < nq ? (max(0, min(off + last, nk)) + kKeys - 1) / kKeys : 0;
-    }
-    const int n = max(n_it[0], n_it[1]);
-    const uint32_t q_sm = base, kv_sm = base + 2 * C::TILE;
-    if (warp >= 8) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-      if (warp == 8) {
-        // ---- loads: Q once, then K_0, V_0, K_1, V_1, ... through the ring
-        int issued = 0;
-        bool ok = true;
-        if (lane == 0) {
-          for (int i = 0; i < 2; ++i) {
-            if (n_it[i] == 0) continue;
-            const uint32_t bar = smem_addr(&sh.q_full[i]);
-            mbar_arrive_expect_tx(bar, uint32_t(a.tok * a.G) * 128 * C::HALVES);
-            for (int h = 0; h < C::HALVES; ++h)
-              tma_load_3d(q_sm + i * C::TILE + h * (kRows * 128), &a.tmq, h * 64, g * a.G,
-                          q0 + t0 + i * a.tok, bar);
-          }
-          for (; issued < 2 * n; ++issued) {
-            const int st = issued % C::STAGES, use = issued / C::STAGES;
-            if (use > 0) ok = wait(smem_addr(&sh.kv_empty[st]), (use - 1) & 1, sh, a.status, a.wait_cycles);
-            if (!ok) break;
-            const uint32_t bar = smem_addr(&sh.kv_full[st]);
-            mbar_arrive_expect_tx(bar, C::TILE);
-            const void* map = (issued & 1) ? &a.tmv : &a.tmk;
-            for (int h = 0; h < C::HALVES; ++h)
-              tma_load_3d(kv_sm + st * C::TILE + h * (kKeys * 128), map, h * 64, g,
-                          k0 + (issued >> 1) * kKeys, bar);
-          }
-        }
-        issued = __shfl_sync(kFull, issued, 0);
-        // no copy may be in flight when the CTA exits (after a wait that gave
-        // up, some may never have been waited for)
-        bool landed = true;
-        for (int i = 0; i < 2; ++i)
-          if (n_it[i] > 0) landed = mbar_wait(smem_addr(&sh.q_full[i]), 0) && landed;
-        for (int x = max(0, issued - C::STAGES); x < issued; ++x)
-          landed = mbar_wait(smem_addr(&sh.kv_full[x % C::STAGES]), (x / C::STAGES) & 1) && landed;
-        if (issued == 2 * n && n * kKeys > nk && __all_sync(kFull, landed)) {
-          // the rows of the last V block behind the sequence belong to nobody or
-          // to the next one: P is zero there, but 0 * NaN is not
-          const uint32_t v_sm = kv_sm + (2 * n - 1) % C::STAGES * C::TILE;
-          for (int y = (nk - (n - 1) * kKeys) * 8 + lane; y < kKeys * 8; y += 32)
-            for (int h = 0; h < C::HALVES; ++h)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v_sm + h * (kKeys * 128) + y * 16), "r"(0)
-                           : "memory");
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&sh.v_clean));
-        }
-      } else if (warp == 9) {
-        // ---- products, all of them from one lane: a warp-wide vote or
-        // __syncwarp between MMAs costs more than their issue
-        if (tc5::elect()) {
-          constexpr uint32_t kIdS = tc5::idesc_bf16(kRows, kKeys, false);
-          constexpr uint32_t kIdO = tc5::idesc_bf16(kRows, D, true);
-          auto full = [&](int x) {  // block x of the ring (K_j: 2j, V_j: 2j + 1) has landed
-            return wait(smem_addr(&sh.kv_full[x % C::STAGES]), (x / C::STAGES) & 1, sh, a.status, a.wait_cycles);
-          };
-          auto release = [&](int x) { tc5::commit(smem_addr(&sh.kv_empty[x % C::STAGES])); };
-          auto scores = [&](int i, int x) {  // S_i = Q_i K^T
-            const uint64_t qd = tc5::desc_sw128(q_sm + i * C::TILE, 16, 1024);
-            const uint64_t kd = tc5::desc_sw128(kv_sm + (x % C::STAGES) * C::TILE, 16, 1024);
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8 && lane == 0) {
+      // ---- loads: each tile's Q, then K_0, V_0, K_1, V_1, ... through the ring
+      int x = 0, q_uses[2] = {0, 0};
+      bool ok = true;
+      Tile t;
+      for (int k = 0; ok && take(k, t); ++k) {
+        taken(k);
+        if (t.rows == 0) break;
+        const int n = max(t.n[0], t.n[1]);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t at = ((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4;
-              tc5::mma_ss(tmem + i * 128, qd + at, kd + at, kIdS, kk > 0);
-            }
-            tc5::commit(smem_addr(&sh.s_full[i]));
-          };
-          bool ok = n == 0 || full(0);
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (n_it[i] == 0) continue;
-            ok = wait(smem_addr(&sh.q_full[i]), 0, sh, a.status, a.wait_cycles);
-            if (ok) scores(i, 0);
+        for (int i = 0; i < 2; ++i) {
+          if (!ok || t.n[i] == 0) continue;
+          if (q_uses[i] > 0) ok = wait_for(&sh.q_empty[i], q_uses[i] - 1);
+          if (!ok) continue;
+          const uint32_t bar = smem_addr(&sh.q_full[i]);
+          mbar_arrive_expect_tx(bar, uint32_t(a.tok * a.G) * 128 * C::HALVES);
+          for (int h = 0; h < C::HALVES; ++h)
+            tma_load_3d(q_sm + i * C::TILE + h * (kRows * 128), &a.tmq, h * 64, t.g * a.G, t.q0 + i * a.tok, bar);
+          ++q_uses[i];
+        }
+        for (int y = 0; y < 2 * n && ok; ++y) {
+          if (x >= C::STAGES) ok = wait_for(&sh.kv_empty[stage(x)], x / C::STAGES - 1);
+          if (!ok) break;
+          const uint32_t bar = smem_addr(&sh.kv_full[stage(x)]);
+          mbar_arrive_expect_tx(bar, C::TILE);
+          const void* map = (y & 1) ? &a.tmv : &a.tmk;
+          for (int h = 0; h < C::HALVES; ++h)
+            tma_load_3d(kv_sm + stage(x) * C::TILE + h * (kKeys * 128), map, h * 64, t.g, t.k0 + (y >> 1) * kKeys, bar);
+          ++x;
+        }
+      }
+      // no copy may be in flight when the CTA exits (after a wait that gave
+      // up, some may never have been waited for)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (q_uses[i] > 0) mbar_wait(smem_addr(&sh.q_full[i]), (q_uses[i] - 1) & 1);
+      for (int y = max(0, x - C::STAGES); y < x; ++y)
+        mbar_wait(smem_addr(&sh.kv_full[stage(y)]), (y / C::STAGES) & 1);
+    } else if (warp == 9) {
+      // ---- products, all of them from one lane: a warp-wide vote or
+      // __syncwarp between MMAs costs more than their issue
+      if (tc5::elect()) {
+        constexpr uint32_t kIdS = tc5::idesc_bf16(kRows, kKeys, false);
+        constexpr uint32_t kIdO = tc5::idesc_bf16(kRows, D, true);
+        int x = 0, tiles[2] = {0, 0}, blocks[2] = {0, 0}, cleaned = 0;
+        auto full = [&](int y) { return wait_for(&sh.kv_full[stage(y)], y / C::STAGES); };
+        auto scores = [&](int i, int y, bool last) {  // S_i = Q_i K^T
+          const uint64_t qd = tc5::desc_sw128(q_sm + i * C::TILE, 16, 1024);
+          const uint64_t kd = tc5::desc_sw128(kv_sm + stage(y) * C::TILE, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t at = ((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4;
+            tc5::mma_ss(tmem + i * 128, qd + at, kd + at, kIdS, kk > 0);
           }
-          if (ok && n > 0) release(0);
-          for (int j = 0; j < n && ok; ++j) {
-            ok = (j + 1) * kKeys > nk ? wait(smem_addr(&sh.v_clean), 0, sh, a.status, a.wait_cycles) : full(2 * j + 1);
-            if (!ok) break;
-            const uint64_t vd = tc5::desc_sw128(kv_sm + ((2 * j + 1) % C::STAGES) * C::TILE, kKeys * 128, 1024);
-            for (int i = 0; i < 2 && ok; ++i) {
-              if (j >= n_it[i]) continue;
-              for (int h = 0; h < 2; ++h) {  // O_i += P_i V, the halves of P as they come
-                ok = wait(smem_addr(&sh.p_ready[i][h]), j & 1, sh, a.status, a.wait_cycles);
+          tc5::commit(smem_addr(&sh.s_full[i]));
+          if (last) tc5::commit(smem_addr(&sh.q_empty[i]));
+        };
+        bool ok = true;
+        Tile t;
+        for (int k = 0; ok && take(k, t); ++k) {
+          taken(k);
+          if (t.rows == 0) break;
+          const int n = max(t.n[0], t.n[1]);
+          if (n == 0) continue;
+          ok = full(x);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!ok || t.n[i] == 0) continue;
+            ok = wait_for(&sh.q_full[i], tiles[i]++);
+            // (S_i's columns are free: the last tile's products with P_i, which
+            // lay there, were issued before)
+            if (!ok) continue;
+            scores(i, x, t.n[i] == 1);
+            if (i == 1 || t.n[1] == 0) tc5::commit(smem_addr(&sh.kv_empty[stage(x)]));
+          }
+          auto v_landed = [&](int j, int y) {
+            return (j + 1) * kKeys > t.nk ? wait_for(&sh.v_clean, cleaned++) : full(y);
+          };
+          for (int j = 0; j < n && ok; ++j, x += 2) {
+            ok = v_landed(j, x + 1);
+            const uint64_t vd = tc5::desc_sw128(kv_sm + stage(x + 1) * C::TILE, kKeys * 128, 1024);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (!ok || j >= t.n[i]) continue;
+              const bool last = i == 1 || j >= t.n[1];  // of the halves that use V_j
+#pragma unroll
+              for (int h = 0; h < kParts; ++h) {  // O_i += P_i V, the parts of P as they come
+                ok = ok && wait_for(&sh.p_ready[i][h], blocks[i]);
                 if (!ok) break;
                 tc5::fence_after();
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 32; ++kk) {
-                  const int k16 = h * (kKeys / 32) + kk;
-                  tc5::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k16 * 8, vd + k16 * (2048 >> 4), kIdO, j > 0 || k16 > 0);
-                }
+                for (int k16 = h ? part_end(h - 1) / 16 : 0; k16 < part_end(h) / 16; ++k16)
+                  tc5::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k16 * 8, vd + k16 * (2048 >> 4), kIdO,
+                              j > 0 || k16 > 0);
               }
-              if (!ok) break;
-              if (j + 1 < n_it[i]) {
-                ok = full(2 * j + 2);
-                if (ok) scores(i, 2 * j + 2);
+              ++blocks[i];
+              if (!ok) continue;
+              if (last) tc5::commit(smem_addr(&sh.kv_empty[stage(x + 1)]));
+              if (j + 1 < t.n[i]) {
+                ok = full(x + 2);
+                if (!ok) continue;
+                scores(i, x + 2, j + 2 == t.n[i]);
+                if (i == 1 || j + 1 >= t.n[1]) tc5::commit(smem_addr(&sh.kv_empty[stage(x + 2)]));
               } else {
-                tc5::commit(smem_addr(&sh.s_full[i]));  // O_i is complete
+                tc5::commit(smem_addr(&sh.o_full[i]));
               }
             }
-            if (!ok) break;
-            release(2 * j + 1);
-            if (j + 1 < n) release(2 * j + 2);
           }
-          // the products in flight end before tensor memory is freed, whether or
-          // not a softmax warp still waits for them
-          tc5::commit(smem_addr(&sh.drained));
-          mbar_wait(smem_addr(&sh.drained), 0);
+        }
+        // the products in flight end before tensor memory is freed, whether or
+        // not a softmax warp still waits for them
+        tc5::commit(smem_addr(&sh.drained));
+        mbar_wait(smem_addr(&sh.drained), 0);
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      // ---- which tiles: the CTA's own index first, then by a shared counter
+      int rank = blockIdx.x;
+      Ranks ranks{a.span, a.lvl, a.B};
+      ranks.top();
+      const long long total = (long long)ranks.from(0) * a.H_kv;
+      for (int k = 0;; ++k) {
+        Tile t;
+        t.rows = 0;
+        if (rank < total) {
+          int seq = 0, tile = 0;
+          ranks.find(rank / a.H_kv, &seq, &tile);
+          t = make_tile(a, rank % a.H_kv, seq, tile);
+        }
+        if (k > 1 && !__all_sync(kFull, wait_for(&sh.tile_empty[k & 1], (k >> 1) - 1))) break;
+        if (lane == 0) {
+          sh.tile[k & 1] = t;
+          mbar_arrive(smem_addr(&sh.tile_full[k & 1]));  // (release: the tile is visible to who waits)
         }
         __syncwarp();
+        if (t.rows == 0) break;
+        if (lane == 0) rank = gridDim.x + int(atomicAdd(a.next, 1u));
+        rank = __shfl_sync(kFull, rank, 0);
       }
-    } else {
-      // ---- softmax and output of tile i: one thread per row
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-      const int i = warp >> 2;
-      const int r = tid & 127;
-      const int tt = r / a.G;
-      const int t = t0 + i * a.tok + tt;
-      const bool valid = tt < a.tok && t < nq;
-      const int limit = valid ? max(0, min(off + t + 1, nk)) : 0;  // keys this row sees
-      const int open = max(0, min(off + t0 + i * a.tok + 1, nk));  // keys every valid row sees
-      const uint32_t lanes = uint32_t(warp & 3) << 21;             // 32 * (warp % 4) in the lane field
-      const uint32_t s_tm = tmem + i * 128 + lanes, o_tm = tmem + 256 + i * 128 + lanes;
-      const uint32_t s_bar = smem_addr(&sh.s_full[i]), p_bar = smem_addr(&sh.p_ready[i][0]);
-      const float c = a.scale_log2;
-      float m = -INFINITY, l = 0.f;
+      // the last CTA to run out leaves the counters at zero
+      if (lane == 0 && atomicAdd(a.next + 1, 1u) == gridDim.x - 1) {
+        a.next[0] = 0;
+        a.next[1] = 0;
+      }
+    } else if (warp == 11) {
+      // ---- the rows of a sequence's last V block that lie behind it belong to
+      // nobody or to the next one: P is zero there, but 0 * NaN is not
+      int x = 0;
       bool ok = true;
-      for (int j = 0; j < n_it[i]; ++j) {
-        ok = __all_sync(kFull, wait(s_bar, j & 1, sh, a.status, a.wait_cycles));
+      Tile t;
+      for (int k = 0; ok && __all_sync(kFull, take(k, t)); ++k) {
+        __syncwarp();
+        if (lane == 0) taken(k);
+        if (t.rows == 0) break;
+        const int n = max(t.n[0], t.n[1]);
+        for (int y = 0; y < 2 * n && ok; ++y, ++x) {
+          ok = __all_sync(kFull, wait_for(&sh.kv_full[stage(x)], x / C::STAGES));
+          if (!ok) break;
+          if (y == 2 * n - 1 && n * kKeys > t.nk) {
+            const uint32_t v_sm = kv_sm + stage(x) * C::TILE;
+            for (int z = (t.nk - (n - 1) * kKeys) * 8 + lane; z < kKeys * 8; z += 32)
+              for (int h = 0; h < C::HALVES; ++h)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v_sm + h * (kKeys * 128) + z * 16), "r"(0)
+                             : "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.v_clean));
+          }
+          if (lane == 0) mbar_arrive(smem_addr(&sh.kv_empty[stage(x)]));
+        }
+      }
+    }
+  } else {
+    // ---- softmax and output of tile half i: one thread per row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int i = warp >> 2;
+    const int r = tid & 127;
+    const int tt = r / a.G;                           // token of the tile
+    const uint32_t lanes = uint32_t(warp & 3) << 21;  // 32 * (warp % 4) in the lane field
+    const uint32_t s_tm = tmem + i * 128 + lanes, o_tm = tmem + 256 + i * 128 + lanes;
+    const uint32_t p_bar = smem_addr(&sh.p_ready[i][0]);
+    const float c = a.scale_log2;
+    const uint32_t out_sm = base + (2 + C::STAGES) * C::TILE + warp * (32 * 128);
+    int blocks = 0, tiles = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!__all_sync(kFull, wait_for(&sh.tile_full[k & 1], k >> 1))) break;
+      const Tile& t = sh.tile[k & 1];  // (given back behind the output: registers are short here)
+      if (t.rows == 0) break;
+      const int n_it = t.n[i];
+      const int row = i * a.tok + tt;  // of the tile pair's tokens
+      const bool valid = tt < a.tok && row < t.rows;
+      const int limit = valid ? max(0, min(t.seen + row, t.nk)) : 0;  // keys this row sees
+      const int open = max(0, min(t.seen + i * a.tok, t.nk));         // keys every valid row sees
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n_it; ++j) {
+        ok = __all_sync(kFull, wait_for(&sh.s_full[i], blocks++));
         if (!ok) break;
         tc5::fence_after();
         uint32_t s[128];
@@ -364,79 +508,85 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           const bool grow = (top - m) * c > kGrow;
           if (__any_sync(kFull, grow)) {
             // PV of block j - 1 is complete: it was issued before these scores
+            // (16 columns at a time: the scores of the block are in registers)
             const float f = grow ? ex2((m - top) * c) : 1.f;
             if (grow) m = top;
             l *= f;
-#pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
-              uint32_t o[32];
-              tc5::ld32(o_tm + 32 * x, o);
+#pragma unroll 1
+            for (int x = 0; x < D / 16; ++x) {
+              uint32_t o[16];
+              tc5::ld16(o_tm + 16 * x, o);
               tc5::wait_ld();
               pin(o);
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tc5::st32(o_tm + 32 * x, o);
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tc5::st16(o_tm + 16 * x, o);
             }
           }
         }
         const float mc = m == -INFINITY ? 0.f : -m * c;
         const uint64_t cc = pair(c, c), mm = pair(mc, mc);
         uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int x = 32 * h; x < 32 * h + 32; ++x) {
-            uint64_t y = pair(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
-            y = fma2(y, cc, mm);
-            const float p0 = ex2(lo(y)), p1 = ex2(hi(y));
-            sum[x & 3] = add2(sum[x & 3], pair(p0, p1));
-            s[x] = pack_bf16x2(p0, p1);
-          }
-          tc5::st32(s_tm + 32 * h, s + 32 * h);
-          tc5::wait_st();
-          tc5::fence_before();
-          mbar_arrive(p_bar + 8 * h);
-        }
+        exp_part<0>(s, cc, mm, sum);
+        hand_over(p_bar, [&] { tc5::st32(s_tm, s); });
+        exp_part<1>(s, cc, mm, sum);
+        hand_over(p_bar + 8, [&] { tc5::st16(s_tm + 32, s + 32); });
+        exp_part<2>(s, cc, mm, sum);
+        hand_over(p_bar + 16, [&] { tc5::st16(s_tm + 48, s + 48); });
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += lo(sum[0]) + hi(sum[0]);
       }
-      if (ok && n_it[i] > 0)
-        ok = __all_sync(kFull, wait(s_bar, n_it[i] & 1, sh, a.status, a.wait_cycles));
-      if (ok) {
-        tc5::fence_after();
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
-        const int h = g * a.G + r - tt * a.G;
-        const int64_t row = int64_t(q0) + t;
-        uint8_t* dst = static_cast<uint8_t*>(a.out) + 2 * (row * a.out_stride + int64_t(h) * D);
+      if (ok && n_it > 0) ok = __all_sync(kFull, wait_for(&sh.o_full[i], tiles++));
+      if (!ok) break;
+      tc5::fence_after();
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
+      const int h = t.g * a.G + r - tt * a.G;
+      const int64_t at = int64_t(t.q0) + row;
+      // where this thread's row goes, -1: nowhere
+      const int64_t to = valid ? 2 * (at * a.out_stride + int64_t(h) * D) : -1;
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
+      for (int x = 0; x < D / 64; ++x) {
+        // 64 columns at a time through shared memory, so that 8 lanes write 128
+        // bytes of a row (a lane writing its own row holds up the load/store
+        // unit, and with it every wait of the CTA, for ~4000 clocks)
+        const bool none = limit == 0;  // no key: nothing was written for the row, or for others' sake only
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
           uint32_t o[32];
-          if (n_it[i] > 0) {
-            tc5::ld32(o_tm + 32 * x, o);
+          if (n_it > 0) {
+            tc5::ld32(o_tm + 64 * x + 32 * z, o);
             tc5::wait_ld();
             pin(o);
-          } else {
-#pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] = 0;
           }
-          if (valid) {
 #pragma unroll
-            for (int y = 0; y < 32; y += 8) {
-              uint4 w;
-              w.x = pack_bf16x2(__uint_as_float(o[y]) * inv, __uint_as_float(o[y + 1]) * inv);
-              w.y = pack_bf16x2(__uint_as_float(o[y + 2]) * inv, __uint_as_float(o[y + 3]) * inv);
-              w.z = pack_bf16x2(__uint_as_float(o[y + 4]) * inv, __uint_as_float(o[y + 5]) * inv);
-              w.w = pack_bf16x2(__uint_as_float(o[y + 6]) * inv, __uint_as_float(o[y + 7]) * inv);
-              if (limit == 0) w = make_uint4(0, 0, 0, 0);  // no key: O was never written for it alone
-              *reinterpret_cast<uint4*>(dst + 2 * (32 * x + y)) = w;
-            }
+          for (int y = 0; y < 4; ++y) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = none ? 0u : pack_bf16x2(__uint_as_float(o[8 * y + 2 * e]) * inv, __uint_as_float(o[8 * y + 2 * e + 1]) * inv);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             out_sm + lane * 128 + (((4 * z + y) ^ (lane & 7)) * 16)),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
           }
         }
-        if (valid && a.lse)
-          a.lse[row * a.H_q + h] = limit == 0 ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
+        __syncwarp();
+#pragma unroll 2
+        for (int y = 0; y < 8; ++y) {
+          const int rr = y * 4 + (lane >> 3), ch = lane & 7;
+          const int64_t dst = __shfl_sync(kFull, to, rr);
+          const uint4 w = lds128(out_sm + rr * 128 + ((ch ^ (rr & 7)) * 16));
+          if (dst >= 0) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + dst + 128 * x + 16 * ch) = w;
+        }
+        __syncwarp();
       }
+      // (the next tile's first P says that O_i has been read)
       tc5::fence_before();
+      if (valid && a.lse) a.lse[at * a.H_q + h] = limit == 0 ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
+      __syncwarp();
+      if (lane == 0) taken(k);
     }
+    tc5::fence_before();
   }
   __syncthreads();
   if (warp == 9) {
@@ -451,8 +601,9 @@ cudaError_t launch_t(const PrefillArgs& a, cudaStream_t st) {
                                              int(Cfg<D>::SMEM));
   if (e != cudaSuccess) return e;
   // sum_b ceil(n_b / span) <= total / span + B
-  const long long tiles = (long long)a.total_q / (2 * a.tok) + a.B;
-  prefill_kernel<D><<<unsigned(tiles * a.H_kv), kThreads, Cfg<D>::SMEM, st>>>(a);
+  const long long tiles = ((long long)a.total_q / (2 * a.tok) + a.B) * a.H_kv;
+  const int grid = int(tiles < device_sm_count() ? tiles : device_sm_count());
+  prefill_kernel<D><<<grid, kThreads, Cfg<D>::SMEM, st>>>(a);
   return cudaGetLastError();
 }
 

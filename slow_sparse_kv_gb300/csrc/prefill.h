@@ -21,6 +21,9 @@ struct PrefillArgs {
   int32_t tok;      // tokens per 128-row query tile: 128 / G
   float scale_log2; // log2(e) / sqrt(d)
   uint32_t* status;
+  uint32_t* next;  // [2]: next tile, CTAs that ran out; zero between launches
+  int32_t* span;   // [B] scratch: CTA tiles of each sequence and KV head
+  int32_t* lvl;    // [B] scratch: the level of its first one
   long long wait_cycles;
 };
 
