@@ -2,25 +2,33 @@
 //
 // A tile is 16 (fp32: 8) consecutive positions of one (sequence, KV head).  All
 // tiles of all sequences stand in one line, sequence by sequence and head by
-// head; CTA c of C takes the c-th of C equal parts of the line, whatever the
-// lengths, and its warp w the tiles whose number is w modulo 8.  Each warp
-// keeps its own ring of tiles in shared memory, filled by its own copies some
-// tiles ahead across the borders of sequences, so that the memory pipe never
-// waits for the arithmetic.  Bound by HBM: 2 d e bytes a position and 4 d G
-// flops, G <= 16.
+// head.  The line is cut, whatever the lengths, into items, one of 3/4 of a CTA's
+// fair share for each CTA and smaller ones taken from a shared counter, because
+// the SMs do not get the same share of HBM (with equal parts the last CTA ended 15%
+// after the median, so 5%).  Four warps look up pages, 32
+// tiles at a time, and copy ahead, across the borders of items and sequences,
+// into rings of 24 KB for each of the eight warps that attend (a warp that looked up and copied for itself waited for
+// the table's reads before each tile: 1.8 times as long).  A tile's place in the
+// line says which warp takes it, so that no sum depends on who took which item.
+// Bound by HBM: 2 d e bytes a position and 4 d G flops, G <= 16.
 //
-// At the end of a piece (the CTA's part of one (sequence, KV head)) the warps'
-// softmax states (m, l, o) are merged through shared memory; a piece that is
-// not the whole unit goes to the workspace, and the CTA that counts the unit's
-// last piece joins them, in the order of the line, so that the result does not
-// depend on who comes last.
+// What an item saw of one (sequence, KV head) is a piece, a softmax state (m, l,
+// o), merged over the warps through shared memory.  The only piece of its unit is
+// normalised and written; others go to the workspace, and a second small kernel,
+// launched early and waiting for the first one's end, joins them in the order of
+// the line.  (Joined by whichever CTA came last, each piece cost a fence and an
+// atomic, 2000 clocks; with pieces of single warps the joins took longer than the
+// merges.)
 //
 // bf16: S^T = K Q^T by mma.sync with the 16 positions as M and the group's heads
 // as N (8 columns; two tiles of them for G > 8), O^T += V^T P^T with P moved to
 // the B operand by movmatrix.  The output is fp32, so P is not rounded to bf16
-// but split into two bf16 terms (what is lost is below 2^-17 of p), at the price
-// of a second product with V.  tcgen05 would leave 128 - G of its 128 rows
-// empty; the kernel waits for HBM either way.
+// but split into three bf16 terms (24 bits in all), at the price of two more
+// products with V; each tile's product starts from zero and is added to o in
+// fp32, because the tensor cores truncate where they add (with two terms and one
+// long chain of MMAs the output's error was 1.5e-6 at 700 positions and 4.3e-6 at
+// 32768).  tcgen05 would leave 128 - G of its 128 rows empty; the kernel waits for
+// HBM either way.
 // fp32: CUDA cores, d spread over the lanes, dots by transpose-reduction.
 #include <cuda_runtime.h>
 
@@ -30,10 +38,14 @@
 namespace sfi {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kStageBytes = 24576;  // ring of one warp
-constexpr float kGrow = 8.0f;       // growth of the maximum (log2) that moves m
+constexpr int kWarps = 8;                    // that attend
+constexpr int kThreads = kWarps * 32;        // of them
+constexpr int kProducers = 4;                // warps that copy
+constexpr int kAllThreads = kThreads + kProducers * 32;
+constexpr int kAttendRegs = 216, kCopyRegs = 72;  // of 168 each at launch: 2 * 216 + 72 = 3 * 168
+constexpr int kRingBytes = 196608;
+constexpr int kItemSlots = 8;                // items that the copies may be ahead
+constexpr float kGrow = 8.0f;                // growth of the maximum (log2) that moves m
 
 enum Load { kTma, kCpAsync, kBulk };
 
@@ -43,19 +55,66 @@ struct Cfg {
   static constexpr int TR = F32 ? 8 : 16;                  // positions per tile
   static constexpr int ROW = D * int(sizeof(T));           // bytes of a row
   static constexpr int HALF = TR * ROW;                    // K part of a stage, then V's
-  static constexpr int STAGES = kStageBytes / (2 * HALF);  // 3 for 8 KB tiles, 6 for 4 KB
+  static constexpr int STAGES = kRingBytes / kWarps / (2 * HALF);  // a warp's: 3 of 8 KB, 6 of 4 KB
+  static constexpr int SLOTS = kWarps * STAGES;
   static constexpr int HEADS = NT * 8;                     // heads that the registers hold
   static constexpr int MH = 4;                             // heads merged at a time
   static constexpr int MROW = D + 4;                       // floats of a merged head: o, m, l
-  static constexpr int SMEM = 1024 + kWarps * kStageBytes + kWarps * MH * MROW * 4;
+  static constexpr int SMEM = 1024 + kRingBytes + kWarps * MH * MROW * 4;
 };
 
-struct Shared {
-  uint64_t full[kWarps][6];
-  volatile int abort;
-  int last;
-  long long pre[kMaxBatch + 1];  // tiles of one KV head in the sequences before b
+// Tiles of one KV head in the sequences before each, in shared memory.
+struct Line {
+  long long pre[kMaxBatch + 1];
   long long part[kWarps];
+};
+
+// How the line of `total` tiles is cut: into regions of equal size, one for each of
+// `grid` CTAs, and each region into items of 3/4, 1/8, 1/16 and 1/16 of it.  The
+// CTAs take their own regions' large items first and then what comes of the
+// small ones, all 1/8s before all 1/16s.  An item's place in the line (place) is
+// not the order in which it is taken (id).
+struct Cut {
+  static constexpr int PARTS = 4;
+  long long total, per, wide;  // tiles of a region; those before `wide` belong to regions with one more
+  int regions, parts, extra;   // extra: regions with one tile more
+
+  __device__ __forceinline__ Cut(long long total_, int grid) {
+    total = total_;
+    // few tiles: fewer regions, of a tile for each warp at least, and no small items
+    const long long most = (total + kWarps - 1) / kWarps;
+    regions = most < grid ? int(most) : grid;
+    per = regions > 0 ? total / regions : 0;
+    extra = regions > 0 ? int(total - per * regions) : 0;
+    wide = extra * (per + 1);
+    parts = per >= 16 * kWarps ? PARTS : 1;
+  }
+  __device__ __forceinline__ long long start(int region) const { return region * per + min(region, extra); }
+  // end of a part, from the region's start
+  __device__ __forceinline__ long long end_of(long long size, int part) const {
+    return part + 1 == parts ? size : size - (size >> (part + 2));
+  }
+  __device__ __forceinline__ bool range(long long id, long long* from, long long* to, int* place) const {
+    const int part = regions > 0 ? int(id / regions) : 0, region = int(id - (long long)part * regions);
+    if (regions == 0 || part >= parts) return false;
+    const long long at = start(region), size = start(region + 1) - at;
+    *from = at + (part > 0 ? end_of(size, part - 1) : 0);
+    *to = at + end_of(size, part);
+    *place = region * parts + part;
+    return true;
+  }
+  // the place of the item that holds tile x
+  __device__ __forceinline__ int holder(long long x) const {
+    int region;
+    if (total < (1LL << 31))  // (a 64-bit division takes ~10 times as long)
+      region = x < wide ? int(uint32_t(x) / uint32_t(per + 1)) : extra + int(uint32_t(x - wide) / uint32_t(per));
+    else
+      region = int(x < wide ? x / (per + 1) : extra + (x - wide) / per);
+    const long long at = start(region), size = start(region + 1) - at;
+    int part = 0;
+    while (part + 1 < parts && x - at >= end_of(size, part)) ++part;
+    return region * parts + part;
+  }
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -93,474 +152,668 @@ struct Unit {
   long long begin, end;
 };
 
-__device__ __forceinline__ void unit_next(Unit& u, const Shared& sh, int B, int H_kv) {
+__device__ __forceinline__ void unit_next(Unit& u, const Line& ln, int B, int H_kv) {
   if (++u.g == H_kv) {
     u.g = 0;
     ++u.b;
   }
   u.begin = u.end;
-  if (u.b < B) u.end += sh.pre[u.b + 1] - sh.pre[u.b];  // else the line's end
+  if (u.b < B) u.end += ln.pre[u.b + 1] - ln.pre[u.b];  // else the line's end
 }
 
 // The unit that holds tile x (x below the line's end).
-__device__ __forceinline__ Unit unit_at(long long x, const Shared& sh, int B, int H_kv) {
+__device__ __forceinline__ Unit unit_at(long long x, const Line& ln, int B, int H_kv) {
   int lo = 0, hi = B;  // last b with pre[b] * H_kv <= x
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (sh.pre[mid] * H_kv <= x) lo = mid;
+    if (ln.pre[mid] * H_kv <= x) lo = mid;
     else hi = mid;
   }
-  const long long nt = sh.pre[lo + 1] - sh.pre[lo];
+  const long long nt = ln.pre[lo + 1] - ln.pre[lo];
+  const long long in = x - ln.pre[lo] * H_kv;
   Unit u;
   u.b = lo;
-  u.g = int((x - sh.pre[lo] * H_kv) / nt);
-  u.begin = sh.pre[lo] * H_kv + u.g * nt;
+  u.g = in < (1LL << 31) ? int(uint32_t(in) / uint32_t(nt)) : int(in / nt);
+  u.begin = ln.pre[lo] * H_kv + u.g * nt;
   u.end = u.begin + nt;
   return u;
 }
 
+// Fills `ln` (the first kThreads threads of a CTA); `flag` reports lengths out of
+// range.
+template <int TR>
+__device__ __forceinline__ void scan_lengths(const PagedGeo& geo, Line& ln, bool flag) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int B = geo.B, cap = geo.max_pages * geo.P;
+  auto tiles = [&](int b) {
+    int n = b < B ? geo.len[b] : 0;
+    if (n < 0 || n > cap) {
+      if (flag) set_status(geo.status, SFI_DEV_LEN_OVER_CAP);
+      n = n < 0 ? 0 : cap;
+    }
+    return (n + TR - 1) / TR;
+  };
+  auto scan = [&](long long x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  if (B <= 32) {
+    if (warp == 0) {
+      const long long run = scan(tiles(lane));
+      if (lane < B) ln.pre[lane + 1] = run;
+      if (lane == 0) ln.pre[0] = 0;
+    }
+    __syncthreads();
+    return;
+  }
+  // (what lies behind the last sequence counts nothing, so the threads behind
+  // kThreads do no harm)
+  constexpr int PER = kMaxBatch / kThreads;
+  int nt[PER];
+  long long mine = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) mine += nt[i] = tiles(tid * PER + i);
+  const long long run = scan(mine);
+  if (lane == 31 && warp < kWarps) ln.part[warp] = run;
+  __syncthreads();
+  long long before = run - mine;
+  for (int w = 0; w < min(warp, kWarps); ++w) before += ln.part[w];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = tid * PER + i;
+    if (b < B) ln.pre[b] = before;
+    before += nt[i];
+    if (b == B - 1) ln.pre[B] = before;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ void attend_sync() { named_bar_sync(1, kThreads); }
+
+// What the warps of a CTA share besides the ring.
+struct Shared {
+  Line ln;
+  uint64_t full[48], empty[48];                           // of each slot of the ring
+  uint64_t item_full[kItemSlots], item_empty[kItemSlots]; // of the items
+  long long item[kItemSlots][2];                          // tiles [from, to); from = to: the end
+  int place[kItemSlots];
+  volatile int abort;
+  float factor[kWarps][4], top[4], sum[4];                // of the heads that are merged
+};
+
+// Tiles of [from, to) whose number is r modulo m (a power of two): the first one,
+// and how many there are.
+__device__ __forceinline__ long long first_of(long long from, int r, int m) { return from + ((r - from) & (m - 1)); }
+__device__ __forceinline__ long long count_of(long long from, long long to, int r, int m) {
+  const long long x = first_of(from, r, m);
+  return x < to ? (to - x + m - 1) / m : 0;
+}
+
+// The copying warps: warp `p` takes the tiles of the attending warps p and p + 4.
 template <typename T, int D, int NT, Load LD>
-__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnArgs a) {
+__device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, const Cut& cut, uint32_t ring, int p) {
+  using C = Cfg<T, D, NT>;
+  constexpr int TR = C::TR;
+  const PagedGeo& geo = a.geo;
+  const int lane = threadIdx.x & 31, P = geo.P, H_kv = geo.H_kv, cap = geo.max_pages * P;
+  const T* const kp = static_cast<const T*>(a.k);
+  const T* const vp = static_cast<const T*>(a.v);
+  uint32_t done[2] = {0, 0};  // tiles of the two warps in the items before
+  // (a CTA beyond the regions has none of its own, and then there are no small items)
+  int ask = blockIdx.x < cut.regions ? int(blockIdx.x) : cut.regions * cut.parts;
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    const int is = k % kItemSlots;
+    long long from, to;
+    if (p == 0) {
+      // this warp takes the items: the CTA's own one first, then from the counter
+      int place = 0;
+      if (!cut.range(__shfl_sync(kFull, ask, 0), &from, &to, &place)) from = to = 0;
+      if (k >= kItemSlots)
+        ok = warp_ctrl_wait(smem_addr(&sh.item_empty[is]), (k / kItemSlots - 1) & 1, &sh.abort, geo.status);
+      if (lane == 0) {
+        sh.item[is][0] = from;
+        sh.item[is][1] = ok ? to : from;
+        sh.place[is] = place;
+        mbar_arrive(smem_addr(&sh.item_full[is]));
+        if (from < to) {
+          ask = cut.regions + atomicAdd(a.next, 1);
+        } else if (atomicAdd(a.next + 1, 1) == int(gridDim.x) - 1) {
+          // the last CTA to run out leaves the counters at zero
+          a.next[0] = 0;
+          a.next[1] = 0;
+        }
+      }
+      __syncwarp();
+    } else {
+      ok = warp_ctrl_wait(smem_addr(&sh.item_full[is]), (k / kItemSlots) & 1, &sh.abort, geo.status);
+      if (!ok) break;
+      from = sh.item[is][0], to = sh.item[is][1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.item_empty[is]));
+    }
+    if (!ok || from >= to) break;
+    const long long first[2] = {first_of(from, p, kWarps), first_of(from, p + kProducers, kWarps)};
+    for (long long x0 = first_of(from, p, kProducers); x0 < to && ok; x0 += kProducers * 32) {
+      // 32 tiles: each lane finds the place and the page of its own
+      const long long x = x0 + kProducers * lane;
+      const bool mine = x < to;
+      Unit u{0, 0, 0, 0};
+      int t = 0, n = 0;
+      int page[LD == kBulk ? TR : 1];
+      if (mine) {
+        u = unit_at(x, sh.ln, geo.B, H_kv);
+        t = int(x - u.begin);
+        n = min(geo.len[u.b], cap);
+      }
+      const int32_t* const row = geo.table + int64_t(u.b) * geo.max_pages;
+      if (LD != kCpAsync) {
+        bool bad = false;
+#pragma unroll
+        for (int r = 0; r < (LD == kBulk ? TR : 1); ++r) {
+          const int pos = t * TR + r;
+          page[r] = mine && pos < n ? row[pos / P] : 0;
+          if (page[r] < 0 || page[r] >= geo.n_pages) bad = true, page[r] = 0;
+        }
+        if (bad) set_status(geo.status, SFI_DEV_BAD_INDEX);
+      }
+      const int count = int(min(32LL, (to - x0 + kProducers - 1) / kProducers));
+      for (int i = 0; i < count && ok; ++i) {
+        const long long xi = x0 + kProducers * i;
+        const int w = int(xi >> 2) & 1;  // which of the two warps
+        const uint32_t y = done[w] + uint32_t(xi - first[w]) / kWarps;
+        const int slot = (p + w * kProducers) * C::STAGES + int(y % C::STAGES);
+        const uint32_t use = y / C::STAGES;
+        if (use > 0) ok = warp_ctrl_wait(smem_addr(&sh.empty[slot]), (use - 1) & 1, &sh.abort, geo.status);
+        if (!ok) break;
+        const uint32_t dst = ring + slot * 2 * C::HALF, bar = smem_addr(&sh.full[slot]);
+        if constexpr (LD == kTma) {
+          if (lane == i) {
+            const int at = int(page[0] * (geo.page_stride / D) + u.g * P + t * TR % P);
+            mbar_arrive_expect_tx(bar, 2 * C::HALF);
+            tma_load_3d(dst, &a.tmk, 0, at, 0, bar);
+            tma_load_3d(dst + C::HALF, &a.tmv, 0, at, 0, bar);
+          }
+        } else if constexpr (LD == kBulk) {
+          if (lane == i) {
+            // runs of rows that lie in one page
+            const int rows = min(TR, n - t * TR);
+            mbar_arrive_expect_tx(bar, uint32_t(rows) * 2 * C::ROW);
+#pragma unroll
+            for (int r = 0; r < TR; ++r) {
+              const int in = (t * TR + r) % P;
+              if (r < rows && (r == 0 || in == 0)) {
+                const uint32_t bytes = uint32_t(min(P - in, rows - r)) * C::ROW;
+                const int64_t at = page[r] * geo.page_stride + (int64_t(u.g) * P + in) * D;
+                bulk_load(dst + r * C::ROW, kp + at, bytes, bar);
+                bulk_load(dst + C::HALF + r * C::ROW, vp + at, bytes, bar);
+              }
+            }
+          }
+        } else {
+          // 16-byte chunks of single rows, in the layout that the maps' swizzle gives
+          constexpr int CH = C::ROW / 16;  // chunks of a row
+          const int ut = __shfl_sync(kFull, t, i), ug = __shfl_sync(kFull, u.g, i), un = __shfl_sync(kFull, n, i);
+          const int32_t* const urow = geo.table + int64_t(__shfl_sync(kFull, u.b, i)) * geo.max_pages;
+          const int pos = ut * TR + lane % TR;
+          int pg = pos < un ? urow[pos / P] : 0;
+          if (pg < 0 || pg >= geo.n_pages) {
+            set_status(geo.status, SFI_DEV_BAD_INDEX);
+            pg = 0;
+          }
+          const int64_t at = pg * geo.page_stride + (int64_t(ug) * P + pos % P) * D;
+#pragma unroll
+          for (int j = 0; j < TR * CH / 32; ++j) {
+            const int r = (j * 32 + lane) / CH, ch = lane % CH;
+            const int64_t ra = __shfl_sync(kFull, at, r) + ch * 8;
+            const uint32_t some = ut * TR + r < un ? 16 : 0;
+            const uint32_t dr = dst + (ch / 8) * (TR * 128) + r * 128 + ((ch & 7) ^ (r & 7)) * 16;
+            cp_async16_zfill(dr, kp + ra, some);
+            cp_async16_zfill(dr + C::HALF, vp + ra, some);
+          }
+          cp_async_arrive_noinc(bar);
+        }
+      }
+      __syncwarp();
+    }
+    for (int w = 0; w < 2; ++w) done[w] += uint32_t(count_of(from, to, p + w * kProducers, kWarps));
+  }
+  // No copy may be in flight when the CTA exits: the attending warps wait for
+  // every tile, unless one of these warps gave up (after seconds, in which all
+  // earlier copies have landed).
+  if (!ok) sh.abort = 2;
+  if (LD == kCpAsync) asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <typename T, int D, int NT, Load LD>
+__global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnArgs a) {
   using C = Cfg<T, D, NT>;
   constexpr bool F32 = C::F32;
   constexpr int TR = C::TR;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
-  const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
-  float* const merge = reinterpret_cast<float*>(smem_raw + (base - smem_addr(smem_raw)) + kWarps * kStageBytes);
+  const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u;
+  float* const merge = reinterpret_cast<float*>(smem_raw + (ring - smem_addr(smem_raw)) + kRingBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PagedGeo& geo = a.geo;
-  const int B = geo.B, H_kv = geo.H_kv, P = geo.P, G = a.G;
-  const int cap = geo.max_pages * P;
+  const int B = geo.B, H_kv = geo.H_kv, G = a.G;
+  const int cap = geo.max_pages * geo.P;
 
-  // ---- tiles before each sequence
-  {
-    constexpr int PER = kMaxBatch / kThreads;
-    int nt[PER];
-    long long mine = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int b = tid * PER + i;
-      int n = b < B ? geo.len[b] : 0;
-      if (n < 0 || n > cap) {
-        if (blockIdx.x == 0) set_status(geo.status, SFI_DEV_LEN_OVER_CAP);
-        n = n < 0 ? 0 : cap;
-      }
-      nt[i] = (n + TR - 1) / TR;
-      mine += nt[i];
-    }
-    long long run = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(kFull, run, o);
-      if (lane >= o) run += y;
-    }
-    if (lane == 31) sh.part[warp] = run;
-    if (tid == 0) sh.abort = 0;
-    if (lane == 0 && LD != kCpAsync) {
-      for (int i = 0; i < C::STAGES; ++i) mbar_init(smem_addr(&sh.full[warp][i]), 1);
-      fence_mbar_init();
-    }
-    __syncthreads();
-    long long before = run - mine;
-    for (int w = 0; w < warp; ++w) before += sh.part[w];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int b = tid * PER + i;
-      if (b < B) sh.pre[b] = before;
-      before += nt[i];
-      if (b == B - 1) sh.pre[B] = before;
-    }
-    __syncthreads();
+  if (tid < C::SLOTS) {
+    mbar_init(smem_addr(&sh.full[tid]), LD == kCpAsync ? 32 : 1);
+    mbar_init(smem_addr(&sh.empty[tid]), 1);
+  } else if (tid >= 64 && tid < 64 + kItemSlots) {
+    mbar_init(smem_addr(&sh.item_full[tid - 64]), 1);
+    mbar_init(smem_addr(&sh.item_empty[tid - 64]), kWarps + kProducers - 1);
+  } else if (tid == 96) {
+    sh.abort = 0;
   }
-  const long long total = sh.pre[B] * H_kv;
+  fence_mbar_init();
+  // (this kernel starts while the one before it on the stream drains, and the
+  // joining kernel while this one drains; each waits for the results before it)
+  pdl_launch();
+  pdl_wait();
+  scan_lengths<TR>(geo, sh.ln, blockIdx.x == 0);
+  const Line& ln = sh.ln;
+  const long long total = ln.pre[B] * H_kv;
 
   // sequences that hold nothing
   for (int u = blockIdx.x; u < B * H_kv; u += gridDim.x) {
     const int b = u / H_kv, g = u - b * H_kv;
-    if (sh.pre[b + 1] != sh.pre[b]) continue;
+    if (ln.pre[b + 1] != ln.pre[b]) continue;
     const int64_t row = int64_t(b) * a.H_q + int64_t(g) * G;
-    for (int i = tid; i < G * D; i += kThreads) a.out[row * D + i] = 0.f;
+    for (int i = tid; i < G * D; i += kAllThreads) a.out[row * D + i] = 0.f;
     if (a.lse && tid < G) a.lse[row + tid] = -INFINITY;
   }
-  // parts of a tile for each warp at least
-  const long long parts = min((long long)gridDim.x, (total + kWarps - 1) / kWarps);
-  if (blockIdx.x >= parts) return;
-  const long long T0 = blockIdx.x * total / parts, T1 = (blockIdx.x + 1) * total / parts;
+  const Cut cut(total, gridDim.x);
 
-  const uint32_t ring = base + warp * kStageBytes;
-  const T* const kp = static_cast<const T*>(a.k);
-  const T* const vp = static_cast<const T*>(a.v);
-  const float c = a.scale_log2;
-
-  // ---- this warp's copies: tile `ld` of unit `lu`, into stage ls
-  const long long first = T0 + ((warp - T0) % kWarps + kWarps) % kWarps;
-  long long ld = first;
-  int ls = 0;
-  Unit lu = unit_at(T0, sh, B, H_kv);
-  int page = 0;  // of this lane's row of tile ld
-  auto fetch_page = [&]() {
-    if (ld >= T1) return;
-    while (ld >= lu.end) unit_next(lu, sh, B, H_kv);
-    const int pos = int(ld - lu.begin) * TR + (LD == kTma ? 0 : lane % TR);
-    const int n = min(geo.len[lu.b], cap);
-    page = pos < n ? geo.table[int64_t(lu.b) * geo.max_pages + pos / P] : 0;
-  };
-  auto issue = [&]() {  // tile ld, whose page is known; then looks up the next one's
-    if (ld >= T1) {
-      if (LD == kCpAsync) asm volatile("cp.async.commit_group;" ::: "memory");
-      return;
-    }
-    if (page < 0 || page >= geo.n_pages) {
-      set_status(geo.status, SFI_DEV_BAD_INDEX);
-      page = 0;
-    }
-    const int t = int(ld - lu.begin);
-    const uint32_t dst = ring + ls * 2 * C::HALF;
-    const uint32_t bar = smem_addr(&sh.full[warp][ls]);
-    if constexpr (LD == kTma) {
-      if (lane == 0) {
-        const int row = int(page * (geo.page_stride / D) + lu.g * P + t * TR % P);
-        mbar_arrive_expect_tx(bar, 2 * C::HALF);
-        tma_load_3d(dst, &a.tmk, 0, row, 0, bar);
-        tma_load_3d(dst + C::HALF, &a.tmv, 0, row, 0, bar);
-      }
-    } else {
-      const int n = min(geo.len[lu.b], cap);
-      const int pos = t * TR + lane % TR;
-      const int in = pos % P;
-      const int64_t at = page * geo.page_stride + (int64_t(lu.g) * P + in) * D;
-      if constexpr (LD == kBulk) {
-        // runs of rows that lie in one page, one lane each
-        if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(min(TR, n - t * TR)) * 2 * C::ROW);
-        __syncwarp();
-        if (lane < TR && pos < n && (lane == 0 || in == 0)) {
-          const uint32_t bytes = uint32_t(min(min(P - in, TR - lane), n - pos)) * C::ROW;
-          bulk_load(dst + lane * C::ROW, kp + at, bytes, bar);
-          bulk_load(dst + C::HALF + lane * C::ROW, vp + at, bytes, bar);
-        }
-      } else {
-        // 16-byte chunks, in the layout that the maps' swizzle gives
-        constexpr int CH = C::ROW / 16;  // chunks of a row
-#pragma unroll
-        for (int i = 0; i < TR * CH / 32; ++i) {
-          const int r = (i * 32 + lane) / CH, ch = lane % CH;
-          const int64_t ra = __shfl_sync(kFull, at, r) + ch * 8;
-          const uint32_t some = t * TR + r < n ? 16 : 0;
-          const uint32_t to = dst + (ch / 8) * (TR * 128) + r * 128 + ((ch & 7) ^ (r & 7)) * 16;
-          cp_async16_zfill(to, kp + ra, some);
-          cp_async16_zfill(to + C::HALF, vp + ra, some);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      }
-    }
-    ls = ls + 1 == C::STAGES ? 0 : ls + 1;
-    ld += kWarps;
-    fetch_page();
-  };
-  fetch_page();
-  for (int i = 0; i < C::STAGES - 1; ++i) issue();
-
-  // ---- the CTA's pieces
-  long long x = first;  // this warp's next tile to compute
-  int cs = 0;
-  uint32_t phase = 0;
-  for (Unit u = unit_at(T0, sh, B, H_kv); u.begin < T1; unit_next(u, sh, B, H_kv)) {
-    if (u.end == u.begin) continue;
-    const long long pe = min(u.end, T1);
-    const int n = min(geo.len[u.b], cap);
-    const int64_t qrow = (int64_t(u.b) * a.H_q + int64_t(u.g) * G) * D;
-
-    // state: bf16 head 2 (lane % 4) + e of column tile h, in every lane with the same lane % 4;
-    // fp32 head 4 h + lane % 4
-    constexpr int NS = F32 ? NT * 2 : NT;
-    constexpr int NE = F32 ? 1 : 2;
-    float m[NS][NE], l[NS][NE];
-#pragma unroll
-    for (int h = 0; h < NS; ++h)
-#pragma unroll
-      for (int e = 0; e < NE; ++e) m[h][e] = -INFINITY, l[h][e] = 0.f;
-
-    // per-lane operands
-    constexpr int KS = D / 16;
-    uint32_t qb[F32 ? 1 : NT][KS][2];
-    float o[F32 ? 1 : KS][F32 ? 1 : NT][4];
-    float qf[F32 ? NS * 4 : 1][4], of[F32 ? NS * 4 : 1][4];
-    constexpr int LPR = D / 4, RPP = 32 / LPR;  // fp32: lanes per row, rows per pass
-    const int li = lane % LPR, half = lane / LPR;
-    if constexpr (!F32) {
-      const uint32_t* qw = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) + qrow);
-#pragma unroll
-      for (int h = 0; h < NT; ++h) {
-        const int head = h * 8 + (lane >> 2);
-#pragma unroll
-        for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            qb[h][kk][e] = head < G ? qw[(head * D + kk * 16 + e * 8) / 2 + (lane & 3)] : 0u;
-      }
-#pragma unroll
-      for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-        for (int h = 0; h < NT; ++h)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[kk][h][e] = 0.f;
-    } else {
-#pragma unroll
-      for (int h = 0; h < NS * 4; ++h) {
-        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (h < G) w = reinterpret_cast<const float4*>(static_cast<const T*>(a.q) + qrow + h * D)[li];
-        qf[h][0] = w.x, qf[h][1] = w.y, qf[h][2] = w.z, qf[h][3] = w.w;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) of[h][e] = 0.f;
-      }
-    }
-
-    for (; x < pe; x += kWarps) {
-      // ---- the next tile's copies go out, this one's rows have landed
+  if (warp >= kWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+    copy_tiles<T, D, NT, LD>(a, sh, cut, ring, warp - kWarps);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAttendRegs));
+    const float c = a.scale_log2;
+    uint32_t y = 0;  // this warp's tiles so far
+    for (int k = 0;; ++k) {
+      const int is = k % kItemSlots;
+      if (!warp_ctrl_wait(smem_addr(&sh.item_full[is]), (k / kItemSlots) & 1, &sh.abort, geo.status)) break;
+      const long long from = sh.item[is][0], to = sh.item[is][1];
+      const int place = sh.place[is];
       __syncwarp();
-      issue();
-      if constexpr (LD == kCpAsync) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(C::STAGES - 1) : "memory");
-        __syncwarp();
-      } else {
-        const bool ok = warp_pipe_wait(smem_addr(&sh.full[warp][cs]), phase, &sh.abort, geo.status, a.wait_cycles);
-        if (!ok) {
-          // no copy of this warp may be in flight when the CTA exits: the
-          // stage's rows land before the warp goes on (without them)
-          mbar_wait(smem_addr(&sh.full[warp][cs]), phase);
-          __syncwarp();
-          if (++cs == C::STAGES) cs = 0, phase ^= 1;
-          continue;
-        }
-      }
-      const uint32_t ks = ring + cs * 2 * C::HALF, vs = ks + C::HALF;
-      const int left = n - int(x - u.begin) * TR;  // rows of the tile that count
+      if (lane == 0) mbar_arrive(smem_addr(&sh.item_empty[is]));
+      if (from >= to) break;
+      long long x = first_of(from, warp, kWarps);  // this warp's next tile
+      for (Unit u = unit_at(from, ln, B, H_kv); u.begin < to; unit_next(u, ln, B, H_kv)) {
+        if (u.end == u.begin) continue;
+        const long long pe = min(u.end, to);
+        const int b = u.b, g = u.g;
+        const int n = min(geo.len[b], cap);
+        const int64_t qrow = (int64_t(b) * a.H_q + int64_t(g) * G) * D;
 
-      if constexpr (!F32) {
-        float s[NT][4];
+        // state: bf16 head 2 (lane % 4) + e of column tile h, in every lane with the same lane % 4;
+        // fp32 head 4 h + lane % 4
+        constexpr int NS = F32 ? NT * 2 : NT;
+        constexpr int NE = F32 ? 1 : 2;
+        float m[NS][NE], l[NS][NE];
 #pragma unroll
-        for (int h = 0; h < NT; ++h)
+        for (int h = 0; h < NS; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[h][e] = 0.f;
-        {
-          const int r = lane & 15, hi = lane >> 4;
-#pragma unroll
-          for (int kk = 0; kk < KS; ++kk) {
-            uint32_t k0, k1, k2, k3;
-            ldsm_x4(ks + (kk / 4) * (TR * 128) + r * 128 + ((((kk & 3) * 2 + hi) ^ (r & 7)) * 16), k0, k1, k2, k3);
-#pragma unroll
-            for (int h = 0; h < NT; ++h) mma_bf16_16816(s[h], k0, k1, k2, k3, qb[h][kk][0], qb[h][kk][1]);
-          }
-        }
-        const int r0 = lane >> 2;
-        const bool in0 = r0 < left, in1 = r0 + 8 < left;
-        uint32_t ph[NT][2], pl[NT][2];
-#pragma unroll
-        for (int h = 0; h < NT; ++h) {
-          float top[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            s[h][e] = in0 ? s[h][e] : -INFINITY;
-            s[h][2 + e] = in1 ? s[h][2 + e] : -INFINITY;
-            top[e] = fmaxf(s[h][e], s[h][2 + e]);
-#pragma unroll
-            for (int w = 4; w < 32; w <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], w));
-          }
-          const bool g0 = (top[0] - m[h][0]) * c > kGrow, g1 = (top[1] - m[h][1]) * c > kGrow;
-          if (__any_sync(kFull, g0 || g1)) {
-            const float f0 = g0 ? ex2((m[h][0] - top[0]) * c) : 1.f, f1 = g1 ? ex2((m[h][1] - top[1]) * c) : 1.f;
-            if (g0) m[h][0] = top[0];
-            if (g1) m[h][1] = top[1];
-            l[h][0] *= f0;
-            l[h][1] *= f1;
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
-              o[kk][h][0] *= f0, o[kk][h][1] *= f1;
-              o[kk][h][2] *= f0, o[kk][h][3] *= f1;
-            }
-          }
-          const float b0 = m[h][0] == -INFINITY ? 0.f : m[h][0] * c, b1 = m[h][1] == -INFINITY ? 0.f : m[h][1] * c;
-          const float p0 = ex2(fmaf(s[h][0], c, -b0)), p1 = ex2(fmaf(s[h][1], c, -b1));
-          const float p2 = ex2(fmaf(s[h][2], c, -b0)), p3 = ex2(fmaf(s[h][3], c, -b1));
-          l[h][0] += p0 + p2;
-          l[h][1] += p1 + p3;
-          const uint32_t h0 = pack_bf16x2(p0, p1), h1 = pack_bf16x2(p2, p3);
-          const uint32_t l0 = pack_bf16x2(p0 - __uint_as_float(h0 << 16), p1 - __uint_as_float(h0 & 0xffff0000u));
-          const uint32_t l1 = pack_bf16x2(p2 - __uint_as_float(h1 << 16), p3 - __uint_as_float(h1 & 0xffff0000u));
-          ph[h][0] = movmatrix_trans(h0), ph[h][1] = movmatrix_trans(h1);
-          pl[h][0] = movmatrix_trans(l0), pl[h][1] = movmatrix_trans(l1);
-        }
-        // rows behind the sequence's end may hold anything: 0 * NaN is not 0
-        const int vr = 2 * (lane & 3);
-        const uint32_t m0 = (vr < left ? 0xffffu : 0u) | (vr + 1 < left ? 0xffff0000u : 0u);
-        const uint32_t m1 = (vr + 8 < left ? 0xffffu : 0u) | (vr + 9 < left ? 0xffff0000u : 0u);
-        const int r = (lane & 7) + (lane >> 4) * 8, hi = (lane >> 3) & 1;
-#pragma unroll
-        for (int kk = 0; kk < KS; ++kk) {
-          uint32_t v0, v1, v2, v3;
-          ldsm_x4_trans(vs + (kk / 4) * (TR * 128) + r * 128 + ((((kk & 3) * 2 + hi) ^ (r & 7)) * 16), v0, v1, v2, v3);
-          if (left < TR) v0 &= m0, v1 &= m0, v2 &= m1, v3 &= m1;
+          for (int e = 0; e < NE; ++e) m[h][e] = -INFINITY, l[h][e] = 0.f;
+
+        // per-lane operands
+        constexpr int KS = D / 16;
+        uint32_t qb[F32 ? 1 : NT][KS][2];
+        float o[F32 ? 1 : KS][F32 ? 1 : NT][4];
+        float qf[F32 ? NS * 4 : 1][4], of[F32 ? NS * 4 : 1][4];
+        constexpr int LPR = D / 4, RPP = 32 / LPR;  // fp32: lanes per row, rows per pass
+        const int li = lane % LPR, half = lane / LPR;
+        if constexpr (!F32) {
+          const uint32_t* qw = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) + qrow);
 #pragma unroll
           for (int h = 0; h < NT; ++h) {
-            mma_bf16_16816(o[kk][h], v0, v1, v2, v3, ph[h][0], ph[h][1]);
-            mma_bf16_16816(o[kk][h], v0, v1, v2, v3, pl[h][0], pl[h][1]);
+            const int head = h * 8 + (lane >> 2);
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                qb[h][kk][e] = head < G ? qw[(head * D + kk * 16 + e * 8) / 2 + (lane & 3)] : 0u;
           }
-        }
-      } else {
-        constexpr int PASS = TR / RPP;
 #pragma unroll
-        for (int h = 0; h < NS; ++h) {
-          if (h * 4 >= G) break;
-          float v[PASS * 4];
+          for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
-          for (int i = 0; i < PASS; ++i) {
-            const uint4 w = lds128(ks + (i * RPP + half) * C::ROW + li * 16);
-            const float k0 = __uint_as_float(w.x), k1 = __uint_as_float(w.y), k2 = __uint_as_float(w.z),
-                        k3 = __uint_as_float(w.w);
+            for (int h = 0; h < NT; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[i * 4 + e] = k0 * qf[h * 4 + e][0] + k1 * qf[h * 4 + e][1] + k2 * qf[h * 4 + e][2] + k3 * qf[h * 4 + e][3];
-          }
-          // lane li of a row group: the dot of pass li / 4 and head 4 h + li % 4
-          transpose_reduce<LPR>(v, li);
-          const int row = (li >> 2) * RPP + half;
-          const float s = row < left ? v[0] : -INFINITY;
-          float top = s;
-#pragma unroll
-          for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, w));
-          const bool grow = (top - m[h][0]) * c > kGrow;
-          if (__any_sync(kFull, grow)) {
-            const float f = grow ? ex2((m[h][0] - top) * c) : 1.f;
-            if (grow) m[h][0] = top;
-            l[h][0] *= f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float fe = __shfl_sync(kFull, f, e);
-#pragma unroll
-              for (int y = 0; y < 4; ++y) of[h * 4 + e][y] *= fe;
-            }
-          }
-          const float p = ex2(fmaf(s, c, -(m[h][0] == -INFINITY ? 0.f : m[h][0] * c)));
-          l[h][0] += p;
-#pragma unroll
-          for (int i = 0; i < PASS; ++i) {
-            uint4 w = lds128(vs + (i * RPP + half) * C::ROW + li * 16);
-            if (i * RPP + half >= left) w = make_uint4(0, 0, 0, 0);  // 0 * NaN is not 0
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float pe_ = __shfl_sync(kFull, p, half * LPR + i * 4 + e);
-              of[h * 4 + e][0] = fmaf(pe_, __uint_as_float(w.x), of[h * 4 + e][0]);
-              of[h * 4 + e][1] = fmaf(pe_, __uint_as_float(w.y), of[h * 4 + e][1]);
-              of[h * 4 + e][2] = fmaf(pe_, __uint_as_float(w.z), of[h * 4 + e][2]);
-              of[h * 4 + e][3] = fmaf(pe_, __uint_as_float(w.w), of[h * 4 + e][3]);
-            }
-          }
-        }
-      }
-      if (++cs == C::STAGES) cs = 0, phase ^= 1;
-    }
-
-    // ---- merge the warps' states, MH heads at a time
-    // the unit's pieces: parts of the CTAs that hold its first to its last tile
-    const long long c0 = ((u.begin + 1) * parts - 1) / total, c1 = (u.end * parts - 1) / total;
-    const int pieces = int(c1 - c0) + 1;
-    const int uid = u.b * H_kv + u.g;
-    float* const slot0 = a.partials + (c0 + uid) * int64_t(G) * (D + 2);
-    float* const slot = slot0 + (blockIdx.x - c0) * int64_t(G) * (D + 2);
-#pragma unroll
-    for (int h0 = 0; h0 < C::HEADS; h0 += C::MH) {
-      if (h0 >= G) break;
-      float* const mine = merge + warp * C::MH * C::MROW;
-      if constexpr (!F32) {
-        const int h = h0 / 8;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float t = l[h][e];
-#pragma unroll
-          for (int w = 4; w < 32; w <<= 1) t += __shfl_xor_sync(kFull, t, w);
-          const int at = h * 8 + 2 * (lane & 3) + e - h0;  // this lane's head
-          if (at < 0 || at >= C::MH) continue;
-          float* const row = mine + at * C::MROW;
-          if (lane < 4) row[D] = m[h][e], row[D + 1] = t;
-#pragma unroll
-          for (int kk = 0; kk < KS; ++kk) {
-            row[kk * 16 + (lane >> 2)] = o[kk][h][e];
-            row[kk * 16 + 8 + (lane >> 2)] = o[kk][h][2 + e];
-          }
-        }
-      } else {
-        const int h = h0 / 4;
-        float t = l[h][0];
-#pragma unroll
-        for (int w = 4; w < 32; w <<= 1) t += __shfl_xor_sync(kFull, t, w);
-        if (lane < 4) mine[lane * C::MROW + D] = m[h][0], mine[lane * C::MROW + D + 1] = t;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            if (RPP == 2) of[h * 4 + e][y] += __shfl_xor_sync(kFull, of[h * 4 + e][y], 16);
-            if (half == 0) mine[e * C::MROW + li * 4 + y] = of[h * 4 + e][y];
-          }
-        }
-      }
-      __syncthreads();
-      for (int i = tid; i < min(C::MH, G - h0) * D; i += kThreads) {
-        const int h = i / D, d = i - h * D;
-        const float* const row = merge + h * C::MROW;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, row[w * C::MH * C::MROW + D]);
-        float L = 0.f, O = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float* const rw = row + w * C::MH * C::MROW;
-          if (rw[D] == -INFINITY && rw[D + 1] == 0.f) continue;  // saw nothing
-          const float f = ex2((rw[D] - M) * c);
-          L += f * rw[D + 1];
-          O += f * rw[d];
-        }
-        if (pieces == 1) {
-          a.out[qrow + (h0 + h) * D + d] = L == 0.f ? 0.f : O / L;
-          if (d == 0 && a.lse) a.lse[qrow / D + h0 + h] = (M * c + log2f(L)) * 0.6931471805599453f;
+              for (int e = 0; e < 4; ++e) o[kk][h][e] = 0.f;
         } else {
-          float* const p = slot + (h0 + h) * (D + 2);
-          p[d] = O;
-          if (d == 0) p[D] = M, p[D + 1] = L;
-        }
-      }
-      __syncthreads();
-    }
-    if (pieces > 1) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const int seen = atomicAdd(a.counters + uid, 1);
-        sh.last = seen == pieces - 1;
-        if (sh.last) a.counters[uid] = 0;
-      }
-      __syncthreads();
-      if (sh.last) {
-        __threadfence();
-        const int64_t step = int64_t(G) * (D + 2);
-        for (int i = tid; i < G * D; i += kThreads) {
-          const int h = i / D, d = i - h * D;
-          const float* const p = slot0 + h * (D + 2);
-          float M = -INFINITY, L = 0.f, O = 0.f;
-#pragma unroll 8
-          for (int w = 0; w < pieces; ++w) M = fmaxf(M, __ldcg(p + w * step + D));
-#pragma unroll 8
-          for (int w = 0; w < pieces; ++w) {
-            const float mw = __ldcg(p + w * step + D), lw = __ldcg(p + w * step + D + 1), ow = __ldcg(p + w * step + d);
-            const bool none = mw == -INFINITY && lw == 0.f;
-            const float f = ex2((mw - M) * c);
-            L += none ? 0.f : f * lw;
-            O += none ? 0.f : f * ow;
+#pragma unroll
+          for (int h = 0; h < NS * 4; ++h) {
+            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (h < G) w = reinterpret_cast<const float4*>(static_cast<const T*>(a.q) + qrow + h * D)[li];
+            qf[h][0] = w.x, qf[h][1] = w.y, qf[h][2] = w.z, qf[h][3] = w.w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) of[h][e] = 0.f;
           }
-          a.out[qrow + h * D + d] = L == 0.f ? 0.f : O / L;
-          if (d == 0 && a.lse) a.lse[qrow / D + h] = (M * c + log2f(L)) * 0.6931471805599453f;
+        }
+
+        for (; x < pe; x += kWarps) {
+          const int slot = warp * C::STAGES + int(y % C::STAGES);
+          const uint32_t use = y / C::STAGES;
+          ++y;
+          const int left = n - int(x - u.begin) * TR;  // rows of the tile that count
+          const bool ok = warp_pipe_wait(smem_addr(&sh.full[slot]), use & 1, &sh.abort, geo.status, a.wait_cycles);
+          if (!ok) {
+            // the stage is given back once its rows have landed, without them
+            if (sh.abort != 2) mbar_wait(smem_addr(&sh.full[slot]), use & 1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.empty[slot]));
+            continue;
+          }
+          const uint32_t ks = ring + slot * 2 * C::HALF, vs = ks + C::HALF;
+
+          if constexpr (!F32) {
+            float s[NT][4];
+#pragma unroll
+            for (int h = 0; h < NT; ++h)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[h][e] = 0.f;
+            {
+              const int r = lane & 15, hi = lane >> 4;
+#pragma unroll
+              for (int kk = 0; kk < KS; ++kk) {
+                uint32_t k0, k1, k2, k3;
+                ldsm_x4(ks + (kk / 4) * (TR * 128) + r * 128 + ((((kk & 3) * 2 + hi) ^ (r & 7)) * 16), k0, k1, k2, k3);
+#pragma unroll
+                for (int h = 0; h < NT; ++h) mma_bf16_16816(s[h], k0, k1, k2, k3, qb[h][kk][0], qb[h][kk][1]);
+              }
+            }
+            const int r0 = lane >> 2;
+            const bool in0 = r0 < left, in1 = r0 + 8 < left;
+            uint32_t pw[NT][3][2];  // P^T in three bf16 terms
+#pragma unroll
+            for (int h = 0; h < NT; ++h) {
+              float top[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                s[h][e] = in0 ? s[h][e] : -INFINITY;
+                s[h][2 + e] = in1 ? s[h][2 + e] : -INFINITY;
+                top[e] = fmaxf(s[h][e], s[h][2 + e]);
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], w));
+              }
+              const bool g0 = (top[0] - m[h][0]) * c > kGrow, g1 = (top[1] - m[h][1]) * c > kGrow;
+              if (__any_sync(kFull, g0 || g1)) {
+                const float f0 = g0 ? ex2((m[h][0] - top[0]) * c) : 1.f, f1 = g1 ? ex2((m[h][1] - top[1]) * c) : 1.f;
+                if (g0) m[h][0] = top[0];
+                if (g1) m[h][1] = top[1];
+                l[h][0] *= f0;
+                l[h][1] *= f1;
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                  o[kk][h][0] *= f0, o[kk][h][1] *= f1;
+                  o[kk][h][2] *= f0, o[kk][h][3] *= f1;
+                }
+              }
+              const float b0 = m[h][0] == -INFINITY ? 0.f : m[h][0] * c, b1 = m[h][1] == -INFINITY ? 0.f : m[h][1] * c;
+              const float p0 = ex2(fmaf(s[h][0], c, -b0)), p1 = ex2(fmaf(s[h][1], c, -b1));
+              const float p2 = ex2(fmaf(s[h][2], c, -b0)), p3 = ex2(fmaf(s[h][3], c, -b1));
+              l[h][0] += p0 + p2;
+              l[h][1] += p1 + p3;
+              float r0 = p0, r1 = p1, r2 = p2, r3 = p3;
+#pragma unroll
+              for (int e = 0; e < 3; ++e) {
+                const uint32_t w0 = pack_bf16x2(r0, r1), w1 = pack_bf16x2(r2, r3);
+                pw[h][e][0] = movmatrix_trans(w0);
+                pw[h][e][1] = movmatrix_trans(w1);
+                r0 -= __uint_as_float(w0 << 16), r1 -= __uint_as_float(w0 & 0xffff0000u);
+                r2 -= __uint_as_float(w1 << 16), r3 -= __uint_as_float(w1 & 0xffff0000u);
+              }
+            }
+            // rows behind the sequence's end may hold anything: 0 * NaN is not 0
+            const int vr = 2 * (lane & 3);
+            const uint32_t m0 = (vr < left ? 0xffffu : 0u) | (vr + 1 < left ? 0xffff0000u : 0u);
+            const uint32_t m1 = (vr + 8 < left ? 0xffffu : 0u) | (vr + 9 < left ? 0xffff0000u : 0u);
+            const int r = (lane & 7) + (lane >> 4) * 8, hi = (lane >> 3) & 1;
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+              uint32_t v0, v1, v2, v3;
+              ldsm_x4_trans(vs + (kk / 4) * (TR * 128) + r * 128 + ((((kk & 3) * 2 + hi) ^ (r & 7)) * 16), v0, v1, v2, v3);
+              if (left < TR) v0 &= m0, v1 &= m0, v2 &= m1, v3 &= m1;
+#pragma unroll
+              for (int h = 0; h < NT; ++h) {
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int e = 2; e >= 0; --e) mma_bf16_16816(d, v0, v1, v2, v3, pw[h][e][0], pw[h][e][1]);  // small terms first
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[kk][h][e] += d[e];
+              }
+            }
+          } else {
+            constexpr int PASS = TR / RPP;
+#pragma unroll
+            for (int h = 0; h < NS; ++h) {
+              if (h * 4 >= G) break;
+              float v[PASS * 4];
+#pragma unroll
+              for (int i = 0; i < PASS; ++i) {
+                const uint4 w = lds128(ks + (i * RPP + half) * C::ROW + li * 16);
+                const float k0 = __uint_as_float(w.x), k1 = __uint_as_float(w.y), k2 = __uint_as_float(w.z),
+                            k3 = __uint_as_float(w.w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  v[i * 4 + e] = k0 * qf[h * 4 + e][0] + k1 * qf[h * 4 + e][1] + k2 * qf[h * 4 + e][2] + k3 * qf[h * 4 + e][3];
+              }
+              // lane li of a row group: the dot of pass li / 4 and head 4 h + li % 4
+              transpose_reduce<LPR>(v, li);
+              const int row = (li >> 2) * RPP + half;
+              const float s = row < left ? v[0] : -INFINITY;
+              float top = s;
+#pragma unroll
+              for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, w));
+              const bool grow = (top - m[h][0]) * c > kGrow;
+              if (__any_sync(kFull, grow)) {
+                const float f = grow ? ex2((m[h][0] - top) * c) : 1.f;
+                if (grow) m[h][0] = top;
+                l[h][0] *= f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float fe = __shfl_sync(kFull, f, e);
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) of[h * 4 + e][y] *= fe;
+                }
+              }
+              const float p = ex2(fmaf(s, c, -(m[h][0] == -INFINITY ? 0.f : m[h][0] * c)));
+              l[h][0] += p;
+#pragma unroll
+              for (int i = 0; i < PASS; ++i) {
+                uint4 w = lds128(vs + (i * RPP + half) * C::ROW + li * 16);
+                if (i * RPP + half >= left) w = make_uint4(0, 0, 0, 0);  // 0 * NaN is not 0
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float pe_ = __shfl_sync(kFull, p, half * LPR + i * 4 + e);
+                  of[h * 4 + e][0] = fmaf(pe_, __uint_as_float(w.x), of[h * 4 + e][0]);
+                  of[h * 4 + e][1] = fmaf(pe_, __uint_as_float(w.y), of[h * 4 + e][1]);
+                  of[h * 4 + e][2] = fmaf(pe_, __uint_as_float(w.z), of[h * 4 + e][2]);
+                  of[h * 4 + e][3] = fmaf(pe_, __uint_as_float(w.w), of[h * 4 + e][3]);
+                }
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh.empty[slot]));
+        }
+
+        // ---- the piece: the warps' states merged, MH heads at a time
+        const bool alone = cut.holder(u.begin) == cut.holder(u.end - 1);  // the unit's only piece
+        float* const slot = a.partials + (place + b * H_kv + g) * int64_t(G) * (D + 2);
+#pragma unroll
+        for (int h0 = 0; h0 < C::HEADS; h0 += C::MH) {
+          if (h0 >= G) break;
+          float* const mine = merge + warp * C::MH * C::MROW;
+          if constexpr (!F32) {
+            const int h = h0 / 8;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float t = l[h][e];
+#pragma unroll
+              for (int w = 4; w < 32; w <<= 1) t += __shfl_xor_sync(kFull, t, w);
+              const int at = h * 8 + 2 * (lane & 3) + e - h0;  // this lane's head
+              if (at < 0 || at >= C::MH) continue;
+              float* const row = mine + at * C::MROW;
+              if (lane < 4) row[D] = m[h][e], row[D + 1] = t;
+#pragma unroll
+              for (int kk = 0; kk < KS; ++kk) {
+                row[kk * 16 + (lane >> 2)] = o[kk][h][e];
+                row[kk * 16 + 8 + (lane >> 2)] = o[kk][h][2 + e];
+              }
+            }
+          } else {
+            const int h = h0 / 4;
+            float t = l[h][0];
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) t += __shfl_xor_sync(kFull, t, w);
+            if (lane < 4) mine[lane * C::MROW + D] = m[h][0], mine[lane * C::MROW + D + 1] = t;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                if (RPP == 2) of[h * 4 + e][y] += __shfl_xor_sync(kFull, of[h * 4 + e][y], 16);
+                if (half == 0) mine[e * C::MROW + li * 4 + y] = of[h * 4 + e][y];
+              }
+            }
+          }
+          attend_sync();
+          if (tid < C::MH * kWarps) {
+            // factors that bring the warps' states to a common maximum
+            const int h = tid / kWarps, w = tid % kWarps;
+            const float* const st = merge + (w * C::MH + h) * C::MROW + D;
+            const float m_ = st[0], l_ = st[1];
+            float M = m_;
+#pragma unroll
+            for (int y = 1; y < kWarps; y <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, y));
+            // (a warp that saw nothing, or only scores of -infinity, adds nothing)
+            const bool none = m_ == -INFINITY && l_ == 0.f;
+            const float f = none ? 0.f : ex2((m_ - M) * c);
+            float L = none ? 0.f : f * l_;
+#pragma unroll
+            for (int y = 1; y < kWarps; y <<= 1) L += __shfl_xor_sync(kFull, L, y);
+            sh.factor[w][h] = none ? -1.f : f;
+            if (w == 0) sh.top[h] = M, sh.sum[h] = L;
+          }
+          attend_sync();
+          for (int i = tid; i < min(C::MH, G - h0) * D; i += kThreads) {
+            const int h = i / D, d = i - h * D;
+            float O = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              const float f = sh.factor[w][h];
+              O += f == -1.f ? 0.f : f * merge[(w * C::MH + h) * C::MROW + d];
+            }
+            const float M = sh.top[h], L = sh.sum[h];
+            if (alone) {
+              a.out[qrow + (h0 + h) * D + d] = L == 0.f ? 0.f : O / L;
+              if (d == 0 && a.lse) a.lse[qrow / D + h0 + h] = (M * c + log2f(L)) * 0.6931471805599453f;
+            } else {
+              float* const p = slot + (h0 + h) * (D + 2);
+              p[d] = O;
+              if (d == 0) p[D] = M, p[D + 1] = L;
+            }
+          }
+          attend_sync();
         }
       }
+    }
+    }
+  }
+
+// Joins the pieces of each unit that has several, in their order:
+//   out = sum_w f_w o_w / sum_w f_w l_w,  f_w = 2^(c (m_w - max m)).
+// Few pieces: a thread for each output.  More than 8: 32 outputs a CTA, the pieces
+// dealt over its warps, and the warps' sums joined.  Bound by the latency of two or
+// three reads from L2.
+struct Joined {
+  float m = -INFINITY, l = 0.f, o = 0.f;
+  // N pieces from `p` on, `step` floats apart, of which `n` are there; output d
+  template <int N>
+  __device__ __forceinline__ void add(const float* p, int64_t step, int n, int d, int D, float c) {
+    float mv[N], lv[N], ov[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      mv[e] = e < n ? __ldcg(p + e * step + D) : -INFINITY;
+      lv[e] = e < n ? __ldcg(p + e * step + D + 1) : 0.f;
+      ov[e] = e < n ? __ldcg(p + e * step + d) : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) add(mv[e], lv[e], ov[e], c);
+  }
+  __device__ __forceinline__ void add(float m_, float l_, float o_, float c) {
+    if (m_ == -INFINITY && l_ == 0.f) return;  // saw only scores of -infinity, or nothing
+    const float top = fmaxf(m, m_), f = ex2((m - top) * c), f_ = ex2((m_ - top) * c);
+    const bool none = m == -INFINITY && l == 0.f;
+    l = (none ? 0.f : f * l) + f_ * l_;
+    o = (none ? 0.f : f * o) + f_ * o_;
+    m = top;
+  }
+  __device__ __forceinline__ void put(const PagedAttnArgs& a, int64_t qrow, int h, int d, int D, float c) const {
+    a.out[qrow + h * D + d] = l == 0.f ? 0.f : o / l;
+    if (d == 0 && a.lse) a.lse[qrow / D + h] = (m * c + log2f(l)) * 0.6931471805599453f;
+  }
+};
+
+template <int TR, int D>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int grid) {
+  constexpr int FEW = 8;
+  __shared__ Line ln;
+  __shared__ float part[3][kWarps][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const PagedGeo& geo = a.geo;
+  const int B = geo.B, H_kv = geo.H_kv, G = a.G;
+  const float c = a.scale_log2;
+  pdl_launch();
+  pdl_wait();
+  scan_lengths<TR>(geo, ln, false);
+  const Cut cut(ln.pre[B] * H_kv, grid);
+  const int64_t step = int64_t(G) * (D + 2);
+  for (int unit = blockIdx.x; unit < B * H_kv; unit += gridDim.x) {
+    const int b = unit / H_kv, g = unit - b * H_kv;
+    const long long nt = ln.pre[b + 1] - ln.pre[b], begin = ln.pre[b] * H_kv + g * nt;
+    if (nt == 0) continue;
+    const int first = cut.holder(begin), pieces = cut.holder(begin + nt - 1) - first + 1;
+    if (pieces == 1) continue;
+    const int64_t qrow = (int64_t(b) * a.H_q + int64_t(g) * G) * D;
+    const float* const p = a.partials + (first + unit) * step;
+    if (pieces <= FEW) {
+      for (int i = blockIdx.y * kThreads + tid; i < G * D; i += gridDim.y * kThreads) {
+        const int h = i / D, d = i - h * D;
+        Joined j;
+        j.add<FEW>(p + h * (D + 2), step, pieces, d, D, c);
+        j.put(a, qrow, h, d, D, c);
+      }
+      continue;
+    }
+    for (int y = blockIdx.y; y < G * (D / 32); y += gridDim.y) {
+      const int h = y / (D / 32), d = y % (D / 32) * 32 + lane;
+      // warp w takes the w-th eighth of the pieces
+      const int share = (pieces + kWarps - 1) / kWarps, w1 = min(pieces, (warp + 1) * share);
+      Joined j;
+      for (int w = warp * share; w < w1; w += FEW) j.add<FEW>(p + h * (D + 2) + w * step, step, w1 - w, d, D, c);
+      part[0][warp][lane] = j.m;
+      part[1][warp][lane] = j.l;
+      part[2][warp][lane] = j.o;
+      __syncthreads();
+      if (warp == 0) {
+        j = Joined();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) j.add(part[0][w][lane], part[1][w][lane], part[2][w][lane], c);
+        j.put(a, qrow, h, d, D, c);
+      }
+      __syncthreads();
     }
   }
 }
@@ -571,8 +824,25 @@ cudaError_t launch_t(const PagedAttnArgs& a, int grid, cudaStream_t st) {
   auto* const kernel = paged_attn_kernel<T, D, NT, LD>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, C::SMEM, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kAllThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e2 = cudaLaunchKernelEx(&cfg, kernel, a);
+  if (e2 != cudaSuccess) return e2;
+  // a CTA for each unit, and for each 32 outputs of it while that is no more
+  // than four CTAs to an SM
+  const int units = a.geo.B * a.geo.H_kv, most = 4 * grid, y = a.G * (D / 32);
+  cfg.gridDim = dim3(units < most ? units : most, units >= most ? 1 : most / units < y ? most / units : y);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::TR, D>, a, grid);
 }
 
 template <int D, int NT>
