@@ -160,8 +160,14 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+# (torch.cuda.current_stream() builds a Stream object: 2.9 us a call against 0.1)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -297,15 +303,15 @@ def sfi_fast_attn_noalloc(layout: Layout, prm: sfi_params, q, k, v, idx, count, 
         _ptr(out), _stream(stream)))
 
 
-def _want(name: str, t: torch.Tensor, shape, dtype: torch.dtype, device: torch.device,
-          inner: int = 0) -> torch.Tensor:
-    """Refuse a tensor of another shape, type or device; its last ``inner`` dimensions must be
-    dense (0: all of them), and ``device`` must be the current one, where the kernels run."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+def _want(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device,
+          inner: bool = False) -> torch.Tensor:
+    """Refuse a tensor of another shape, type or device, or one that is not dense (with
+    ``inner``: not dense behind its first dimension)."""
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} lies on {t.device}, the layout on {device}")
-    if not (t.is_contiguous() if inner == 0 else t.numel() == 0 or t[0].is_contiguous()):
+    if not t.is_contiguous() and not (inner and t[0].is_contiguous()):
         raise ValueError(f"{name} must be dense{' behind its first dimension' if inner else ''}")
     return t
 
@@ -357,10 +363,10 @@ def sfi_prefill_attn(layout: PackedLayout, q, k, v, out, lse_out=None, ws=None, 
     L, c = layout, sfi_packed_layout.from_buffer_copy(layout._c)
     _here(L.device, stream)
     rq, rk = (L.total_q, L.n_q_heads, L.head_dim), (L.total_k, L.n_kv_heads, L.head_dim)
-    _want("q", q, rq, L.dtype, L.device, 2)
-    _want("k", k, rk, L.dtype, L.device, 2)
-    _want("v", v, rk, L.dtype, L.device, 2)
-    _want("out", out, rq, L.dtype, L.device, 2)
+    _want("q", q, rq, L.dtype, L.device, True)
+    _want("k", k, rk, L.dtype, L.device, True)
+    _want("v", v, rk, L.dtype, L.device, True)
+    _want("out", out, rq, L.dtype, L.device, True)
     if lse_out is not None:
         _want("lse_out", lse_out, rq[:2], torch.float32, L.device)
     # (a row stride only means something where there is a second row)
@@ -390,25 +396,24 @@ class PagedLayout:
         self.n_q_heads, self.n_kv_heads, self.head_dim, self.dtype = n_q_heads, n_kv_heads, head_dim, dtype
         self.page_size, self.n_pages, self.page_stride = page_size, n_pages, page_stride
         self.page_table, self.len = page_table, len
+        self._pool_shape = (n_pages, n_kv_heads, page_size, head_dim)
+        self._page_strides = (page_size * head_dim, head_dim, 1)
         self.c = sfi_paged_layout(self.B, n_q_heads, n_kv_heads, head_dim, dtype_code(dtype), page_size,
                                   n_pages, self.max_pages, page_stride, page_table.data_ptr(),
                                   len.data_ptr())
 
     def _pool(self, name: str, t: torch.Tensor, layers: int = 0) -> torch.Tensor:
         """Refuse a tensor that is not a pool ([layers,] n_pages, H_kv, page_size, d) of this layout."""
-        page = (self.n_pages, self.n_kv_heads, self.page_size, self.head_dim)
-        want = (layers,) + page if layers else page
-        if t.dtype != self.dtype or tuple(t.shape) != want or t.device != self.device:
+        want = (layers,) + self._pool_shape if layers else self._pool_shape
+        if t.dtype is not self.dtype or t.shape != want or t.device != self.device:
             raise ValueError(f"{name}: expected {self.dtype} {want} on {self.device}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-        d, p = self.head_dim, self.page_size
-        dense = self.n_kv_heads * p * d
+        apart = self.page_stride or self.n_kv_heads * self.page_size * self.head_dim
         strides = t.stride()[-4:]
-        if strides[1:] != (p * d, d, 1) and not t[(0,) * (t.dim() - 3)].is_contiguous():
+        if strides[1:] != self._page_strides and not t[(0,) * (t.dim() - 3)].is_contiguous():
             raise ValueError(f"{name}: a page must be dense")
-        if self.n_pages > 1 and strides[0] != (self.page_stride or dense):
-            raise ValueError(f"{name}: pages lie {strides[0]} elements apart, the layout says "
-                             f"{self.page_stride or dense}")
+        if self.n_pages > 1 and strides[0] != apart:
+            raise ValueError(f"{name}: pages lie {strides[0]} elements apart, the layout says {apart}")
         return t
 
 
@@ -423,14 +428,11 @@ class PageStore:
         self.layers = k.shape[0] if k.dim() == 5 else 0
         self.c = sfi_page_store(_ptr(ref), _ptr(k), _ptr(v), max(1, self.layers),
                                 k.stride(0) if self.layers > 1 else 0)
-        self._for = None
 
     def _check(self, layout: PagedLayout) -> "PageStore":
-        if self._for is not layout:
-            _want("ref", self.ref, (layout.n_pages,), torch.int32, layout.device)
-            layout._pool("k", self.k, self.layers)
-            layout._pool("v", self.v, self.layers)
-            self._for = layout
+        _want("ref", self.ref, (layout.n_pages,), torch.int32, layout.device)
+        layout._pool("k", self.k, self.layers)
+        layout._pool("v", self.v, self.layers)
         return self
 
 
@@ -472,8 +474,8 @@ def sfi_paged_append(layout: PagedLayout, k_new, v_new, k, v, cu_new=None, ws=No
     L = layout
     _here(L.device, stream)
     new = (k_new.shape[0], L.n_kv_heads, L.head_dim)
-    _want("k_new", k_new, new, L.dtype, L.device, 2)
-    _want("v_new", v_new, new, L.dtype, L.device, 2)
+    _want("k_new", k_new, new, L.dtype, L.device, True)
+    _want("v_new", v_new, new, L.dtype, L.device, True)
     L._pool("k", k)
     L._pool("v", v)
     if cu_new is not None:

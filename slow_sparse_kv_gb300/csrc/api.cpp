@@ -64,6 +64,17 @@ int device_sm_count() {
   return cached[dev];
 }
 
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t s = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (s == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return s;
+}
+
 WsPlan plan_workspace(int B, int H_q, int H_kv, int D, int max_len) {
   (void)D;
   const int G = H_q / H_kv;

@@ -32,6 +32,8 @@
 // fp32: CUDA cores, d spread over the lanes, dots by transpose-reduction.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "paged.h"
 
@@ -319,11 +321,26 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, c
 #pragma unroll
         for (int r = 0; r < (LD == kBulk ? TR : 1); ++r) {
           const int pos = t * TR + r;
-          page[r] = mine && pos < n ? row[pos / P] : 0;
+          page[r] = mine && pos < n ? row[pos / P] : 0;  // (fp32: mostly the same entry)
           if (page[r] < 0 || page[r] >= geo.n_pages) bad = true, page[r] = 0;
         }
         if (bad) set_status(geo.status, SFI_DEV_BAD_INDEX);
       }
+      // fp32: the lane's rows, and where they go on in another page
+      int rows = 0, in0 = 0;
+      uint32_t starts = 0;
+      if (LD == kBulk) {
+        rows = min(TR, n - t * TR);
+        in0 = t * TR % P;
+        int in = in0;
+#pragma unroll
+        for (int r = 1; r < TR; ++r) {
+          in = in + 1 == P ? 0 : in + 1;
+          if (in == 0 && r < rows) starts |= 1u << r;
+        }
+      }
+      const int64_t at0 = page[0] * geo.page_stride + (int64_t(u.g) * P + in0) * D;
+      const int row0 = LD == kTma ? int(page[0] * (geo.page_stride / D) + u.g * P + t * TR % P) : 0;
       const int count = int(min(32LL, (to - x0 + kProducers - 1) / kProducers));
       for (int i = 0; i < count && ok; ++i) {
         const long long xi = x0 + kProducers * i;
@@ -336,24 +353,25 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, c
         const uint32_t dst = ring + slot * 2 * C::HALF, bar = smem_addr(&sh.full[slot]);
         if constexpr (LD == kTma) {
           if (lane == i) {
-            const int at = int(page[0] * (geo.page_stride / D) + u.g * P + t * TR % P);
             mbar_arrive_expect_tx(bar, 2 * C::HALF);
-            tma_load_3d(dst, &a.tmk, 0, at, 0, bar);
-            tma_load_3d(dst + C::HALF, &a.tmv, 0, at, 0, bar);
+            tma_load_3d(dst, &a.tmk, 0, row0, 0, bar);
+            tma_load_3d(dst + C::HALF, &a.tmv, 0, row0, 0, bar);
           }
         } else if constexpr (LD == kBulk) {
           if (lane == i) {
             // runs of rows that lie in one page
-            const int rows = min(TR, n - t * TR);
             mbar_arrive_expect_tx(bar, uint32_t(rows) * 2 * C::ROW);
+            const uint32_t bytes = uint32_t(min(P - in0, rows)) * C::ROW;
+            bulk_load(dst, kp + at0, bytes, bar);
+            bulk_load(dst + C::HALF, vp + at0, bytes, bar);
+            if (starts) {
 #pragma unroll
-            for (int r = 0; r < TR; ++r) {
-              const int in = (t * TR + r) % P;
-              if (r < rows && (r == 0 || in == 0)) {
-                const uint32_t bytes = uint32_t(min(P - in, rows - r)) * C::ROW;
-                const int64_t at = page[r] * geo.page_stride + (int64_t(u.g) * P + in) * D;
-                bulk_load(dst + r * C::ROW, kp + at, bytes, bar);
-                bulk_load(dst + C::HALF + r * C::ROW, vp + at, bytes, bar);
+              for (int r = 1; r < TR; ++r) {
+                if (!(starts >> r & 1)) continue;
+                const uint32_t more = uint32_t(min(P, rows - r)) * C::ROW;
+                const int64_t at = page[r] * geo.page_stride + int64_t(u.g) * P * D;
+                bulk_load(dst + r * C::ROW, kp + at, more, bar);
+                bulk_load(dst + C::HALF + r * C::ROW, vp + at, more, bar);
               }
             }
           }
@@ -822,7 +840,8 @@ template <typename T, int D, int NT, Load LD>
 cudaError_t launch_t(const PagedAttnArgs& a, int grid, cudaStream_t st) {
   using C = Cfg<T, D, NT>;
   auto* const kernel = paged_attn_kernel<T, D, NT, LD>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<uint64_t> allowed{0};  // the devices on which the kernel may use its shared memory
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::SMEM, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);

@@ -23,6 +23,8 @@
 // tensor memory only then.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "prefill.h"
 #include "tc5.cuh"
 
@@ -597,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 
 template <int D>
 cudaError_t launch_t(const PrefillArgs& a, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(Cfg<D>::SMEM));
+  static std::atomic<uint64_t> allowed{0};  // the devices on which the kernel may use its shared memory
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(prefill_kernel<D>), int(Cfg<D>::SMEM), allowed);
   if (e != cudaSuccess) return e;
   // sum_b ceil(n_b / span) <= total / span + B
   const long long tiles = ((long long)a.total_q / (2 * a.tok) + a.B) * a.H_kv;

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/sfi.h"
 
 namespace sfi {
@@ -149,6 +151,9 @@ cudaError_t launch_fpass(const FpassArgs& a, cudaStream_t st);
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t st);
 
 int device_sm_count();
+// Let `kernel` use `bytes` of dynamic shared memory on the current device, once
+// for each device (`done`: a bit for each).
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 // Pipeline-wait limit given to every attention and verify launch (SM clocks;
 // sfi_set_wait_limit changes it for the whole process).
 long long wait_limit_cycles();
