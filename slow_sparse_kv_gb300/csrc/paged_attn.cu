@@ -36,6 +36,7 @@
 
 #include "common.cuh"
 #include "paged.h"
+#include "pdl.cuh"
 
 namespace sfi {
 namespace {
@@ -233,9 +234,6 @@ __device__ __forceinline__ void scan_lengths(const PagedGeo& geo, Line& ln, bool
   }
   __syncthreads();
 }
-
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ void attend_sync() { named_bar_sync(1, kThreads); }
 
@@ -843,25 +841,14 @@ cudaError_t launch_t(const PagedAttnArgs& a, int grid, cudaStream_t st) {
   static std::atomic<uint64_t> allowed{0};  // the devices on which the kernel may use its shared memory
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::SMEM, allowed);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kAllThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e2 = cudaLaunchKernelEx(&cfg, kernel, a);
+  const cudaError_t e2 = launch_pdl(kernel, dim3(grid), kAllThreads, C::SMEM, st, a);
   if (e2 != cudaSuccess) return e2;
   // a CTA for each unit, and for each 32 outputs of it while that is no more
   // than four CTAs to an SM
   const int units = a.geo.B * a.geo.H_kv, most = 4 * grid, y = a.G * (D / 32);
-  cfg.gridDim = dim3(units < most ? units : most, units >= most ? 1 : most / units < y ? most / units : y);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::TR, D>, a, grid);
+  return launch_pdl(paged_join_kernel<C::TR, D>,
+                    dim3(units < most ? units : most, units >= most ? 1 : most / units < y ? most / units : y),
+                    kThreads, 0, st, a, grid);
 }
 
 template <int D, int NT>

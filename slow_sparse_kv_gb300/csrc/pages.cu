@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "paged.h"
+#include "pdl.cuh"
 
 namespace sfi {
 namespace {
@@ -79,6 +80,8 @@ __global__ void __launch_bounds__(kPlan) extend_kernel(PagedGeo g, int32_t* ref,
   __shared__ long long at[kMaxBatch];
   const int b = threadIdx.x, warp = b >> 5, lane = b & 31;
   const int cap = g.max_pages * g.P;
+  pdl_launch();
+  pdl_wait();
   int n = 0, more = 0, want = 0;
   uint32_t flags = 0;
   if (b < g.B) {
@@ -133,6 +136,8 @@ __global__ void __launch_bounds__(kPlan) fork_kernel(PagedGeo g, int32_t* ref, c
   __shared__ int32_t fresh[kMaxBatch];
   __shared__ int full[kMaxBatch];  // full pages to share, -1: a pair that stays out
   const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
+  pdl_launch();
+  pdl_wait();
   int len = 0, need = 0, s = 0, t = 0;
   uint32_t flags = 0;
   bool in = false;
@@ -181,6 +186,8 @@ __global__ void __launch_bounds__(kPlan) fork_kernel(PagedGeo g, int32_t* ref, c
 }
 
 __global__ void __launch_bounds__(kCopy) free_kernel(PagedGeo g, int32_t* ref, const __grid_constant__ SeqList seqs) {
+  pdl_launch();
+  pdl_wait();
   const int b = seqs.id[blockIdx.x];
   const int n = g.len[b];
   if (n < 0 || n > g.max_pages * g.P) {
@@ -201,6 +208,11 @@ __global__ void __launch_bounds__(kCopy) free_kernel(PagedGeo g, int32_t* ref, c
   }
   __syncthreads();
   if (threadIdx.x == 0) g.len[b] = 0;
+}
+
+// x / y for 0 <= x, 0 < y: in 32 bits where they do (a tenth of the time).
+__device__ __forceinline__ long long div_fast(long long x, long long y) {
+  return ((x | y) >> 32) == 0 ? (long long)(uint32_t(x) / uint32_t(y)) : x / y;
 }
 
 // Bytes [0, n) from src to dst (both 16-byte aligned), by one CTA.
@@ -231,11 +243,14 @@ __device__ __forceinline__ void copy_page_item(const PageMove& mv, int bytes, in
 // The partly filled pages of forks: job (source, new page, rows); rows of one
 // head are one run.
 __global__ void __launch_bounds__(kCopy) fork_copy_kernel(const __grid_constant__ PageMove mv, const int4* jobs, int n) {
+  pdl_launch();
+  pdl_wait();
   const int slices = (mv.P * mv.row_bytes + kSlice - 1) / kSlice;
   const long long per = (long long)mv.n_layers * 2 * mv.H_kv * slices, items = per * n;
   for (long long x = blockIdx.x; x < items; x += gridDim.x) {
-    const int4 job = jobs[x / per];
-    long long y = x % per;
+    const long long i = div_fast(x, per);
+    const int4 job = jobs[i];
+    uint32_t y = uint32_t(x - i * per);
     const int sl = int(y % slices);
     y /= slices;
     const int h = int(y % mv.H_kv);
@@ -250,14 +265,16 @@ __global__ void __launch_bounds__(kCopy) fork_copy_kernel(const __grid_constant_
 
 __global__ void __launch_bounds__(kCopy) page_copy_kernel(const __grid_constant__ PageMove mv, const int32_t* src,
                                                           const int32_t* dst, int n) {
+  pdl_launch();
+  pdl_wait();
   const int bytes = mv.H_kv * mv.P * mv.row_bytes, slices = (bytes + kSlice - 1) / kSlice;
   const int per = mv.n_layers * 2 * slices;
   for (long long x = blockIdx.x; x < (long long)per * n; x += gridDim.x) {
-    const int i = int(x / per), from = src[i], to = dst[i];
+    const int i = int(div_fast(x, per)), from = src[i], to = dst[i];
     if (from < 0 || from >= mv.n_pages || to < 0 || to >= mv.n_pages) {
       if (threadIdx.x == 0) set_status(mv.status, SFI_DEV_BAD_INDEX);
     } else if (from != to) {
-      copy_page_item(mv, bytes, slices, from, to, int(x % per));
+      copy_page_item(mv, bytes, slices, from, to, int(x - (long long)i * per));
     }
   }
 }
@@ -269,6 +286,8 @@ __global__ void __launch_bounds__(kCopy) page_copy_kernel(const __grid_constant_
 __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const int32_t* ref, int n_pages, int chunk, int32_t* map,
                                                              int32_t* holes, int32_t* moved, int32_t* n_moved) {
   __shared__ long long part[32];
+  pdl_launch();
+  pdl_wait();
   const int lo = blockIdx.x * chunk, hi = min(lo + chunk, n_pages);
   int all = 0, before = 0;
   for (int p = threadIdx.x; p < n_pages; p += kPlan) {
@@ -307,6 +326,8 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const int32_t* ref,
 __global__ void __launch_bounds__(kCopy) compact_kernel(const __grid_constant__ PageMove mv, PagedGeo g, int32_t* ref,
                                                         int32_t* new_id, const int32_t* map, const int32_t* holes,
                                                         const int32_t* moved, const int32_t* n_moved) {
+  pdl_launch();
+  pdl_wait();
   const int n = *n_moved;
   const long long tid = (long long)blockIdx.x * kCopy + threadIdx.x, all = (long long)gridDim.x * kCopy;
   for (long long i = tid; i < n; i += all) {
@@ -336,14 +357,16 @@ __global__ void __launch_bounds__(kCopy) compact_kernel(const __grid_constant__ 
   const int bytes = mv.H_kv * mv.P * mv.row_bytes, slices = (bytes + kSlice - 1) / kSlice;
   const int per = mv.n_layers * 2 * slices;
   for (long long x = blockIdx.x; x < (long long)per * n; x += gridDim.x) {
-    const int i = int(x / per);
-    copy_page_item(mv, bytes, slices, moved[i], holes[i], int(x % per));
+    const int i = int(div_fast(x, per));
+    copy_page_item(mv, bytes, slices, moved[i], holes[i], int(x - (long long)i * per));
   }
 }
 
 // New rows into their pages: a warp takes one token's K and V.
 __global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ AppendArgs a) {
   const PagedGeo& g = a.geo;
+  pdl_launch();
+  pdl_wait();
   const int cap = g.max_pages * g.P;
   if (blockIdx.x == 0) {
     // every sequence's rows and length, once
@@ -412,28 +435,23 @@ long long page_slices(const PageMove& mv) {
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
-  append_kernel<<<(a.total + kCopy / 32 - 1) / (kCopy / 32), kCopy, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(append_kernel, dim3((a.total + kCopy / 32 - 1) / (kCopy / 32)), kCopy, 0, st, a);
 }
 
 cudaError_t launch_extend(const PagedGeo& g, int32_t* ref, const int32_t* n_new, int32_t* fresh, cudaStream_t st) {
-  extend_kernel<<<1, kPlan, 0, st>>>(g, ref, n_new, fresh);
-  return cudaGetLastError();
+  return launch_pdl(extend_kernel, dim3(1), kPlan, 0, st, g, ref, n_new, fresh);
 }
 
 cudaError_t launch_fork(const PagedGeo& g, int32_t* ref, const SeqList& src, const SeqList& dst, int n,
                         const PageMove& mv, int4* jobs, cudaStream_t st) {
-  fork_kernel<<<1, kPlan, 0, st>>>(g, ref, src, dst, n, jobs);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(fork_kernel, dim3(1), kPlan, 0, st, g, ref, src, dst, n, jobs);
   if (e != cudaSuccess) return e;
   const long long slices = ((long long)mv.P * mv.row_bytes + kSlice - 1) / kSlice;
-  fork_copy_kernel<<<copy_grid(slices * mv.H_kv * 2 * mv.n_layers * n), kCopy, 0, st>>>(mv, jobs, n);
-  return cudaGetLastError();
+  return launch_pdl(fork_copy_kernel, dim3(copy_grid(slices * mv.H_kv * 2 * mv.n_layers * n)), kCopy, 0, st, mv, jobs, n);
 }
 
 cudaError_t launch_free(const PagedGeo& g, int32_t* ref, const SeqList& seqs, int n, cudaStream_t st) {
-  free_kernel<<<n, kCopy, 0, st>>>(g, ref, seqs);
-  return cudaGetLastError();
+  return launch_pdl(free_kernel, dim3(n), kCopy, 0, st, g, ref, seqs);
 }
 
 cudaError_t launch_compact(const PagedGeo& g, int32_t* ref, int32_t* new_id, const PageMove& mv, int32_t* map,
@@ -441,16 +459,15 @@ cudaError_t launch_compact(const PagedGeo& g, int32_t* ref, int32_t* new_id, con
   // parts of whole rounds of a CTA, at most one CTA to an SM
   const int rounds = (g.n_pages + kPlan - 1) / kPlan, sms = device_sm_count();
   const int chunk = (rounds + sms - 1) / sms * kPlan;
-  compact_plan_kernel<<<(g.n_pages + chunk - 1) / chunk, kPlan, 0, st>>>(ref, g.n_pages, chunk, map, holes, moved, n_moved);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(compact_plan_kernel, dim3((g.n_pages + chunk - 1) / chunk), kPlan, 0, st, ref,
+                                   g.n_pages, chunk, map, holes, moved, n_moved);
   if (e != cudaSuccess) return e;
-  compact_kernel<<<copy_grid(page_slices(mv) * g.n_pages), kCopy, 0, st>>>(mv, g, ref, new_id, map, holes, moved, n_moved);
-  return cudaGetLastError();
+  return launch_pdl(compact_kernel, dim3(copy_grid(page_slices(mv) * g.n_pages)), kCopy, 0, st, mv, g, ref, new_id, map,
+                    holes, moved, n_moved);
 }
 
 cudaError_t launch_page_copy(const PageMove& mv, const int32_t* src, const int32_t* dst, int n, cudaStream_t st) {
-  page_copy_kernel<<<copy_grid(page_slices(mv) * n), kCopy, 0, st>>>(mv, src, dst, n);
-  return cudaGetLastError();
+  return launch_pdl(page_copy_kernel, dim3(copy_grid(page_slices(mv) * n)), kCopy, 0, st, mv, src, dst, n);
 }
 
 }  // namespace sfi

@@ -25,6 +25,7 @@
 
 #include <atomic>
 
+#include "pdl.cuh"
 #include "prefill.h"
 #include "tc5.cuh"
 
@@ -240,6 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int span_tok = 2 * a.tok;
 
+  pdl_launch();
+  pdl_wait();
   for (int b = tid; b < a.B; b += kThreads) {
     const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
     const bool ok = q0 >= 0 && q0 <= q1 && q1 <= a.total_q && k0 >= 0 && k0 <= k1 && k1 <= a.total_k;
@@ -605,8 +608,7 @@ cudaError_t launch_t(const PrefillArgs& a, cudaStream_t st) {
   // sum_b ceil(n_b / span) <= total / span + B
   const long long tiles = ((long long)a.total_q / (2 * a.tok) + a.B) * a.H_kv;
   const int grid = int(tiles < device_sm_count() ? tiles : device_sm_count());
-  prefill_kernel<D><<<grid, kThreads, Cfg<D>::SMEM, st>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(prefill_kernel<D>, dim3(grid), kThreads, Cfg<D>::SMEM, st, a);
 }
 
 }  // namespace
