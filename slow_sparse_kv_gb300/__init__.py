@@ -11,6 +11,7 @@ handle, or None for torch's current stream.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_uint32, c_void_p
@@ -487,9 +488,9 @@ def sfi_paged_append(layout: PagedLayout, k_new, v_new, k, v, cu_new=None, ws=No
 
 
 def _ids(v):
-    """A host list of sequences as a C array."""
-    v = [int(x) for x in v]
-    return (c_int32 * max(1, len(v)))(*v), len(v)
+    """A host list of sequences as C ints: (their array, its address, how many)."""
+    ids = array.array("i", v)
+    return ids, ids.buffer_info()[0], len(ids)
 
 
 def sfi_pages_extend(layout: PagedLayout, store: PageStore, n_new=None, ws=None, stream=None):
@@ -506,7 +507,7 @@ def sfi_pages_extend(layout: PagedLayout, store: PageStore, n_new=None, ws=None,
 def sfi_pages_fork(layout: PagedLayout, store: PageStore, src, dst, ws=None, stream=None):
     """The empty sequences dst[i] become copies of src[i] (host lists)."""
     _here(layout.device, stream)
-    (s, n), (d, m) = _ids(src), _ids(dst)
+    (_s, s, n), (_d, d, m) = _ids(src), _ids(dst)
     if n != m:
         raise ValueError(f"{n} sources, but {m} destinations")
     _check("sfi_pages_fork", lib.sfi_pages_fork(
@@ -517,7 +518,7 @@ def sfi_pages_fork(layout: PagedLayout, store: PageStore, src, dst, ws=None, str
 def sfi_pages_free(layout: PagedLayout, store: PageStore, seqs, ws=None, stream=None):
     """The listed sequences (host list) give up their pages."""
     _here(layout.device, stream)
-    s, n = _ids(seqs)
+    _s, s, n = _ids(seqs)
     _check("sfi_pages_free", lib.sfi_pages_free(
         ctypes.byref(layout.c), ctypes.byref(store._check(layout).c), s, n, *_ws(ws, layout.device),
         _stream(stream)))
