@@ -18,10 +18,10 @@ def attend(q, K, V, limit):
     return p @ V[:limit], m + np.log(e.sum()), p @ np.abs(V[:limit]), size
 
 
-def prefill(q, k, v, cu_q, cu_k):
+def prefill(q, k, v, cu_q, cu_k, rows=None):
     """Causal attention over packed prompts: q [T, H_q, d], k, v [T_k, H_kv, d].
     Returns out, lse, and the two error scales of `attend`; rows outside every
-    sequence are NaN."""
+    sequence, and those that are not in `rows` if it is given, are NaN."""
     T, Hq, d = q.shape
     G = Hq // k.shape[1]
     out, scale = np.full((T, Hq, d), np.nan), np.full((T, Hq, d), np.nan)
@@ -30,6 +30,8 @@ def prefill(q, k, v, cu_q, cu_k):
         nq, nk = cu_q[b + 1] - cu_q[b], cu_k[b + 1] - cu_k[b]
         for i in range(nq):
             t = cu_q[b] + i
+            if rows is not None and t not in rows:
+                continue
             for h in range(Hq):
                 K = k[cu_k[b]:cu_k[b + 1], h // G]
                 V = v[cu_k[b]:cu_k[b + 1], h // G]

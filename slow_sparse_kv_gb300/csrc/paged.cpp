@@ -14,8 +14,20 @@
 namespace sfi {
 namespace {
 
-// the status word, the counters of the tiles, and two numbers for each sequence
+// The prompt attention's workspace: the status word, the counters of the tiles, two
+// numbers for each sequence, and where tiles may be cut along their keys, the
+// states of their parts.
 constexpr size_t kPrefillWs = 512 + 8 * kMaxBatch;
+bool may_cut(const sfi_packed_layout* L) {
+  const int span = 2 * (128 / (L->n_q_heads / L->n_kv_heads));
+  // (there are at least total_q / span tiles for each KV head, if the sequences
+  // hold all rows)
+  return L->total_k >= kSplitKeys &&
+         (long long)L->total_q / span * L->n_kv_heads < (long long)kSplitWaves * kPrefillMaxGrid;
+}
+size_t prefill_ws(const sfi_packed_layout* L) {
+  return kPrefillWs + (may_cut(L) ? size_t(kPrefillMaxGrid) * 256 * (L->head_dim + 2) * 4 : 0);
+}
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 bool misaligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
@@ -200,7 +212,7 @@ using namespace sfi;
 extern "C" {
 
 size_t sfi_prefill_attn_workspace_size(const sfi_packed_layout* L) {
-  return check_packed(L) == SFI_OK ? kPrefillWs : 0;
+  return check_packed(L) == SFI_OK ? prefill_ws(L) : 0;
 }
 
 sfi_status sfi_prefill_attn(const sfi_packed_layout* L, const void* q, const void* k, const void* v, void* out,
@@ -213,7 +225,7 @@ sfi_status sfi_prefill_attn(const sfi_packed_layout* L, const void* q, const voi
   if ((s = row_stride("k_stride", L->k_stride, int64_t(L->n_kv_heads) * D, 8, &ks)) != SFI_OK) return s;
   if ((s = row_stride("v_stride", L->v_stride, int64_t(L->n_kv_heads) * D, 8, &vs)) != SFI_OK) return s;
   if ((s = row_stride("out_stride", L->out_stride, int64_t(L->n_q_heads) * D, 8, &os)) != SFI_OK) return s;
-  if ((s = check_workspace(ws, ws_bytes, kPrefillWs)) != SFI_OK) return s;
+  if ((s = check_workspace(ws, ws_bytes, prefill_ws(L))) != SFI_OK) return s;
   if (L->total_q == 0) return SFI_OK;
   if (!q || !out || (L->total_k > 0 && (!k || !v)))
     return fail(SFI_ERR_INVALID_ARG, "q, k, v and out must be set");
@@ -238,6 +250,7 @@ sfi_status sfi_prefill_attn(const sfi_packed_layout* L, const void* q, const voi
   a.next = a.status + 64;
   a.span = reinterpret_cast<int32_t*>(a.status + 128);
   a.lvl = a.span + kMaxBatch;
+  a.partials = may_cut(L) ? reinterpret_cast<float*>(static_cast<char*>(ws) + kPrefillWs) : nullptr;
   a.wait_cycles = wait_limit_cycles();
   bool ok = encode_heads(&a.tmq, q, D, L->n_q_heads, L->total_q, qs, G, a.tok);
   if (L->total_k > 0)  // without keys the kernel loads neither

@@ -62,6 +62,7 @@ struct Tile {
   int k0, nk;  // the sequence's first key row and its number of keys
   int seen;    // keys that the first token sees (may be negative: none, and none for some after it)
   int n[2];    // key blocks of each half
+  int slot;    // where a part of a tile leaves its state, -1: a whole tile
 };
 
 constexpr int kTileReaders = 11;  // loads, MMAs, the cleaning warp, 8 softmax warps
@@ -221,6 +222,7 @@ __device__ __forceinline__ Tile make_tile(const PrefillArgs& a, int g, int seq, 
   t.g = g;
   t.k0 = a.cu_k[seq];
   t.nk = a.cu_k[seq + 1] - t.k0;
+  t.slot = -1;
   t.q0 = q0 + first;
   t.rows = min(span, nq - first);
   t.seen = t.nk - nq + first + 1;
@@ -230,6 +232,59 @@ __device__ __forceinline__ Tile make_tile(const PrefillArgs& a, int g, int seq, 
     t.n[i] = t.rows > i * a.tok ? (max(0, min(t.seen + tokens - 1, t.nk)) + kKeys - 1) / kKeys : 0;
   }
   return t;
+}
+
+// Which tiles are cut along their keys.  A few waves of tiles of about the same
+// length (the next chunks of long prompts, say) leave most SMs idle in the last
+// one: its tiles, the last `tiles` ranks, are then cut into `parts` of at least 4
+// key blocks, so that all SMs get one.  (A whole prompt's last tiles are its short
+// ones and fill the gaps as they are.)
+struct Split {
+  long long total;  // tiles
+  long long first;  // ranks from here on are cut
+  int tiles, parts;
+};
+
+__device__ __forceinline__ Split split_of(const PrefillArgs& a, int grid) {  // one warp
+  Ranks r{a.span, a.lvl, a.B};
+  r.top();
+  Split s;
+  s.total = s.first = (long long)r.from(0) * a.H_kv;
+  s.tiles = 0;
+  s.parts = 1;
+  if (a.partials == nullptr || s.total == 0 || s.total >= kSplitWaves * grid) return s;
+  const int rest = int(s.total % grid);
+  if (rest == 0) return s;
+  int seq = 0, tile = 0;
+  r.find(0, &seq, &tile);
+  const Tile longest = make_tile(a, 0, seq, tile);
+  r.find(int((s.total - 1) / a.H_kv), &seq, &tile);
+  const Tile shortest = make_tile(a, 0, seq, tile);
+  const int most = max(longest.n[0], longest.n[1]), least = max(shortest.n[0], shortest.n[1]);
+  if (s.total > grid && 2 * least < most) return s;
+  const int parts = min(min(kMaxParts, grid / rest), (s.total > grid ? least : most) / 4);
+  if (parts < 2) return s;
+  s.tiles = rest;
+  s.first = s.total - rest;
+  s.parts = parts;
+  return s;
+}
+
+// The part of a tile as a tile of its own, whose keys begin with the part's.
+__device__ __forceinline__ void take_part(Tile& t, int part, int parts, int slot) {
+  const int n = max(t.n[0], t.n[1]), j0 = int((long long)n * part / parts), j1 = int((long long)n * (part + 1) / parts);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) t.n[i] = max(0, min(t.n[i], j1) - j0);
+  t.k0 += j0 * kKeys;
+  t.nk -= j0 * kKeys;
+  t.seen -= j0 * kKeys;
+  t.slot = slot;
+}
+
+// The state of a tile pair's 256 rows: o as [D][256], then m and l.
+template <int D>
+__device__ __forceinline__ float* slot_of(const PrefillArgs& a, int slot) {
+  return a.partials + int64_t(slot) * (2 * kRows * (D + 2));
 }
 
 template <int D>
@@ -410,17 +465,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       __syncwarp();
     } else if (warp == 10) {
       // ---- which tiles: the CTA's own index first, then by a shared counter
-      int rank = blockIdx.x;
+      long long rank = blockIdx.x;
+      const Split split = split_of(a, gridDim.x);
       Ranks ranks{a.span, a.lvl, a.B};
       ranks.top();
-      const long long total = (long long)ranks.from(0) * a.H_kv;
       for (int k = 0;; ++k) {
         Tile t;
         t.rows = 0;
-        if (rank < total) {
+        if (rank < split.first + (long long)split.tiles * split.parts) {
+          // (the parts of a tile have neighbouring ranks)
+          const int cut = rank < split.first ? 0 : int(rank - split.first);
+          const int whole = int(rank < split.first ? rank : split.first + cut / split.parts);
           int seq = 0, tile = 0;
-          ranks.find(rank / a.H_kv, &seq, &tile);
-          t = make_tile(a, rank % a.H_kv, seq, tile);
+          ranks.find(whole / a.H_kv, &seq, &tile);
+          t = make_tile(a, whole % a.H_kv, seq, tile);
+          if (rank >= split.first) take_part(t, cut % split.parts, split.parts, cut);
         }
         if (k > 1 && !__all_sync(kFull, wait_for(&sh.tile_empty[k & 1], (k >> 1) - 1))) break;
         if (lane == 0) {
@@ -429,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
         __syncwarp();
         if (t.rows == 0) break;
-        if (lane == 0) rank = gridDim.x + int(atomicAdd(a.next, 1u));
+        if (lane == 0) rank = gridDim.x + (long long)atomicAdd(a.next, 1u);
         rank = __shfl_sync(kFull, rank, 0);
       }
       // the last CTA to run out leaves the counters at zero
@@ -544,6 +603,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (ok && n_it > 0) ok = __all_sync(kFull, wait_for(&sh.o_full[i], tiles++));
       if (!ok) break;
       tc5::fence_after();
+      if (t.slot >= 0) {
+        // a part of a tile: the state as it is (rows side by side, so that the
+        // lanes' stores are), for the joining kernel
+        float* const st = slot_of<D>(a, t.slot) + i * kRows + r;
+        for (int x = 0; x < (n_it > 0 ? D / 16 : 0); ++x) {
+          uint32_t o[16];
+          tc5::ld16(o_tm + 16 * x, o);
+          tc5::wait_ld();
+          pin(o);
+#pragma unroll
+          for (int y = 0; y < 16; ++y) st[(16 * x + y) * (2 * kRows)] = __uint_as_float(o[y]);
+        }
+        st[D * (2 * kRows)] = m;
+        st[(D + 1) * (2 * kRows)] = l;
+        tc5::fence_before();
+        __syncwarp();
+        if (lane == 0) taken(k);
+        continue;
+      }
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
       const int h = t.g * a.G + r - tt * a.G;
       const int64_t at = int64_t(t.q0) + row;
@@ -600,15 +678,96 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   }
 }
 
+// Joins the parts of the tiles that were cut, in order:
+//   out = sum_w f_w o_w / sum_w f_w l_w,  f_w = 2^(c (m_w - max m)).
+// A CTA takes 32 rows of a tile pair, a lane a row, a warp an eighth of d.
+template <int D>
+__global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant__ PrefillArgs a, int grid) {
+  __shared__ Tile shared_tile;
+  __shared__ int shared_parts;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch();
+  pdl_wait();
+  if (warp == 0) {
+    const Split split = split_of(a, grid);
+    const int parts = int(blockIdx.x) < split.tiles ? split.parts : 0;
+    if (parts > 0) {
+      const long long rank = split.first + blockIdx.x;
+      Ranks ranks{a.span, a.lvl, a.B};
+      ranks.top();
+      int seq = 0, tile = 0;
+      ranks.find(int(rank / a.H_kv), &seq, &tile);
+      const Tile t = make_tile(a, int(rank % a.H_kv), seq, tile);
+      if (lane == 0) shared_tile = t;
+    }
+    if (lane == 0) shared_parts = parts;
+  }
+  __syncthreads();
+  const int parts = shared_parts;
+  if (parts == 0) return;
+  const Tile t = shared_tile;
+  const float c = a.scale_log2;
+  const int at = blockIdx.y * 32 + lane, i = at / kRows, r = at % kRows, tt = r / a.G;
+  const int row = i * a.tok + tt;
+  if (tt >= a.tok || row >= t.rows) return;
+  const float* const p = slot_of<D>(a, blockIdx.x * parts) + at;
+  constexpr int64_t STEP = 2 * kRows * (D + 2);
+  float f[kMaxParts], M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMaxParts; ++w) {
+    f[w] = w < parts ? __ldcg(p + w * STEP + D * (2 * kRows)) : -INFINITY;
+    M = fmaxf(M, f[w]);
+  }
+#pragma unroll
+  for (int w = 0; w < kMaxParts; ++w) {
+    const float l = w < parts ? __ldcg(p + w * STEP + (D + 1) * (2 * kRows)) : 0.f;
+    // (a part that saw no key, or only scores of -infinity, adds nothing)
+    const bool none = f[w] == -INFINITY && l == 0.f;
+    f[w] = none ? -1.f : ex2((f[w] - M) * c);
+    L += none ? 0.f : f[w] * l;
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  constexpr int PER = D / 8;
+  float o[PER];
+#pragma unroll
+  for (int y = 0; y < PER; ++y) o[y] = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMaxParts; ++w) {
+    if (w >= parts || f[w] == -1.f) continue;
+#pragma unroll
+    for (int y = 0; y < PER; ++y) o[y] = fmaf(f[w], __ldcg(p + w * STEP + (warp * PER + y) * (2 * kRows)), o[y]);
+  }
+  const int h = t.g * a.G + r - tt * a.G;
+  const int64_t q = int64_t(t.q0) + row;
+  uint8_t* const dst = static_cast<uint8_t*>(a.out) + 2 * (q * a.out_stride + int64_t(h) * D + warp * PER);
+#pragma unroll
+  for (int y = 0; y < PER; y += 8) {
+    uint4 v;
+    v.x = pack_bf16x2(o[y] * inv, o[y + 1] * inv);
+    v.y = pack_bf16x2(o[y + 2] * inv, o[y + 3] * inv);
+    v.z = pack_bf16x2(o[y + 4] * inv, o[y + 5] * inv);
+    v.w = pack_bf16x2(o[y + 6] * inv, o[y + 7] * inv);
+    *reinterpret_cast<uint4*>(dst + 2 * y) = v;
+  }
+  if (warp == 0 && a.lse) a.lse[q * a.H_q + h] = (M * c + log2f(L)) * 0.6931471805599453f;
+}
+
 template <int D>
 cudaError_t launch_t(const PrefillArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> allowed{0};  // the devices on which the kernel may use its shared memory
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(prefill_kernel<D>), int(Cfg<D>::SMEM), allowed);
   if (e != cudaSuccess) return e;
-  // sum_b ceil(n_b / span) <= total / span + B
-  const long long tiles = ((long long)a.total_q / (2 * a.tok) + a.B) * a.H_kv;
-  const int grid = int(tiles < device_sm_count() ? tiles : device_sm_count());
-  return launch_pdl(prefill_kernel<D>, dim3(grid), kThreads, Cfg<D>::SMEM, st, a);
+  // total / span <= sum_b ceil(n_b / span) <= total / span + B, if the sequences
+  // hold all rows
+  const long long least = (long long)a.total_q / (2 * a.tok) * a.H_kv, most = least + (long long)a.B * a.H_kv;
+  const int sms = device_sm_count() < kPrefillMaxGrid ? device_sm_count() : kPrefillMaxGrid;
+  PrefillArgs b = a;
+  if (least >= (long long)kSplitWaves * sms) b.partials = nullptr;
+  // (which tiles are cut depends on the grid: the SMs' number wherever some may be)
+  const int grid = b.partials != nullptr || most > sms ? sms : int(most);
+  const cudaError_t e2 = launch_pdl(prefill_kernel<D>, dim3(grid), kThreads, Cfg<D>::SMEM, st, b);
+  if (e2 != cudaSuccess || b.partials == nullptr) return e2;
+  return launch_pdl(prefill_join_kernel<D>, dim3(grid, 2 * kRows / 32), 256, 0, st, b, grid);
 }
 
 }  // namespace

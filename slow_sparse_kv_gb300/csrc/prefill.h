@@ -7,6 +7,10 @@
 namespace sfi {
 
 constexpr int kPrefillMaxGroup = 16;  // query heads per KV head, at most
+constexpr int kPrefillMaxGrid = 256;  // CTAs of a launch, at most
+constexpr int kMaxParts = 8;          // parts that a tile is cut into, at most
+constexpr int kSplitWaves = 8;        // waves of tiles below which the last one's may be cut
+constexpr int kSplitKeys = 1024;      // keys in all below which none is
 
 struct PrefillArgs {
   // 3-D maps [row][head][d] of q, k and v, boxes of 64 elements of d with a
@@ -24,6 +28,7 @@ struct PrefillArgs {
   uint32_t* next;  // [2]: next tile, CTAs that ran out; zero between launches
   int32_t* span;   // [B] scratch: CTA tiles of each sequence and KV head
   int32_t* lvl;    // [B] scratch: the level of its first one
+  float* partials;  // [kPrefillMaxGrid][256][d + 2] states of the parts of tiles; null: none is cut
   long long wait_cycles;
 };
 

@@ -30,13 +30,15 @@ def run(sfi, q, k, v, cu_q, cu_k, ws=None):
     return out, lse
 
 
-def check(q, k, v, cu_q, cu_k, out, lse):
-    ref, rl, scale, size = P.prefill(f64(q), f64(k), f64(v), cu_q, cu_k)
+def check(q, k, v, cu_q, cu_k, out, lse, rows=None):
+    ref, rl, scale, size = P.prefill(f64(q), f64(k), f64(v), cu_q, cu_k, rows)
     inside = ~np.isnan(rl)
     assert not (cu_q[-1] > cu_q[0]) or inside.any()
     d = q.shape[2]
     close(f64(out)[inside], ref[inside], bf16_tolerance(ref, scale, size, d)[inside], "out")
     close_lse(f64(lse)[inside], rl[inside], size[inside], d)
+    if rows is not None:
+        return
     # rows of no sequence stay as they were
     assert (f64(out)[~inside] == 7.0).all() and (f64(lse)[~inside] == 7.0).all()
 
@@ -70,6 +72,44 @@ def test_prefill_matches_oracle(sfi, hq, hkv, d, nq, nk):
     check(q, k, v, cu_q, cu_k, out, lse)
     again, lse2 = run(sfi, q, k, v, cu_q, cu_k)
     assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+CUT = [
+    # few tiles over many keys, so that they are cut along the keys and joined
+    (8, 2, 128, [70, 64, 5], [2000, 1500, 3001]),
+    (8, 2, 64, [33, 1], [1025, 4000]),
+    (3, 1, 128, [50], [1700]),
+    (16, 1, 64, [20, 9], [900, 2222]),
+    (4, 1, 128, [1030], None),                      # a whole prompt: some parts see no key of some rows
+    (4, 1, 64, [200, 3, 0, 300], [90, 3, 500, 1111]),  # rows without keys among them
+]
+
+
+@pytest.mark.parametrize("hq,hkv,d,nq,nk", CUT)
+def test_cut_tiles_are_joined(sfi, hq, hkv, d, nq, nk):
+    cu_q, cu_k = offsets(nq), offsets(nk or nq)
+    assert cu_k[-1] >= 1024
+    q = normal((cu_q[-1] + 2, hq, d), BF16, 1)
+    k, v = normal((cu_k[-1] + 3, hkv, d), BF16, 2), normal((cu_k[-1] + 3, hkv, d), BF16, 3)
+    k[cu_k[-1]:], v[cu_k[-1]:] = float("nan"), float("nan")
+    out, lse = run(sfi, q, k, v, cu_q, cu_k)
+    rows = set(range(0, cu_q[-1], 1 if cu_q[-1] < 200 else 13)) | {x for y in cu_q for x in (y - 1, y)}
+    check(q, k, v, cu_q, cu_k, out, lse, rows)
+    assert (out[cu_q[-1]:] == 7.0).all() and (lse[cu_q[-1]:] == 7.0).all()
+    again, lse2 = run(sfi, q, k, v, cu_q, cu_k)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+def test_last_wave_is_cut(sfi):
+    """More tiles of one length than SMs: the last, partly filled wave's are cut (8 KV heads x 25
+    tiles of 64 tokens, 48 of the 200 on a GPU with 152 SMs), the others are not."""
+    hq, hkv, d, nq, nk = 32, 8, 64, 1600, 3400
+    q, k, v = normal((nq, hq, d), BF16, 1), normal((nk, hkv, d), BF16, 2), normal((nk, hkv, d), BF16, 3)
+    out, lse = run(sfi, q, k, v, [0, nq], [0, nk])
+    check(q, k, v, [0, nq], [0, nk], out, lse, set(range(0, nq, 67)) | {0, 63, 64, nq - 1})
+    # the tiles of a call with one head group are all cut: the same within the rounding of both
+    one, lse1 = run(sfi, q[:, :4].contiguous(), k[:, :1].contiguous(), v[:, :1].contiguous(), [0, nq], [0, nk])
+    check(q[:, :4], k[:, :1], v[:, :1], [0, nq], [0, nk], one, lse1, set(range(0, nq, 31)))
 
 
 def test_growing_scores_rescale(sfi):
