@@ -50,7 +50,7 @@ struct Cfg {
   static constexpr int HALVES = D / 64;
   static constexpr uint32_t TILE = kRows * 128 * HALVES;  // bytes of a 128-row tile
   static constexpr int STAGES = D == 128 ? 4 : 6;         // K and V blocks in flight
-  static constexpr uint32_t OUT = 8 * 32 * 128;           // 32 rows of 64 outputs for each softmax warp
+  static constexpr uint32_t OUT = 8 * 2 * 32 * 64;        // twice 32 rows of 32 outputs for each softmax warp
   static constexpr uint32_t SMEM = 1024 + (2 + STAGES) * TILE + OUT;
 };
 
@@ -99,6 +99,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -168,24 +175,43 @@ __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
 // neighbours.  A CTA asks for growing ranks, so the walk goes on from where it
 // stood.
 struct Ranks {
-  const int* span;
-  const int* lvl;
-  int B;
+  const PrefillArgs& a;
+  // (up to 32 sequences stay in registers, a lane each: reading them back from
+  // memory for every step of the search took 10 to 15 us at a kernel's start)
+  int span1 = 0, lvl1 = 0;
   int level, before, here;  // the level it stands at, tiles above it and on it
 
-  // tiles on levels tau and above
-  __device__ __forceinline__ int from(int tau) const {
-    int n = 0;
-    for (int b = threadIdx.x & 31; b < B; b += 32) n += min(max(lvl[b] + span[b] - tau, 0), span[b]);
-    return __reduce_add_sync(kFull, n);
-  }
-  __device__ __forceinline__ void top() {
+  // Stands above the highest level.
+  __device__ __forceinline__ explicit Ranks(const PrefillArgs& a_) : a(a_) {
+    const int lane = threadIdx.x & 31;
+    if (a.B <= 32 && lane < a.B) sequence(a, lane, &span1, &lvl1);
     int t = 0;
-    for (int b = threadIdx.x & 31; b < B; b += 32) t = max(t, span[b] > 0 ? lvl[b] + span[b] : 0);
+    each([&](int, int span, int lvl) { t = max(t, span > 0 ? lvl + span : 0); });
     level = __reduce_max_sync(kFull, t);
     before = here = 0;
   }
-  // sequence and tile of a rank below from(0)
+  // CTA tiles and first level of sequence b; false if its offsets are out of order
+  static __device__ __forceinline__ bool sequence(const PrefillArgs& a, int b, int* span, int* lvl) {
+    const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1], tokens = 2 * a.tok;
+    const bool ok = q0 >= 0 && q0 <= q1 && q1 <= a.total_q && k0 >= 0 && k0 <= k1 && k1 <= a.total_k;
+    *span = ok ? (q1 - q0 + tokens - 1) / tokens : 0;
+    *lvl = ok ? max(0, (k1 - k0) - (q1 - q0)) / tokens : 0;
+    return ok;
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    const int lane = threadIdx.x & 31;
+    if (a.B <= 32) f(lane, span1, lvl1);
+    else
+      for (int b = lane; b < a.B; b += 32) f(b, a.span[b], a.lvl[b]);
+  }
+  // tiles on levels tau and above
+  __device__ __forceinline__ int from(int tau) const {
+    int n = 0;
+    each([&](int, int span, int lvl) { n += min(max(lvl + span - tau, 0), span); });
+    return __reduce_add_sync(kFull, n);
+  }
+  // sequence and tile of a rank below from(0), for growing ranks
   __device__ __forceinline__ void find(int rank, int* seq, int* tile) {
     const int lane = threadIdx.x & 31;
     if (rank >= before + here) {
@@ -202,12 +228,14 @@ struct Ranks {
       here = from(lo) - before;
     }
     int left = rank - before;
-    for (int b0 = 0; b0 < B; b0 += 32) {
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
-      const uint32_t in = __ballot_sync(kFull, b < B && lvl[b] <= level && level < lvl[b] + span[b]);
+      const int span = a.B <= 32 ? span1 : b < a.B ? a.span[b] : 0, lvl = a.B <= 32 ? lvl1 : b < a.B ? a.lvl[b] : 0;
+      const uint32_t in = __ballot_sync(kFull, lvl <= level && level < lvl + span);
       if (left < __popc(in)) {
-        *seq = b0 + __fns(in, 0, left + 1);
-        *tile = level - lvl[*seq];
+        const int at = __fns(in, 0, left + 1);
+        *seq = b0 + at;
+        *tile = level - __shfl_sync(kFull, lvl, at);
         return;
       }
       left -= __popc(in);
@@ -246,8 +274,7 @@ struct Split {
 };
 
 __device__ __forceinline__ Split split_of(const PrefillArgs& a, int grid) {  // one warp
-  Ranks r{a.span, a.lvl, a.B};
-  r.top();
+  Ranks r(a);
   Split s;
   s.total = s.first = (long long)r.from(0) * a.H_kv;
   s.tiles = 0;
@@ -294,18 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   __shared__ Shared sh;
   const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int span_tok = 2 * a.tok;
 
-  pdl_launch();
-  pdl_wait();
-  for (int b = tid; b < a.B; b += kThreads) {
-    const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
-    const bool ok = q0 >= 0 && q0 <= q1 && q1 <= a.total_q && k0 >= 0 && k0 <= k1 && k1 <= a.total_k;
-    if (!ok && blockIdx.x == 0) set_status(a.status, SFI_DEV_LEN_OVER_CAP);
-    // (every CTA writes the same values and reads its own)
-    a.span[b] = ok ? (q1 - q0 + span_tok - 1) / span_tok : 0;
-    a.lvl[b] = ok ? max(0, (k1 - k0) - (q1 - q0)) / span_tok : 0;
-  }
   if (warp == 9) {
     if (lane == 0) {
       sh.abort = 0;
@@ -330,6 +346,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     tc5::alloc(smem_addr(&sh.tmem), 512);
     tc5::fence_before();
   }
+  pdl_launch();
+  pdl_wait();
+  if (blockIdx.x == 0 || a.B > 32)
+    for (int b = tid; b < a.B; b += kThreads) {
+      int span, lvl;
+      const bool ok = Ranks::sequence(a, b, &span, &lvl);
+      if (!ok && blockIdx.x == 0) set_status(a.status, SFI_DEV_LEN_OVER_CAP);
+      // (every CTA writes the same values and reads its own)
+      if (a.B > 32) a.span[b] = span, a.lvl[b] = lvl;
+    }
   __syncthreads();
   tc5::fence_after();
   const uint32_t tmem = sh.tmem;
@@ -467,8 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       // ---- which tiles: the CTA's own index first, then by a shared counter
       long long rank = blockIdx.x;
       const Split split = split_of(a, gridDim.x);
-      Ranks ranks{a.span, a.lvl, a.B};
-      ranks.top();
+      Ranks ranks(a);
       for (int k = 0;; ++k) {
         Tile t;
         t.rows = 0;
@@ -627,41 +652,54 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const int64_t at = int64_t(t.q0) + row;
       // where this thread's row goes, -1: nowhere
       const int64_t to = valid ? 2 * (at * a.out_stride + int64_t(h) * D) : -1;
+      const bool none = limit == 0;  // no key: nothing was written for the row, or for others' sake only
+      // Out through shared memory, 32 columns at a time in two buffers, by TMA where
+      // the warp's 32 rows are whole tokens of the tile, and else with 4 lanes to 64
+      // bytes.  (Stores from registers, a row to a lane or rows by 8 lanes, hold up
+      // the load/store unit, and with it every wait of the CTA, for 3000 clocks.)
+      const bool whole = 32 % a.G == 0 && __all_sync(kFull, valid);
 #pragma unroll
-      for (int x = 0; x < D / 64; ++x) {
-        // 64 columns at a time through shared memory, so that 8 lanes write 128
-        // bytes of a row (a lane writing its own row holds up the load/store
-        // unit, and with it every wait of the CTA, for ~4000 clocks)
-        const bool none = limit == 0;  // no key: nothing was written for the row, or for others' sake only
+      for (int x = 0; x < D / 32; ++x) {
+        uint32_t o[32];
+        if (n_it > 0) {
+          tc5::ld32(o_tm + 32 * x, o);
+          tc5::wait_ld();
+          pin(o);
+        }
+        const uint32_t buf = out_sm + (x & 1) * 2048;
+        if (lane == 0) {  // the copy that read this buffer last is done
+          if (x < 2) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        }
+        __syncwarp();
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          uint32_t o[32];
-          if (n_it > 0) {
-            tc5::ld32(o_tm + 64 * x + 32 * z, o);
-            tc5::wait_ld();
-            pin(o);
+        for (int y = 0; y < 4; ++y) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = none ? 0u : pack_bf16x2(__uint_as_float(o[8 * y + 2 * e]) * inv, __uint_as_float(o[8 * y + 2 * e + 1]) * inv);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + ((y ^ ((lane >> 1) & 3)) * 16)),
+                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+        if (whole) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&a.tmo, buf, x * 32, t.g * a.G, t.q0 + i * a.tok + (warp & 3) * 32 / a.G);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
+        } else {
+          __syncwarp();
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = none ? 0u : pack_bf16x2(__uint_as_float(o[8 * y + 2 * e]) * inv, __uint_as_float(o[8 * y + 2 * e + 1]) * inv);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             out_sm + lane * 128 + (((4 * z + y) ^ (lane & 7)) * 16)),
-                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                         : "memory");
+            const int rr = y * 8 + (lane >> 2), ch = lane & 3;
+            const int64_t dst = __shfl_sync(kFull, to, rr);
+            const uint4 w = lds128(buf + rr * 64 + ((ch ^ ((rr >> 1) & 3)) * 16));
+            if (dst >= 0) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + dst + 64 * x + 16 * ch) = w;
           }
+          __syncwarp();
         }
-        __syncwarp();
-#pragma unroll 2
-        for (int y = 0; y < 8; ++y) {
-          const int rr = y * 4 + (lane >> 3), ch = lane & 7;
-          const int64_t dst = __shfl_sync(kFull, to, rr);
-          const uint4 w = lds128(out_sm + rr * 128 + ((ch ^ (rr & 7)) * 16));
-          if (dst >= 0) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + dst + 128 * x + 16 * ch) = w;
-        }
-        __syncwarp();
       }
       // (the next tile's first P says that O_i has been read)
       tc5::fence_before();
@@ -669,6 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       __syncwarp();
       if (lane == 0) taken(k);
     }
+    // (shared memory outlives the copies out of it)
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     tc5::fence_before();
   }
   __syncthreads();
@@ -693,8 +733,7 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant
     const int parts = int(blockIdx.x) < split.tiles ? split.parts : 0;
     if (parts > 0) {
       const long long rank = split.first + blockIdx.x;
-      Ranks ranks{a.span, a.lvl, a.B};
-      ranks.top();
+      Ranks ranks(a);
       int seq = 0, tile = 0;
       ranks.find(int(rank / a.H_kv), &seq, &tile);
       const Tile t = make_tile(a, int(rank % a.H_kv), seq, tile);
