@@ -18,6 +18,8 @@ namespace {
 // numbers for each sequence, and where tiles may be cut along their keys, the
 // states of their parts.
 constexpr size_t kPrefillWs = 512 + 8 * kMaxBatch;
+constexpr size_t kCutWs = 256 + kPrefillMaxGrid * 64;  // the cut tiles
+static_assert(sizeof(PrefillTile) <= 64, "kCutWs");
 bool may_cut(const sfi_packed_layout* L) {
   const int span = 2 * (128 / (L->n_q_heads / L->n_kv_heads));
   // (there are at least total_q / span tiles for each KV head, if the sequences
@@ -26,7 +28,7 @@ bool may_cut(const sfi_packed_layout* L) {
          (long long)L->total_q / span * L->n_kv_heads < (long long)kSplitWaves * kPrefillMaxGrid;
 }
 size_t prefill_ws(const sfi_packed_layout* L) {
-  return kPrefillWs + (may_cut(L) ? size_t(kPrefillMaxGrid) * 256 * (L->head_dim + 2) * 4 : 0);
+  return kPrefillWs + (may_cut(L) ? kCutWs + size_t(kPrefillMaxGrid) * 256 * (L->head_dim + 2) * 4 : 0);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -251,7 +253,12 @@ sfi_status sfi_prefill_attn(const sfi_packed_layout* L, const void* q, const voi
   a.next = a.status + 64;
   a.span = reinterpret_cast<int32_t*>(a.status + 128);
   a.lvl = a.span + kMaxBatch;
-  a.partials = may_cut(L) ? reinterpret_cast<float*>(static_cast<char*>(ws) + kPrefillWs) : nullptr;
+  if (may_cut(L)) {
+    char* const cut = static_cast<char*>(ws) + kPrefillWs;
+    a.cut_count = reinterpret_cast<int32_t*>(cut);
+    a.cuts = reinterpret_cast<PrefillTile*>(cut + 256);
+    a.partials = reinterpret_cast<float*>(cut + kCutWs);
+  }
   a.wait_cycles = wait_limit_cycles();
   bool ok = encode_heads(&a.tmq, q, D, L->n_q_heads, L->total_q, qs, G, a.tok);
   if (32 % G == 0) ok = ok && encode_heads(&a.tmo, out, D, L->n_q_heads, L->total_q, os, G, 32 / G, 32);

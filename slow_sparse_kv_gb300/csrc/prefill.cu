@@ -54,16 +54,7 @@ struct Cfg {
   static constexpr uint32_t SMEM = 1024 + (2 + STAGES) * TILE + OUT;
 };
 
-// A pair of 128-row tiles: 2 x 128 / G tokens of one (sequence, KV head).
-struct Tile {
-  int rows;    // tokens it has (0: no tile, the end)
-  int g;       // KV head
-  int q0;      // first query row
-  int k0, nk;  // the sequence's first key row and its number of keys
-  int seen;    // keys that the first token sees (may be negative: none, and none for some after it)
-  int n[2];    // key blocks of each half
-  int slot;    // where a part of a tile leaves its state, -1: a whole tile
-};
+using Tile = PrefillTile;
 
 constexpr int kTileReaders = 11;  // loads, MMAs, the cleaning warp, 8 softmax warps
 
@@ -233,7 +224,9 @@ struct Ranks {
       const int span = a.B <= 32 ? span1 : b < a.B ? a.span[b] : 0, lvl = a.B <= 32 ? lvl1 : b < a.B ? a.lvl[b] : 0;
       const uint32_t in = __ballot_sync(kFull, lvl <= level && level < lvl + span);
       if (left < __popc(in)) {
-        const int at = __fns(in, 0, left + 1);
+        // the lane with `left` set bits below its own
+        const bool me = (in >> lane & 1) && __popc(in & ((1u << lane) - 1)) == left;
+        const int at = __ffs(__ballot_sync(kFull, me)) - 1;
         *seq = b0 + at;
         *tile = level - __shfl_sync(kFull, lvl, at);
         return;
@@ -280,12 +273,13 @@ __device__ __forceinline__ Split split_of(const PrefillArgs& a, int grid) {  // 
   s.tiles = 0;
   s.parts = 1;
   if (a.partials == nullptr || s.total == 0 || s.total >= kSplitWaves * grid) return s;
-  const int rest = int(s.total % grid);
+  // (below 2^31: kSplitWaves * grid)
+  const int rest = int(uint32_t(s.total) % uint32_t(grid));
   if (rest == 0) return s;
   int seq = 0, tile = 0;
   r.find(0, &seq, &tile);
   const Tile longest = make_tile(a, 0, seq, tile);
-  r.find(int((s.total - 1) / a.H_kv), &seq, &tile);
+  r.find(int(uint32_t(s.total - 1) / uint32_t(a.H_kv)), &seq, &tile);
   const Tile shortest = make_tile(a, 0, seq, tile);
   const int most = max(longest.n[0], longest.n[1]), least = max(shortest.n[0], shortest.n[1]);
   if (s.total > grid && 2 * least < most) return s;
@@ -493,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       // ---- which tiles: the CTA's own index first, then by a shared counter
       long long rank = blockIdx.x;
       const Split split = split_of(a, gridDim.x);
+      if (blockIdx.x == 0 && lane == 0 && a.partials != nullptr) a.cut_count[0] = split.tiles, a.cut_count[1] = split.parts;
       Ranks ranks(a);
       for (int k = 0;; ++k) {
         Tile t;
@@ -504,7 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           int seq = 0, tile = 0;
           ranks.find(whole / a.H_kv, &seq, &tile);
           t = make_tile(a, whole % a.H_kv, seq, tile);
-          if (rank >= split.first) take_part(t, cut % split.parts, split.parts, cut);
+          if (rank >= split.first) {
+            if (lane == 0 && cut % split.parts == 0) a.cuts[cut / split.parts] = t;
+            take_part(t, cut % split.parts, split.parts, cut);
+          }
         }
         if (k > 1 && !__all_sync(kFull, wait_for(&sh.tile_empty[k & 1], (k >> 1) - 1))) break;
         if (lane == 0) {
@@ -720,31 +718,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 
 // Joins the parts of the tiles that were cut, in order:
 //   out = sum_w f_w o_w / sum_w f_w l_w,  f_w = 2^(c (m_w - max m)).
-// A CTA takes 32 rows of a tile pair, a lane a row, a warp an eighth of d.
+// A CTA takes 32 rows of a tile pair and 64 columns, a lane a row, a warp 8 columns.
 template <int D>
-__global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant__ PrefillArgs a, int grid) {
-  __shared__ Tile shared_tile;
-  __shared__ int shared_parts;
+__global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant__ PrefillArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch();
   pdl_wait();
-  if (warp == 0) {
-    const Split split = split_of(a, grid);
-    const int parts = int(blockIdx.x) < split.tiles ? split.parts : 0;
-    if (parts > 0) {
-      const long long rank = split.first + blockIdx.x;
-      Ranks ranks(a);
-      int seq = 0, tile = 0;
-      ranks.find(int(rank / a.H_kv), &seq, &tile);
-      const Tile t = make_tile(a, int(rank % a.H_kv), seq, tile);
-      if (lane == 0) shared_tile = t;
-    }
-    if (lane == 0) shared_parts = parts;
-  }
-  __syncthreads();
-  const int parts = shared_parts;
-  if (parts == 0) return;
-  const Tile t = shared_tile;
+  if (int(blockIdx.x) >= a.cut_count[0]) return;
+  const int parts = a.cut_count[1];
+  const Tile t = a.cuts[blockIdx.x];
   const float c = a.scale_log2;
   const int at = blockIdx.y * 32 + lane, i = at / kRows, r = at % kRows, tt = r / a.G;
   const int row = i * a.tok + tt;
@@ -766,29 +748,32 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant
     L += none ? 0.f : f[w] * l;
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  constexpr int PER = D / 8;
+  constexpr int PER = 8;  // columns of a thread
+  const int d = blockIdx.z * 64 + warp * PER;
   float o[PER];
 #pragma unroll
   for (int y = 0; y < PER; ++y) o[y] = 0.f;
 #pragma unroll
-  for (int w = 0; w < kMaxParts; ++w) {
-    if (w >= parts || f[w] == -1.f) continue;
+  for (int w0 = 0; w0 < kMaxParts; w0 += 4) {
+    float v[4][PER];  // 32 reads in flight
 #pragma unroll
-    for (int y = 0; y < PER; ++y) o[y] = fmaf(f[w], __ldcg(p + w * STEP + (warp * PER + y) * (2 * kRows)), o[y]);
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+      for (int y = 0; y < PER; ++y) v[w][y] = w0 + w < parts ? __ldcg(p + (w0 + w) * STEP + (d + y) * (2 * kRows)) : 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+      for (int y = 0; y < PER; ++y) o[y] = f[w0 + w] == -1.f ? o[y] : fmaf(f[w0 + w], v[w][y], o[y]);
   }
   const int h = t.g * a.G + r - tt * a.G;
   const int64_t q = int64_t(t.q0) + row;
-  uint8_t* const dst = static_cast<uint8_t*>(a.out) + 2 * (q * a.out_stride + int64_t(h) * D + warp * PER);
-#pragma unroll
-  for (int y = 0; y < PER; y += 8) {
-    uint4 v;
-    v.x = pack_bf16x2(o[y] * inv, o[y + 1] * inv);
-    v.y = pack_bf16x2(o[y + 2] * inv, o[y + 3] * inv);
-    v.z = pack_bf16x2(o[y + 4] * inv, o[y + 5] * inv);
-    v.w = pack_bf16x2(o[y + 6] * inv, o[y + 7] * inv);
-    *reinterpret_cast<uint4*>(dst + 2 * y) = v;
-  }
-  if (warp == 0 && a.lse) a.lse[q * a.H_q + h] = (M * c + log2f(L)) * 0.6931471805599453f;
+  uint4 v;
+  v.x = pack_bf16x2(o[0] * inv, o[1] * inv);
+  v.y = pack_bf16x2(o[2] * inv, o[3] * inv);
+  v.z = pack_bf16x2(o[4] * inv, o[5] * inv);
+  v.w = pack_bf16x2(o[6] * inv, o[7] * inv);
+  *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + 2 * (q * a.out_stride + int64_t(h) * D + d)) = v;
+  if (d == 0 && a.lse) a.lse[q * a.H_q + h] = (M * c + log2f(L)) * 0.6931471805599453f;
 }
 
 template <int D>
@@ -806,7 +791,7 @@ cudaError_t launch_t(const PrefillArgs& a, cudaStream_t st) {
   const int grid = b.partials != nullptr || most > sms ? sms : int(most);
   const cudaError_t e2 = launch_pdl(prefill_kernel<D>, dim3(grid), kThreads, Cfg<D>::SMEM, st, b);
   if (e2 != cudaSuccess || b.partials == nullptr) return e2;
-  return launch_pdl(prefill_join_kernel<D>, dim3(grid, 2 * kRows / 32), 256, 0, st, b, grid);
+  return launch_pdl(prefill_join_kernel<D>, dim3(grid, 2 * kRows / 32, D / 64), 256, 0, st, b);
 }
 
 }  // namespace
