@@ -336,6 +336,10 @@ sfi_status sfi_fast_attn_noalloc(const sfi_layout* layout, const sfi_params* par
  *  - cu_q and cu_k are ascending; an entry pair that descends or leaves
  *    [0, total_q] ([0, total_k]) sets SFI_DEV_LEN_OVER_CAP and that sequence's
  *    rows are not computed.
+ *  - The same call gives the same bits.  With few query rows over many keys (1024
+ *    or more in all) some rows are computed in up to 8 parts of their keys that
+ *    are joined in fp32; which ones, and so the rounding, depends on the whole
+ *    batch.
  *  - total_q = 0 is a call that does nothing; total_k = 0 (k and v may then be
  *    NULL) gives every row no key.
  * The workspace (sfi_prefill_attn_workspace_size, 0 for invalid arguments)

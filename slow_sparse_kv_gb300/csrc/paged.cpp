@@ -78,12 +78,11 @@ sfi_status check_packed(const sfi_packed_layout* L) {
   return SFI_OK;
 }
 
-// [rows][heads][D] with `stride` elements between rows, boxes of `bd` elements x `bh` heads x `br` rows.
-bool encode_heads(CUtensorMap* m, const void* base, int D, int heads, int rows, int64_t stride, int bh, int br,
-                  int bd = 64) {
+// [rows][heads][D] with `stride` elements between rows, boxes of `bh` heads x `br` rows.
+bool encode_heads(CUtensorMap* m, const void* base, int D, int heads, int rows, int64_t stride, int bh, int br) {
   const uint64_t dims[3] = {uint64_t(D), uint64_t(heads), uint64_t(rows)};
   const uint64_t st[2] = {uint64_t(D) * 2, uint64_t(stride) * 2};
-  const uint32_t box[3] = {uint32_t(bd), uint32_t(bh), uint32_t(br)};
+  const uint32_t box[3] = {64, uint32_t(bh), uint32_t(br)};
   return encode_bf16_3d(m, base, dims, st, box);
 }
 
@@ -261,7 +260,7 @@ sfi_status sfi_prefill_attn(const sfi_packed_layout* L, const void* q, const voi
   }
   a.wait_cycles = wait_limit_cycles();
   bool ok = encode_heads(&a.tmq, q, D, L->n_q_heads, L->total_q, qs, G, a.tok);
-  if (32 % G == 0) ok = ok && encode_heads(&a.tmo, out, D, L->n_q_heads, L->total_q, os, G, 32 / G, 32);
+  if (32 % G == 0) ok = ok && encode_heads(&a.tmo, out, D, L->n_q_heads, L->total_q, os, G, 32 / G);
   if (L->total_k > 0)  // without keys the kernel loads neither
     ok = ok && encode_heads(&a.tmk, k, D, L->n_kv_heads, L->total_k, ks, 1, 128) &&
          encode_heads(&a.tmv, v, D, L->n_kv_heads, L->total_k, vs, 1, 128);

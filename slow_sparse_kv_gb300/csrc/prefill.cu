@@ -50,7 +50,7 @@ struct Cfg {
   static constexpr int HALVES = D / 64;
   static constexpr uint32_t TILE = kRows * 128 * HALVES;  // bytes of a 128-row tile
   static constexpr int STAGES = D == 128 ? 4 : 6;         // K and V blocks in flight
-  static constexpr uint32_t OUT = 8 * 2 * 32 * 64;        // twice 32 rows of 32 outputs for each softmax warp
+  static constexpr uint32_t OUT = 8 * 32 * 128;           // 32 rows of 64 outputs for each softmax warp
   static constexpr uint32_t SMEM = 1024 + (2 + STAGES) * TILE + OUT;
 };
 
@@ -651,50 +651,52 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       // where this thread's row goes, -1: nowhere
       const int64_t to = valid ? 2 * (at * a.out_stride + int64_t(h) * D) : -1;
       const bool none = limit == 0;  // no key: nothing was written for the row, or for others' sake only
-      // Out through shared memory, 32 columns at a time in two buffers, by TMA where
-      // the warp's 32 rows are whole tokens of the tile, and else with 4 lanes to 64
-      // bytes.  (Stores from registers, a row to a lane or rows by 8 lanes, hold up
-      // the load/store unit, and with it every wait of the CTA, for 3000 clocks.)
+      // Out through shared memory, 64 columns at a time, by TMA where the warp's 32
+      // rows are whole tokens of the tile, and else with 8 lanes to 128 bytes.
+      // (Stores from registers, a row to a lane or rows by 8 lanes, hold up the
+      // load/store unit, and with it every wait of the CTA, for 3000 clocks.)
       const bool whole = 32 % a.G == 0 && __all_sync(kFull, valid);
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x) {
-        uint32_t o[32];
-        if (n_it > 0) {
-          tc5::ld32(o_tm + 32 * x, o);
-          tc5::wait_ld();
-          pin(o);
-        }
-        const uint32_t buf = out_sm + (x & 1) * 2048;
-        if (lane == 0) {  // the copy that read this buffer last is done
-          if (x < 2) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        }
-        __syncwarp();
+      for (int x = 0; x < D / 64; ++x) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t w[4];
+        for (int z = 0; z < 2; ++z) {
+          uint32_t o[32];
+          if (n_it > 0) {
+            tc5::ld32(o_tm + 64 * x + 32 * z, o);
+            tc5::wait_ld();
+            pin(o);
+          }
+          if (z == 0) {  // the copy that read the buffer last is done
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+          }
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = none ? 0u : pack_bf16x2(__uint_as_float(o[8 * y + 2 * e]) * inv, __uint_as_float(o[8 * y + 2 * e + 1]) * inv);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + ((y ^ ((lane >> 1) & 3)) * 16)),
-                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                       : "memory");
+          for (int y = 0; y < 4; ++y) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = none ? 0u : pack_bf16x2(__uint_as_float(o[8 * y + 2 * e]) * inv, __uint_as_float(o[8 * y + 2 * e + 1]) * inv);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             out_sm + lane * 128 + (((4 * z + y) ^ (lane & 7)) * 16)),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
+          }
         }
         if (whole) {
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(&a.tmo, buf, x * 32, t.g * a.G, t.q0 + i * a.tok + (warp & 3) * 32 / a.G);
+            tma_store_3d(&a.tmo, out_sm, x * 64, t.g * a.G, t.q0 + i * a.tok + (warp & 3) * 32 / a.G);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         } else {
           __syncwarp();
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int rr = y * 8 + (lane >> 2), ch = lane & 3;
+          for (int y = 0; y < 8; ++y) {
+            const int rr = y * 4 + (lane >> 3), ch = lane & 7;
             const int64_t dst = __shfl_sync(kFull, to, rr);
-            const uint4 w = lds128(buf + rr * 64 + ((ch ^ ((rr >> 1) & 3)) * 16));
-            if (dst >= 0) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + dst + 64 * x + 16 * ch) = w;
+            const uint4 w = lds128(out_sm + rr * 128 + ((ch ^ (rr & 7)) * 16));
+            if (dst >= 0) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + dst + 128 * x + 16 * ch) = w;
           }
           __syncwarp();
         }
@@ -731,6 +733,8 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant
   const int at = blockIdx.y * 32 + lane, i = at / kRows, r = at % kRows, tt = r / a.G;
   const int row = i * a.tok + tt;
   if (tt >= a.tok || row >= t.rows) return;
+  // (after a wait that gave up, the tile may be one that an earlier call left)
+  if (t.q0 < 0 || t.q0 + row >= a.total_q || t.g < 0 || t.g >= a.H_kv || parts > kMaxParts) return;
   const float* const p = slot_of<D>(a, blockIdx.x * parts) + at;
   constexpr int64_t STEP = 2 * kRows * (D + 2);
   float f[kMaxParts], M = -INFINITY, L = 0.f;

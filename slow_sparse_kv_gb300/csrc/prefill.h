@@ -27,8 +27,7 @@ struct PrefillArgs {
   // 3-D maps [row][head][d] of q, k and v, boxes of 64 elements of d with a
   // 128-byte swizzle: G heads x 128 / G rows of q, 1 head x 128 rows of k and v
   CUtensorMap tmq, tmk, tmv;
-  // the same of out, boxes of 32 elements, G heads and 32 / G rows with a 64-byte
-  // swizzle (where G divides 32)
+  // the same of out, boxes of G heads x 32 / G rows (where G divides 32)
   CUtensorMap tmo;
   void* out;
   float* lse;  // [total_q][H_q] or null

@@ -180,9 +180,9 @@ ItemSplit choose_item_split(long long n_a, int rows_a, long long n_b, int rows_b
 // Fill a.tmk / a.tmv for bf16 caches (sets a.use_tma; leaves it 0 if the
 // driver entry point is unavailable).
 void attach_tensor_maps(AttnArgs& a, const sfi_layout* L);
-// A 3-D map of bf16 elements: extents, the byte strides of dimensions 1 and 2,
-// box extents (box[0] = 64: with a 128-byte swizzle, 32: with a 64-byte one).
-// Elements outside the extents read as zero.
+// A 3-D map of bf16 elements with a 128-byte swizzle: extents, the byte
+// strides of dimensions 1 and 2, box extents (box[0] = 64).  Elements outside
+// the extents read as zero.
 bool encode_bf16_3d(CUtensorMap* m, const void* base, const uint64_t (&dims)[3],
                     const uint64_t (&strides)[2], const uint32_t (&box)[3]);
 sfi_status fail(sfi_status s, const char* fmt, ...);
