@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
 
 // Joins the pieces of each unit that has several, in their order:
 //   out = sum_w f_w o_w / sum_w f_w l_w,  f_w = 2^(c (m_w - max m)).
-// Few pieces: a thread for each output.  More than 8: 32 outputs a CTA, the pieces
+// Up to 16 pieces: a thread for each output.  More: 32 outputs a CTA, the pieces
 // dealt over its warps, and the warps' sums joined.  Bound by the latency of two or
 // three reads from L2.
 struct Joined {
@@ -784,7 +784,7 @@ struct Joined {
 
 template <int TR, int D>
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int grid) {
-  constexpr int FEW = 8;
+  constexpr int AHEAD = 8;  // pieces read at a time
   __shared__ Line ln;
   __shared__ float part[3][kWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -804,11 +804,11 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     if (pieces == 1) continue;
     const int64_t qrow = (int64_t(b) * a.H_q + int64_t(g) * G) * D;
     const float* const p = a.partials + (first + unit) * step;
-    if (pieces <= FEW) {
+    if (pieces <= 2 * AHEAD) {
       for (int i = blockIdx.y * kThreads + tid; i < G * D; i += gridDim.y * kThreads) {
         const int h = i / D, d = i - h * D;
         Joined j;
-        j.add<FEW>(p + h * (D + 2), step, pieces, d, D, c);
+        for (int w = 0; w < pieces; w += AHEAD) j.add<AHEAD>(p + h * (D + 2) + w * step, step, pieces - w, d, D, c);
         j.put(a, qrow, h, d, D, c);
       }
       continue;
@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
       // warp w takes the w-th eighth of the pieces
       const int share = (pieces + kWarps - 1) / kWarps, w1 = min(pieces, (warp + 1) * share);
       Joined j;
-      for (int w = warp * share; w < w1; w += FEW) j.add<FEW>(p + h * (D + 2) + w * step, step, w1 - w, d, D, c);
+      for (int w = warp * share; w < w1; w += AHEAD) j.add<AHEAD>(p + h * (D + 2) + w * step, step, w1 - w, d, D, c);
       part[0][warp][lane] = j.m;
       part[1][warp][lane] = j.l;
       part[2][warp][lane] = j.o;
