@@ -119,6 +119,32 @@ def test_largest_batch(sfi):
     c.check(*c.run(sfi))
 
 
+@pytest.mark.parametrize("hq,hkv,d,dtype,page,lens", [
+    (4, 2, 64, BF16, 16, [70000, 8191, 0, 130001]),  # units of far more than 16 pieces
+    (32, 8, 64, BF16, 20, [24001] * 4),              # shares in four parts, gathered rows
+    (8, 8, 128, BF16, 64, [24576] * 12),             # the same by boxes, one head a group
+    (2, 2, 64, F32, 16, [90000, 40003, 90001]),
+])
+def test_long_shares_are_cut_and_joined(sfi, hq, hkv, d, dtype, page, lens):
+    """Lengths at which a CTA's share is cut into parts, and units into many pieces: the first,
+    a middle and the last sequence, and the first and last KV head of each."""
+    c = Cache(hq, hkv, d, dtype, page, lens, seed=60)
+    out, lse = c.run(sfi)
+    again, lse2 = c.run(sfi)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    G = hq // hkv
+    for b in sorted({0, len(lens) // 2, len(lens) - 1}):
+        ids = c.rows[b][:-(-lens[b] // page)].tolist()
+        for g in sorted({0, hkv - 1}):
+            rows = torch.tensor(ids, device="cuda", dtype=torch.long)
+            K, V = (f64(x[rows, g].reshape(-1, d)) for x in (c.k, c.v))
+            for h in (g * G, g * G + G - 1):
+                ref, rl, scale, size = (np.asarray(x)[None] for x in P.attend(f64(c.q[b, h]), K, V, lens[b]))
+                tol = f32_tolerance(ref, scale, size, d, lens[b], dtype == BF16)
+                close(f64(out[b, h])[None], ref, tol, ("out", b, h))
+                close_lse(f64(lse[b, h])[None], rl, size, d, ("lse", b, h))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_pages_apart(sfi, dtype):
     """K and V of a page side by side in one allocation."""
