@@ -408,11 +408,11 @@ size_t sfi_paged_workspace_size(const sfi_paged_layout* layout);
  * len[b] includes the token, whose K and V are in the cache already
  * (sfi_paged_append).  q: [B][H_q][d] (dtype), 16-byte aligned; out and lse_out
  * fp32.  len[b] = 0 gives out = 0 and lse = -infinity.  Rows of a page at or
- * past len[b] may hold anything.  One launch: all rows of all sequences are
- * dealt evenly over the SMs, and the pieces of a split (sequence, KV head) are
- * joined by whichever CTA finishes last, in a fixed order: the same call gives the
- * same bits, but where a sequence is split, and so the order of its fp32 sums,
- * depends on all lengths of the batch.  The waits for copies have the limit of
+ * past len[b] may hold anything.  Two launches: all rows of all sequences are dealt
+ * over the SMs, and a small second kernel joins the pieces of each split
+ * (sequence, KV head) in a fixed order: the same call gives the same bits, but
+ * where a sequence is split, and so the order of its fp32 sums, depends on all
+ * lengths of the batch.  The waits for copies have the limit of
  * sfi_set_wait_limit. */
 sfi_status sfi_paged_attn(const sfi_paged_layout* layout, const void* q, const void* k,
                           const void* v, float* out, float* lse_out, void* ws, size_t ws_bytes,
@@ -426,7 +426,9 @@ sfi_status sfi_paged_attn(const sfi_paged_layout* layout, const void* q, const v
  * be NULL: one row per sequence, total_new = B.  A sequence whose rows leave
  * [0, total_new] or outnumber len[b] is flagged (SFI_DEV_LEN_OVER_CAP) and left
  * out; with cu_new NULL one with len[b] = 0 is an idle slot, whose row is not
- * stored.  k_new and v_new are 16-byte aligned and apart from the pool. */
+ * stored.  k_new and v_new are 16-byte aligned and apart from the pool.  The rows
+ * go to the pages that the table names, whoever else holds them: only positions
+ * added by the last sfi_pages_extend are sure to be the sequence's own. */
 sfi_status sfi_paged_append(const sfi_paged_layout* layout, int32_t total_new, const void* k_new,
                             const void* v_new, int64_t k_stride, int64_t v_stride,
                             const int32_t* cu_new, void* k, void* v, void* ws, size_t ws_bytes,

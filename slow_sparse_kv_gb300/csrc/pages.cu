@@ -6,6 +6,10 @@
 // and its result does not depend on their order.  It is bound by the latency
 // of a few dependent reads.  The copies are bound by HBM (read and write each
 // row once) and run on all SMs in slices of 16 KB, 64 bytes in flight a thread.
+// Measured (GPU time of a launch that finds nothing in L2): extending 64 sequences
+// 3.4 us, freeing 3.6, a fork's plan 6.3 and its copies 6.6 (16 pages, 8 layers), a
+// compaction's plan 4.5 and its moves of 352 MB 52 (6.77 TB/s), a token's rows for
+// 64 sequences 5.5, a prompt batch's 267 MB 37 to 39.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
