@@ -314,6 +314,9 @@ def _want(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: 
         raise ValueError(f"{name} lies on {t.device}, the layout on {device}")
     if not t.is_contiguous() and not (inner and t[0].is_contiguous()):
         raise ValueError(f"{name} must be dense{' behind its first dimension' if inner else ''}")
+    if inner and shape[0] > 1 and t.stride(0) < shape[1] * shape[2]:
+        # (an expanded row has stride 0, which the C calls read as rows without gaps)
+        raise ValueError(f"{name}: rows {t.stride(0)} elements apart overlap")
     return t
 
 

@@ -256,3 +256,13 @@ def test_wait_limit(sfi):
     ws.zero_()
     again, _ = run(sfi, q, k, v, [0, n], [0, n], ws)
     assert torch.equal(good, again)
+
+
+def test_expanded_rows_are_refused(sfi):
+    q, k = (torch.zeros(9, h, 64, device="cuda", dtype=BF16) for h in (4, 2))
+    lay = sfi.PackedLayout(4, 2, 64, BF16, ints([0, 9]), ints([0, 9]), 9, 9)
+    ws, out = sfi.prefill_workspace(lay), torch.empty_like(q)
+    for a in ((q[:1].expand(9, 4, 64), k, k, out), (q, k[:1].expand(9, 2, 64), k, out),
+              (q, k, k[:1].expand(9, 2, 64), out), (q, k, k, out[:1].expand(9, 4, 64))):
+        with pytest.raises(ValueError):
+            sfi.sfi_prefill_attn(lay, *a, None, ws)

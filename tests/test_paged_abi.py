@@ -160,3 +160,14 @@ def test_binding_refuses_mismatched_pools(sfi):
     k = torch.zeros(3, 2, 16, 64)
     with pytest.raises(ValueError):
         sfi.PageStore(torch.zeros(3, dtype=torch.int32), k, k[:2])
+
+
+def test_binding_refuses_rows_that_overlap(sfi):
+    """A stride of 0 means rows without gaps to the C calls: an expanded row is none of that."""
+    row, shape = torch.zeros(1, 2, 64), (3, 2, 64)
+    flat = torch.zeros(1000)
+    for t in (row.expand(shape), flat.as_strided(shape, (64, 64, 1)), flat.as_strided(shape, (127, 64, 1))):
+        with pytest.raises(ValueError):
+            sfi._want("q", t, shape, torch.float32, t.device, True)
+    for t, n in ((row.expand(1, 2, 64), 1), (flat.as_strided(shape, (192, 64, 1)), 3), (torch.zeros(0, 2, 64), 0)):
+        sfi._want("q", t, (n, 2, 64), torch.float32, t.device, True)
