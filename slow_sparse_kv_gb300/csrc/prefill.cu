@@ -41,10 +41,6 @@ namespace sfi {
 namespace {
 
 constexpr int kThreads = 384;  // 2 softmax warpgroups; a load, an MMA, a scheduling and a cleaning warp
-// Registers a thread: launched with 168 (64512 in all); the softmax threads
-// hold a whole row of scores, the third warpgroup gives up what they take
-// (128 * (2 * 216 + 72) = 64512).
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kRows = 128;     // query rows per tile
 constexpr int kKeys = 128;     // keys per block
 // P of a block is handed over in parts, the first 64 keys, then twice 32: the
@@ -60,6 +56,11 @@ struct Cfg {
   static constexpr int STAGES = D == 128 ? 4 : 6;         // K and V blocks in flight
   static constexpr uint32_t OUT = 8 * 32 * 128;           // 32 rows of 64 outputs for each softmax warp
   static constexpr uint32_t SMEM = 1024 + (2 + STAGES) * TILE + OUT;
+  // Registers a thread: launched with 168; the softmax threads hold a whole row of
+  // scores, the third warpgroup gives up what they take.  (d = 128: 208 and 88
+  // against 216 and 72, 16 packed prompts 220 against 224 us; d = 64: 186 against
+  // 180, 8192 tokens; with 200 the row spills, 233 us.)
+  static constexpr int SOFTMAX_REGS = D == 128 ? 208 : 216, OTHER_REGS = 504 - 2 * SOFTMAX_REGS;
 };
 
 using Tile = PrefillTile;
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   auto taken = [&](int k) { mbar_arrive(smem_addr(&sh.tile_empty[k & 1])); };
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (warp == 8 && lane == 0) {
       // ---- loads: each tile's Q, then K_0, V_0, K_1, V_1, ... through the ring
       int x = 0, q_uses[2] = {0, 0};
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
   } else {
     // ---- softmax and output of tile half i: one thread per row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX_REGS));
     const int i = warp >> 2;
     const int r = tid & 127;
     const int tt = r / a.G;                           // token of the tile
@@ -662,49 +663,49 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       // Out through shared memory, 64 columns at a time, by TMA where the warp's 32
       // rows are whole tokens of the tile, and else with 8 lanes to 128 bytes.
       // (Stores from registers, a row to a lane or rows by 8 lanes, hold up the
-      // load/store unit, and with it every wait of the CTA, for 3000 clocks.)
+      // load/store unit, and with it every wait of the CTA, for 3000 clocks.  A loop,
+      // not unrolled: this code runs once a tile, and fetching it costs more than
+      // running it; 220 -> 216 us for 16 packed prompts.)
       const bool whole = 32 % a.G == 0 && __all_sync(kFull, valid);
-#pragma unroll
-      for (int x = 0; x < D / 64; ++x) {
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          uint32_t o[32];
-          if (n_it > 0) {
-            tc5::ld32(o_tm + 64 * x + 32 * z, o);
-            tc5::wait_ld();
-            pin(o);
-          }
-          if (z == 0) {  // the copy that read the buffer last is done
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            __syncwarp();
-          }
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = none ? 0u : pack_bf16x2(__uint_as_float(o[8 * y + 2 * e]) * inv, __uint_as_float(o[8 * y + 2 * e + 1]) * inv);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             out_sm + lane * 128 + (((4 * z + y) ^ (lane & 7)) * 16)),
-                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                         : "memory");
-          }
+#pragma unroll 1
+      for (int x = 0; x < D / 32; ++x) {
+        uint32_t o[32];
+        if (n_it > 0) {
+          tc5::ld32(o_tm + 32 * x, o);
+          tc5::wait_ld();
+          pin(o);
         }
+        if (x % 2 == 0) {  // the copy that read the buffer last is done
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = none ? 0u : pack_bf16x2(__uint_as_float(o[8 * y + 2 * e]) * inv, __uint_as_float(o[8 * y + 2 * e + 1]) * inv);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           out_sm + lane * 128 + (((x % 2 * 4 + y) ^ (lane & 7)) * 16)),
+                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+        if (x % 2 == 0) continue;
         if (whole) {
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(&a.tmo, out_sm, x * 64, t.g * a.G, t.q0 + i * a.tok + (warp & 3) * 32 / a.G);
+            tma_store_3d(&a.tmo, out_sm, x / 2 * 64, t.g * a.G, t.q0 + i * a.tok + (warp & 3) * 32 / a.G);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         } else {
           __syncwarp();
-#pragma unroll
+#pragma unroll 1
           for (int y = 0; y < 8; ++y) {
             const int rr = y * 4 + (lane >> 3), ch = lane & 7;
             const int64_t dst = __shfl_sync(kFull, to, rr);
             const uint4 w = lds128(out_sm + rr * 128 + ((ch ^ (rr & 7)) * 16));
-            if (dst >= 0) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + dst + 128 * x + 16 * ch) = w;
+            if (dst >= 0) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + dst + 128 * (x / 2) + 16 * ch) = w;
           }
           __syncwarp();
         }
