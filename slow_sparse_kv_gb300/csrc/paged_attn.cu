@@ -13,7 +13,7 @@
 // Bound by HBM: 2 d e bytes a position and 4 d G flops, G <= 16.  Measured, 32 / 8
 // heads of 128 in pages of 16: 8 x 32768 positions (1.07 GB) in 164 us, 6.56 TB/s,
 // where a copy reaches 6.78; fp32, 4 x 32768, 166 us; 32 sequences of 4096 to
-// 65536 (2.57 GB) in 384 us, 6.70 TB/s; one of 128 in 11 us, the two launches.
+// 65536 (2.57 GB) in 384 us, 6.70 TB/s; one of 700 in 9.9 us, the two launches.
 //
 // What an item saw of one (sequence, KV head) is a piece, a softmax state (m, l,
 // o), merged over the warps through shared memory.  The only piece of its unit is
@@ -248,7 +248,7 @@ struct Shared {
   long long item[kItemSlots][2];                          // tiles [from, to); from = to: the end
   int place[kItemSlots];
   volatile int abort;
-  float factor[kWarps][4], top[4], sum[4];                // of the heads that are merged
+  uint64_t merge_free;                                    // the warps' states have been read
 };
 
 // Tiles of [from, to) whose number is r modulo m (a power of two): the first one,
@@ -432,6 +432,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
     mbar_init(smem_addr(&sh.item_full[tid - 64]), 1);
     mbar_init(smem_addr(&sh.item_empty[tid - 64]), kWarps + kProducers - 1);
   } else if (tid == 96) {
+    mbar_init(smem_addr(&sh.merge_free), kWarps);
     sh.abort = 0;
   }
   fence_mbar_init();
@@ -459,7 +460,39 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAttendRegs));
     const float c = a.scale_log2;
-    uint32_t y = 0;  // this warp's tiles so far
+    uint32_t y = 0;       // this warp's tiles so far
+    uint32_t merges = 0;  // and rounds of merging
+    constexpr int NS = F32 ? NT * 2 : NT;  // (see the state below)
+    constexpr int NE = F32 ? 1 : 2;
+    constexpr int KS = D / 16;
+    constexpr int LPR = D / 4, RPP = 32 / LPR;  // fp32: lanes per row, rows per pass
+    const int li = lane % LPR, half = lane / LPR;
+    // the lane's part of a unit's queries, and the sequence's length
+    uint32_t qb[F32 ? 1 : NT][KS][2];
+    float qf[F32 ? NS * 4 : 1][4];
+    auto load_unit = [&](const Unit& u) {
+      const int64_t qrow = (int64_t(u.b) * a.H_q + int64_t(u.g) * G) * D;
+      if constexpr (!F32) {
+        const uint32_t* qw = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) + qrow);
+#pragma unroll
+        for (int h = 0; h < NT; ++h) {
+          const int head = h * 8 + (lane >> 2);
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              qb[h][kk][e] = head < G ? qw[(head * D + kk * 16 + e * 8) / 2 + (lane & 3)] : 0u;
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < NS * 4; ++h) {
+          float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (h < G) w = reinterpret_cast<const float4*>(static_cast<const T*>(a.q) + qrow + h * D)[li];
+          qf[h][0] = w.x, qf[h][1] = w.y, qf[h][2] = w.z, qf[h][3] = w.w;
+        }
+      }
+      return min(geo.len[u.b], cap);
+    };
     for (int k = 0;; ++k) {
       const int is = k % kItemSlots;
       if (!warp_ctrl_wait(smem_addr(&sh.item_full[is]), (k / kItemSlots) & 1, &sh.abort, geo.status)) break;
@@ -469,41 +502,23 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
       if (lane == 0) mbar_arrive(smem_addr(&sh.item_empty[is]));
       if (from >= to) break;
       long long x = first_of(from, warp, kWarps);  // this warp's next tile
-      for (Unit u = unit_at(from, ln, B, H_kv); u.begin < to; unit_next(u, ln, B, H_kv)) {
-        if (u.end == u.begin) continue;
+      Unit u = unit_at(from, ln, B, H_kv);
+      int n = load_unit(u);
+      while (true) {
         const long long pe = min(u.end, to);
         const int b = u.b, g = u.g;
-        const int n = min(geo.len[b], cap);
         const int64_t qrow = (int64_t(b) * a.H_q + int64_t(g) * G) * D;
 
         // state: bf16 head 2 (lane % 4) + e of column tile h, in every lane with the same lane % 4;
         // fp32 head 4 h + lane % 4
-        constexpr int NS = F32 ? NT * 2 : NT;
-        constexpr int NE = F32 ? 1 : 2;
         float m[NS][NE], l[NS][NE];
 #pragma unroll
         for (int h = 0; h < NS; ++h)
 #pragma unroll
           for (int e = 0; e < NE; ++e) m[h][e] = -INFINITY, l[h][e] = 0.f;
 
-        // per-lane operands
-        constexpr int KS = D / 16;
-        uint32_t qb[F32 ? 1 : NT][KS][2];
-        float o[F32 ? 1 : KS][F32 ? 1 : NT][4];
-        float qf[F32 ? NS * 4 : 1][4], of[F32 ? NS * 4 : 1][4];
-        constexpr int LPR = D / 4, RPP = 32 / LPR;  // fp32: lanes per row, rows per pass
-        const int li = lane % LPR, half = lane / LPR;
+        float o[F32 ? 1 : KS][F32 ? 1 : NT][4], of[F32 ? NS * 4 : 1][4];
         if constexpr (!F32) {
-          const uint32_t* qw = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) + qrow);
-#pragma unroll
-          for (int h = 0; h < NT; ++h) {
-            const int head = h * 8 + (lane >> 2);
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                qb[h][kk][e] = head < G ? qw[(head * D + kk * 16 + e * 8) / 2 + (lane & 3)] : 0u;
-          }
 #pragma unroll
           for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
@@ -512,13 +527,9 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
               for (int e = 0; e < 4; ++e) o[kk][h][e] = 0.f;
         } else {
 #pragma unroll
-          for (int h = 0; h < NS * 4; ++h) {
-            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (h < G) w = reinterpret_cast<const float4*>(static_cast<const T*>(a.q) + qrow + h * D)[li];
-            qf[h][0] = w.x, qf[h][1] = w.y, qf[h][2] = w.z, qf[h][3] = w.w;
+          for (int h = 0; h < NS * 4; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e) of[h][e] = 0.f;
-          }
         }
 
         for (; x < pe; x += kWarps) {
@@ -668,12 +679,25 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
           if (lane == 0) mbar_arrive(smem_addr(&sh.empty[slot]));
         }
 
-        // ---- the piece: the warps' states merged, MH heads at a time
-        const bool alone = cut.holder(u.begin) == cut.holder(u.end - 1);  // the unit's only piece
+        // the next unit of the item; its queries are on their way during the merge
+        Unit next = u;
+        do unit_next(next, ln, B, H_kv);
+        while (next.begin < to && next.end == next.begin);
+        const bool more = next.begin < to;
+        if (more) n = load_unit(next);
+
+        // ---- the piece: the warps' states merged, MH heads at a time.  A warp writes
+        // when all have read the round before, which they mostly have long since,
+        // so that a round is one wait for all.  (With factors by 32 threads between two
+        // more of them, and the next queries loaded behind it: 106 us against 84 for
+        // 256 x 300 positions, 93 against 88 for 131072.)
+        const bool alone = u.begin >= from && u.end <= to;  // the unit's only piece
         float* const slot = a.partials + (place + b * H_kv + g) * int64_t(G) * (D + 2);
 #pragma unroll
         for (int h0 = 0; h0 < C::HEADS; h0 += C::MH) {
           if (h0 >= G) break;
+          if (merges > 0) warp_ctrl_wait(smem_addr(&sh.merge_free), (merges - 1) & 1, &sh.abort, geo.status);
+          ++merges;
           float* const mine = merge + warp * C::MH * C::MROW;
           if constexpr (!F32) {
             const int h = h0 / 8;
@@ -708,33 +732,23 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
             }
           }
           attend_sync();
-          if (tid < C::MH * kWarps) {
-            // factors that bring the warps' states to a common maximum
-            const int h = tid / kWarps, w = tid % kWarps;
-            const float* const st = merge + (w * C::MH + h) * C::MROW + D;
-            const float m_ = st[0], l_ = st[1];
-            float M = m_;
-#pragma unroll
-            for (int y = 1; y < kWarps; y <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, y));
-            // (a warp that saw nothing, or only scores of -infinity, adds nothing)
-            const bool none = m_ == -INFINITY && l_ == 0.f;
-            const float f = none ? 0.f : ex2((m_ - M) * c);
-            float L = none ? 0.f : f * l_;
-#pragma unroll
-            for (int y = 1; y < kWarps; y <<= 1) L += __shfl_xor_sync(kFull, L, y);
-            sh.factor[w][h] = none ? -1.f : f;
-            if (w == 0) sh.top[h] = M, sh.sum[h] = L;
-          }
-          attend_sync();
           for (int i = tid; i < min(C::MH, G - h0) * D; i += kThreads) {
             const int h = i / D, d = i - h * D;
-            float O = 0.f;
+            float2 ml[kWarps];
+            float M = -INFINITY, L = 0.f, O = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-              const float f = sh.factor[w][h];
-              O += f == -1.f ? 0.f : f * merge[(w * C::MH + h) * C::MROW + d];
+              ml[w] = *reinterpret_cast<const float2*>(merge + (w * C::MH + h) * C::MROW + D);
+              M = fmaxf(M, ml[w].x);
             }
-            const float M = sh.top[h], L = sh.sum[h];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              // (a warp that saw nothing, or only scores of -infinity, adds nothing)
+              const bool none = ml[w].x == -INFINITY && ml[w].y == 0.f;
+              const float f = ex2((ml[w].x - M) * c);
+              L += none ? 0.f : f * ml[w].y;
+              O += none ? 0.f : f * merge[(w * C::MH + h) * C::MROW + d];
+            }
             if (alone) {
               a.out[qrow + (h0 + h) * D + d] = L == 0.f ? 0.f : O / L;
               if (d == 0 && a.lse) a.lse[qrow / D + h0 + h] = (M * c + log2f(L)) * 0.6931471805599453f;
@@ -744,12 +758,15 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
               if (d == 0) p[D] = M, p[D + 1] = L;
             }
           }
-          attend_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh.merge_free));
         }
+        if (!more) break;
+        u = next;
       }
     }
-    }
   }
+}
 
 // Joins the pieces of each unit that has several, in their order:
 //   out = sum_w f_w o_w / sum_w f_w l_w,  f_w = 2^(c (m_w - max m)).
