@@ -130,7 +130,7 @@ sfi_status check_paged(const sfi_paged_layout* L) {
 
 // What the paged calls keep in their workspace.
 struct PagedPlan {
-  size_t next, partials, jobs, map, holes, moved, n_moved, total;
+  size_t partials, jobs, map, holes, moved, n_moved, total;
 };
 
 PagedPlan plan_paged(const sfi_paged_layout* L) {
@@ -142,8 +142,7 @@ PagedPlan plan_paged(const sfi_paged_layout* L) {
     off += align256(bytes);
     return at;
   };
-  p.next = take(2 * 4);
-  p.partials = take((units + size_t(kPagedItems) * kPagedMaxGrid) * G * (L->head_dim + 2) * 4);
+  p.partials = take((units + kPagedMaxGrid) * G * (L->head_dim + 2) * 4);
   p.jobs = take(size_t(kMaxBatch) * sizeof(int4));
   p.map = take(size_t(L->n_pages) * 4);
   p.holes = take(size_t(L->n_pages) * 4);
@@ -296,7 +295,6 @@ sfi_status sfi_paged_attn(const sfi_paged_layout* L, const void* q, const void* 
   a.H_q = L->n_q_heads;
   a.G = L->n_q_heads / L->n_kv_heads;
   a.scale_log2 = float(1.4426950408889634 / std::sqrt(double(D)));
-  a.next = reinterpret_cast<int32_t*>(w + p.next);
   a.partials = reinterpret_cast<float*>(w + p.partials);
   a.wait_cycles = wait_limit_cycles();
   // A tile of 16 positions that lies in one page is one box per tensor; other

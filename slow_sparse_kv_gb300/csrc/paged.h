@@ -7,7 +7,6 @@
 namespace sfi {
 
 constexpr int kPagedMaxGrid = 256;  // CTAs of a paged-attention launch, at most
-constexpr int kPagedItems = 4;      // items that a CTA's share is cut into, at most
 
 // Geometry of a paged cache on the device.
 struct PagedGeo {
@@ -30,8 +29,7 @@ struct PagedAttnArgs {
   float* lse;  // nullable
   int32_t H_q, G;
   float scale_log2;   // log2(e) / sqrt(d)
-  float* partials;    // [kPagedItems * grid + B * H_kv][G][d + 2]
-  int32_t* next;      // [2]: next item, CTAs that ran out; zero between launches
+  float* partials;    // [grid + B * H_kv][G][d + 2]
   long long wait_cycles;
 };
 

@@ -2,20 +2,17 @@
 //
 // A tile is 16 (fp32: 8) consecutive positions of one (sequence, KV head).  All
 // tiles of all sequences stand in one line, sequence by sequence and head by
-// head.  The line is cut, whatever the lengths, into items, one of 3/4 of a CTA's
-// fair share for each CTA and smaller ones taken from a shared counter, because
-// the SMs do not get the same share of HBM (with equal parts the last CTA ended 15%
-// after the median, so 5%).  Four warps look up pages, 32
-// tiles at a time, and copy ahead, across the borders of items and sequences,
-// into rings of 24 KB for each of the eight warps that attend (a warp that looked up and copied for itself waited for
-// the table's reads before each tile: 1.8 times as long).  A tile's place in the
-// line says which warp takes it, so that no sum depends on who took which item.
+// head, and the line is cut, whatever the lengths, into a share for each CTA.  Four
+// warps look up pages, 32 tiles at a time, and copy ahead, across the borders of
+// sequences, into rings of 24 KB for each of the eight warps that attend (a warp that
+// looked up and copied for itself waited for the table's reads before each tile: 1.8
+// times as long).  A tile's place in the line says which warp takes it.
 // Bound by HBM: 2 d e bytes a position and 4 d G flops, G <= 16.  Measured, 32 / 8
 // heads of 128 in pages of 16: 8 x 32768 positions (1.07 GB) in 164 us, 6.56 TB/s,
 // where a copy reaches 6.78; fp32, 4 x 32768, 166 us; 32 sequences of 4096 to
 // 65536 (2.57 GB) in 384 us, 6.70 TB/s; one of 700 in 9.9 us, the two launches.
 //
-// What an item saw of one (sequence, KV head) is a piece, a softmax state (m, l,
+// What a CTA saw of one (sequence, KV head) is a piece, a softmax state (m, l,
 // o), merged over the warps through shared memory.  The only piece of its unit is
 // normalised and written; others go to the workspace, and a second small kernel,
 // launched early and waiting for the first one's end, joins them in the order of
@@ -50,7 +47,6 @@ constexpr int kProducers = 4;                // warps that copy
 constexpr int kAllThreads = kThreads + kProducers * 32;
 constexpr int kAttendRegs = 216, kCopyRegs = 72;  // of 168 each at launch: 2 * 216 + 72 = 3 * 168
 constexpr int kRingBytes = 196608;
-constexpr int kItemSlots = 8;                // items that the copies may be ahead
 constexpr float kGrow = 8.0f;                // growth of the maximum (log2) that moves m
 
 enum Load { kTma, kCpAsync, kBulk };
@@ -75,51 +71,31 @@ struct Line {
   long long part[kWarps];
 };
 
-// How the line of `total` tiles is cut: into regions of equal size, one for each of
-// `grid` CTAs, and each region into items of 3/4, 1/8, 1/16 and 1/16 of it.  The
-// CTAs take their own regions' large items first and then what comes of the
-// small ones, all 1/8s before all 1/16s.  An item's place in the line (place) is
-// not the order in which it is taken (id).
+// How the line of `total` tiles is cut: into shares of equal size, one for each of
+// `grid` CTAs.  (With the last quarter of each share as three smaller items, taken
+// from a counter, the CTAs end closer together: 492 us instead of 500 for 32 sequences
+// of 4096 to 65536, 161.5 instead of 163 for 8 x 32768; but each item costs a merge, a
+// longer join and registers: 60 instead of 53 us for 64 x 1000, 150 instead of 133 for
+// 8 x ~24000 with 16 heads a group, 189 instead of 176 for 8 x 32768 in fp32 with d = 64.)
 struct Cut {
-  static constexpr int PARTS = 4;
-  long long total, per, wide;  // tiles of a region; those before `wide` belong to regions with one more
-  int regions, parts, extra;   // extra: regions with one tile more
+  long long total, per, wide;  // tiles of a share; those before `wide` belong to shares with one more
+  int shares, extra;           // extra: shares with one tile more
 
   __device__ __forceinline__ Cut(long long total_, int grid) {
     total = total_;
-    // few tiles: fewer regions, of a tile for each warp at least, and no small items
+    // few tiles: fewer shares, of a tile for each warp at least
     const long long most = (total + kWarps - 1) / kWarps;
-    regions = most < grid ? int(most) : grid;
-    per = regions > 0 ? total / regions : 0;
-    extra = regions > 0 ? int(total - per * regions) : 0;
+    shares = most < grid ? int(most) : grid;
+    per = shares > 0 ? total / shares : 0;
+    extra = shares > 0 ? int(total - per * shares) : 0;
     wide = extra * (per + 1);
-    parts = per >= 16 * kWarps ? PARTS : 1;
   }
-  __device__ __forceinline__ long long start(int region) const { return region * per + min(region, extra); }
-  // end of a part, from the region's start
-  __device__ __forceinline__ long long end_of(long long size, int part) const {
-    return part + 1 == parts ? size : size - (size >> (part + 2));
-  }
-  __device__ __forceinline__ bool range(long long id, long long* from, long long* to, int* place) const {
-    const int part = regions > 0 ? int(id / regions) : 0, region = int(id - (long long)part * regions);
-    if (regions == 0 || part >= parts) return false;
-    const long long at = start(region), size = start(region + 1) - at;
-    *from = at + (part > 0 ? end_of(size, part - 1) : 0);
-    *to = at + end_of(size, part);
-    *place = region * parts + part;
-    return true;
-  }
-  // the place of the item that holds tile x
+  __device__ __forceinline__ long long start(int share) const { return share * per + min(share, extra); }
+  // the share that holds tile x
   __device__ __forceinline__ int holder(long long x) const {
-    int region;
     if (total < (1LL << 31))  // (a 64-bit division takes ~10 times as long)
-      region = x < wide ? int(uint32_t(x) / uint32_t(per + 1)) : extra + int(uint32_t(x - wide) / uint32_t(per));
-    else
-      region = int(x < wide ? x / (per + 1) : extra + (x - wide) / per);
-    const long long at = start(region), size = start(region + 1) - at;
-    int part = 0;
-    while (part + 1 < parts && x - at >= end_of(size, part)) ++part;
-    return region * parts + part;
+      return x < wide ? int(uint32_t(x) / uint32_t(per + 1)) : extra + int(uint32_t(x - wide) / uint32_t(per));
+    return int(x < wide ? x / (per + 1) : extra + (x - wide) / per);
   }
 };
 
@@ -244,175 +220,132 @@ __device__ __forceinline__ void attend_sync() { named_bar_sync(1, kThreads); }
 struct Shared {
   Line ln;
   uint64_t full[48], empty[48];                           // of each slot of the ring
-  uint64_t item_full[kItemSlots], item_empty[kItemSlots]; // of the items
-  long long item[kItemSlots][2];                          // tiles [from, to); from = to: the end
-  int place[kItemSlots];
   volatile int abort;
   uint64_t merge_free;                                    // the warps' states have been read
 };
 
-// Tiles of [from, to) whose number is r modulo m (a power of two): the first one,
-// and how many there are.
+// The first tile from `from` on whose number is r modulo m (a power of two).
 __device__ __forceinline__ long long first_of(long long from, int r, int m) { return from + ((r - from) & (m - 1)); }
-__device__ __forceinline__ long long count_of(long long from, long long to, int r, int m) {
-  const long long x = first_of(from, r, m);
-  return x < to ? (to - x + m - 1) / m : 0;
-}
 
 // The copying warps: warp `p` takes the tiles of the attending warps p and p + 4.
 template <typename T, int D, int NT, Load LD>
-__device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, const Cut& cut, uint32_t ring, int p) {
+__device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, long long from, long long to,
+                                           uint32_t ring, int p) {
   using C = Cfg<T, D, NT>;
   constexpr int TR = C::TR;
   const PagedGeo& geo = a.geo;
   const int lane = threadIdx.x & 31, P = geo.P, H_kv = geo.H_kv, cap = geo.max_pages * P;
   const T* const kp = static_cast<const T*>(a.k);
   const T* const vp = static_cast<const T*>(a.v);
-  uint32_t done[2] = {0, 0};  // tiles of the two warps in the items before
-  // (a CTA beyond the regions has none of its own, and then there are no small items)
-  int ask = blockIdx.x < cut.regions ? int(blockIdx.x) : cut.regions * cut.parts;
   bool ok = true;
-  for (int k = 0; ok; ++k) {
-    const int is = k % kItemSlots;
-    long long from, to;
-    if (p == 0) {
-      // this warp takes the items: the CTA's own one first, then from the counter
-      int place = 0;
-      if (!cut.range(__shfl_sync(kFull, ask, 0), &from, &to, &place)) from = to = 0;
-      if (k >= kItemSlots)
-        ok = warp_ctrl_wait(smem_addr(&sh.item_empty[is]), (k / kItemSlots - 1) & 1, &sh.abort, geo.status);
-      if (lane == 0) {
-        sh.item[is][0] = from;
-        sh.item[is][1] = ok ? to : from;
-        sh.place[is] = place;
-        mbar_arrive(smem_addr(&sh.item_full[is]));
-        if (from < to) {
-          ask = cut.regions + atomicAdd(a.next, 1);
-        } else if (atomicAdd(a.next + 1, 1) == int(gridDim.x) - 1) {
-          // the last CTA to run out leaves the counters at zero
-          a.next[0] = 0;
-          a.next[1] = 0;
-        }
-      }
-      __syncwarp();
-    } else {
-      ok = warp_ctrl_wait(smem_addr(&sh.item_full[is]), (k / kItemSlots) & 1, &sh.abort, geo.status);
-      if (!ok) break;
-      from = sh.item[is][0], to = sh.item[is][1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sh.item_empty[is]));
+  const long long first[2] = {first_of(from, p, kWarps), first_of(from, p + kProducers, kWarps)};
+  for (long long x0 = first_of(from, p, kProducers); x0 < to && ok; x0 += kProducers * 32) {
+    // 32 tiles: each lane finds the place and the page of its own
+    const long long x = x0 + kProducers * lane;
+    const bool mine = x < to;
+    Unit u{0, 0, 0, 0};
+    int t = 0, n = 0;
+    int page[LD == kBulk ? TR : 1];
+    if (mine) {
+      u = unit_at(x, sh.ln, geo.B, H_kv);
+      t = int(x - u.begin);
+      n = min(geo.len[u.b], cap);
     }
-    if (!ok || from >= to) break;
-    const long long first[2] = {first_of(from, p, kWarps), first_of(from, p + kProducers, kWarps)};
-    for (long long x0 = first_of(from, p, kProducers); x0 < to && ok; x0 += kProducers * 32) {
-      // 32 tiles: each lane finds the place and the page of its own
-      const long long x = x0 + kProducers * lane;
-      const bool mine = x < to;
-      Unit u{0, 0, 0, 0};
-      int t = 0, n = 0;
-      int page[LD == kBulk ? TR : 1];
-      if (mine) {
-        u = unit_at(x, sh.ln, geo.B, H_kv);
-        t = int(x - u.begin);
-        n = min(geo.len[u.b], cap);
-      }
-      const int32_t* const row = geo.table + int64_t(u.b) * geo.max_pages;
-      if (LD != kCpAsync) {
-        bool bad = false;
+    const int32_t* const row = geo.table + int64_t(u.b) * geo.max_pages;
+    if (LD != kCpAsync) {
+      bool bad = false;
 #pragma unroll
-        for (int r = 0; r < (LD == kBulk ? TR : 1); ++r) {
-          const int pos = t * TR + r;
-          page[r] = mine && pos < n ? row[pos / P] : 0;  // (fp32: mostly the same entry)
-          if (page[r] < 0 || page[r] >= geo.n_pages) bad = true, page[r] = 0;
+      for (int r = 0; r < (LD == kBulk ? TR : 1); ++r) {
+        const int pos = t * TR + r;
+        page[r] = mine && pos < n ? row[pos / P] : 0;  // (fp32: mostly the same entry)
+        if (page[r] < 0 || page[r] >= geo.n_pages) bad = true, page[r] = 0;
+      }
+      if (bad) set_status(geo.status, SFI_DEV_BAD_INDEX);
+    }
+    // fp32: the lane's rows, and where they go on in another page
+    int rows = 0, in0 = 0;
+    uint32_t starts = 0;
+    if (LD == kBulk) {
+      rows = min(TR, n - t * TR);
+      in0 = t * TR % P;
+      int in = in0;
+#pragma unroll
+      for (int r = 1; r < TR; ++r) {
+        in = in + 1 == P ? 0 : in + 1;
+        if (in == 0 && r < rows) starts |= 1u << r;
+      }
+    }
+    const int64_t at0 = page[0] * geo.page_stride + (int64_t(u.g) * P + in0) * D;
+    const int row0 = LD == kTma ? int(page[0] * (geo.page_stride / D) + u.g * P + t * TR % P) : 0;
+    const int count = int(min(32LL, (to - x0 + kProducers - 1) / kProducers));
+    // kCpAsync: the i-th tile's row of this lane (lane % TR): its page, and where in it,
+    // -1 for no row.  A tile's pages are read while the one before it is copied (waited
+    // for before each tile: 136 us against 129 for 8 x ~24000 positions in pages of 20).
+    int pg = 0, in = -1;
+    auto row_of = [&](int i) {
+      const int ut = __shfl_sync(kFull, t, i), ug = __shfl_sync(kFull, u.g, i), un = __shfl_sync(kFull, n, i);
+      const int32_t* const urow = geo.table + int64_t(__shfl_sync(kFull, u.b, i)) * geo.max_pages;
+      const int pos = ut * TR + lane % TR;
+      pg = pos < un ? urow[pos / P] : 0;
+      in = pos < un ? ug * P + pos % P : -1;
+    };
+    if (LD == kCpAsync) row_of(0);
+    for (int i = 0; i < count && ok; ++i) {
+      const long long xi = x0 + kProducers * i;
+      const int w = int(xi >> 2) & 1;  // which of the two warps
+      const uint32_t y = uint32_t(xi - first[w]) / kWarps;
+      const int slot = (p + w * kProducers) * C::STAGES + int(y % C::STAGES);
+      const uint32_t use = y / C::STAGES;
+      if (use > 0) ok = warp_ctrl_wait(smem_addr(&sh.empty[slot]), (use - 1) & 1, &sh.abort, geo.status);
+      if (!ok) break;
+      const uint32_t dst = ring + slot * 2 * C::HALF, bar = smem_addr(&sh.full[slot]);
+      if constexpr (LD == kTma) {
+        if (lane == i) {
+          mbar_arrive_expect_tx(bar, 2 * C::HALF);
+          tma_load_3d(dst, &a.tmk, 0, row0, 0, bar);
+          tma_load_3d(dst + C::HALF, &a.tmv, 0, row0, 0, bar);
         }
-        if (bad) set_status(geo.status, SFI_DEV_BAD_INDEX);
-      }
-      // fp32: the lane's rows, and where they go on in another page
-      int rows = 0, in0 = 0;
-      uint32_t starts = 0;
-      if (LD == kBulk) {
-        rows = min(TR, n - t * TR);
-        in0 = t * TR % P;
-        int in = in0;
+      } else if constexpr (LD == kBulk) {
+        if (lane == i) {
+          // runs of rows that lie in one page
+          mbar_arrive_expect_tx(bar, uint32_t(rows) * 2 * C::ROW);
+          const uint32_t bytes = uint32_t(min(P - in0, rows)) * C::ROW;
+          bulk_load(dst, kp + at0, bytes, bar);
+          bulk_load(dst + C::HALF, vp + at0, bytes, bar);
+          if (starts) {
 #pragma unroll
-        for (int r = 1; r < TR; ++r) {
-          in = in + 1 == P ? 0 : in + 1;
-          if (in == 0 && r < rows) starts |= 1u << r;
-        }
-      }
-      const int64_t at0 = page[0] * geo.page_stride + (int64_t(u.g) * P + in0) * D;
-      const int row0 = LD == kTma ? int(page[0] * (geo.page_stride / D) + u.g * P + t * TR % P) : 0;
-      const int count = int(min(32LL, (to - x0 + kProducers - 1) / kProducers));
-      // kCpAsync: the i-th tile's row of this lane (lane % TR): its page, and where in it,
-      // -1 for no row.  A tile's pages are read while the one before it is copied (waited
-      // for before each tile: 136 us against 129 for 8 x ~24000 positions in pages of 20).
-      int pg = 0, in = -1;
-      auto row_of = [&](int i) {
-        const int ut = __shfl_sync(kFull, t, i), ug = __shfl_sync(kFull, u.g, i), un = __shfl_sync(kFull, n, i);
-        const int32_t* const urow = geo.table + int64_t(__shfl_sync(kFull, u.b, i)) * geo.max_pages;
-        const int pos = ut * TR + lane % TR;
-        pg = pos < un ? urow[pos / P] : 0;
-        in = pos < un ? ug * P + pos % P : -1;
-      };
-      if (LD == kCpAsync) row_of(0);
-      for (int i = 0; i < count && ok; ++i) {
-        const long long xi = x0 + kProducers * i;
-        const int w = int(xi >> 2) & 1;  // which of the two warps
-        const uint32_t y = done[w] + uint32_t(xi - first[w]) / kWarps;
-        const int slot = (p + w * kProducers) * C::STAGES + int(y % C::STAGES);
-        const uint32_t use = y / C::STAGES;
-        if (use > 0) ok = warp_ctrl_wait(smem_addr(&sh.empty[slot]), (use - 1) & 1, &sh.abort, geo.status);
-        if (!ok) break;
-        const uint32_t dst = ring + slot * 2 * C::HALF, bar = smem_addr(&sh.full[slot]);
-        if constexpr (LD == kTma) {
-          if (lane == i) {
-            mbar_arrive_expect_tx(bar, 2 * C::HALF);
-            tma_load_3d(dst, &a.tmk, 0, row0, 0, bar);
-            tma_load_3d(dst + C::HALF, &a.tmv, 0, row0, 0, bar);
-          }
-        } else if constexpr (LD == kBulk) {
-          if (lane == i) {
-            // runs of rows that lie in one page
-            mbar_arrive_expect_tx(bar, uint32_t(rows) * 2 * C::ROW);
-            const uint32_t bytes = uint32_t(min(P - in0, rows)) * C::ROW;
-            bulk_load(dst, kp + at0, bytes, bar);
-            bulk_load(dst + C::HALF, vp + at0, bytes, bar);
-            if (starts) {
-#pragma unroll
-              for (int r = 1; r < TR; ++r) {
-                if (!(starts >> r & 1)) continue;
-                const uint32_t more = uint32_t(min(P, rows - r)) * C::ROW;
-                const int64_t at = page[r] * geo.page_stride + int64_t(u.g) * P * D;
-                bulk_load(dst + r * C::ROW, kp + at, more, bar);
-                bulk_load(dst + C::HALF + r * C::ROW, vp + at, more, bar);
-              }
+            for (int r = 1; r < TR; ++r) {
+              if (!(starts >> r & 1)) continue;
+              const uint32_t more = uint32_t(min(P, rows - r)) * C::ROW;
+              const int64_t at = page[r] * geo.page_stride + int64_t(u.g) * P * D;
+              bulk_load(dst + r * C::ROW, kp + at, more, bar);
+              bulk_load(dst + C::HALF + r * C::ROW, vp + at, more, bar);
             }
           }
-        } else {
-          // 16-byte chunks of single rows, in the layout that the maps' swizzle gives
-          constexpr int CH = C::ROW / 16;  // chunks of a row
-          if (pg < 0 || pg >= geo.n_pages) {
-            set_status(geo.status, SFI_DEV_BAD_INDEX);
-            pg = 0;
-          }
-          const int at = in < 0 ? -1 : int(pg * (geo.page_stride / D) + in);  // of the pool's rows, below 2^31
-          if (i + 1 < count) row_of(i + 1);
-#pragma unroll
-          for (int j = 0; j < TR * CH / 32; ++j) {
-            const int r = (j * 32 + lane) / CH, ch = lane % CH;
-            const int from_row = __shfl_sync(kFull, at, r);
-            const int64_t ra = int64_t(max(from_row, 0)) * D + ch * 8;
-            const uint32_t some = from_row >= 0 ? 16 : 0;
-            const uint32_t dr = dst + (ch / 8) * (TR * 128) + r * 128 + ((ch & 7) ^ (r & 7)) * 16;
-            cp_async16_zfill(dr, kp + ra, some);
-            cp_async16_zfill(dr + C::HALF, vp + ra, some);
-          }
-          cp_async_arrive_noinc(bar);
         }
+      } else {
+        // 16-byte chunks of single rows, in the layout that the maps' swizzle gives
+        constexpr int CH = C::ROW / 16;  // chunks of a row
+        if (pg < 0 || pg >= geo.n_pages) {
+          set_status(geo.status, SFI_DEV_BAD_INDEX);
+          pg = 0;
+        }
+        const int at = in < 0 ? -1 : int(pg * (geo.page_stride / D) + in);  // of the pool's rows, below 2^31
+        if (i + 1 < count) row_of(i + 1);
+#pragma unroll
+        for (int j = 0; j < TR * CH / 32; ++j) {
+          const int r = (j * 32 + lane) / CH, ch = lane % CH;
+          const int from_row = __shfl_sync(kFull, at, r);
+          const int64_t ra = int64_t(max(from_row, 0)) * D + ch * 8;
+          const uint32_t some = from_row >= 0 ? 16 : 0;
+          const uint32_t dr = dst + (ch / 8) * (TR * 128) + r * 128 + ((ch & 7) ^ (r & 7)) * 16;
+          cp_async16_zfill(dr, kp + ra, some);
+          cp_async16_zfill(dr + C::HALF, vp + ra, some);
+        }
+        cp_async_arrive_noinc(bar);
       }
-      __syncwarp();
     }
-    for (int w = 0; w < 2; ++w) done[w] += uint32_t(count_of(from, to, p + w * kProducers, kWarps));
+    __syncwarp();
   }
   // No copy may be in flight when the CTA exits: the attending warps wait for
   // every tile, unless one of these warps gave up (after seconds, in which all
@@ -438,9 +371,6 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
   if (tid < C::SLOTS) {
     mbar_init(smem_addr(&sh.full[tid]), LD == kCpAsync ? 32 : 1);
     mbar_init(smem_addr(&sh.empty[tid]), 1);
-  } else if (tid >= 64 && tid < 64 + kItemSlots) {
-    mbar_init(smem_addr(&sh.item_full[tid - 64]), 1);
-    mbar_init(smem_addr(&sh.item_empty[tid - 64]), kWarps + kProducers - 1);
   } else if (tid == 96) {
     mbar_init(smem_addr(&sh.merge_free), kWarps);
     sh.abort = 0;
@@ -462,11 +392,15 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
     for (int i = tid; i < G * D; i += kAllThreads) a.out[row * D + i] = 0.f;
     if (a.lse && tid < G) a.lse[row + tid] = -INFINITY;
   }
+  // this CTA's share of the line (a CTA beyond the shares has none)
   const Cut cut(total, gridDim.x);
+  const int share = blockIdx.x;
+  const long long from = share < cut.shares ? cut.start(share) : total;
+  const long long to = share < cut.shares ? cut.start(share + 1) : total;
 
   if (warp >= kWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
-    copy_tiles<T, D, NT, LD>(a, sh, cut, ring, warp - kWarps);
+    copy_tiles<T, D, NT, LD>(a, sh, from, to, ring, warp - kWarps);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAttendRegs));
     const float c = a.scale_log2;
@@ -503,14 +437,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
       }
       return min(geo.len[u.b], cap);
     };
-    for (int k = 0;; ++k) {
-      const int is = k % kItemSlots;
-      if (!warp_ctrl_wait(smem_addr(&sh.item_full[is]), (k / kItemSlots) & 1, &sh.abort, geo.status)) break;
-      const long long from = sh.item[is][0], to = sh.item[is][1];
-      const int place = sh.place[is];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sh.item_empty[is]));
-      if (from >= to) break;
+    if (from < to) {
       long long x = first_of(from, warp, kWarps);  // this warp's next tile
       Unit u = unit_at(from, ln, B, H_kv);
       int n = load_unit(u);
@@ -689,7 +616,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
           if (lane == 0) mbar_arrive(smem_addr(&sh.empty[slot]));
         }
 
-        // the next unit of the item; its queries are on their way during the merge
+        // the next unit of the share; its queries are on their way during the merge
         Unit next = u;
         do unit_next(next, ln, B, H_kv);
         while (next.begin < to && next.end == next.begin);
@@ -702,7 +629,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
         // more of them, and the next queries loaded behind it: 106 us against 84 for
         // 256 x 300 positions, 93 against 88 for 131072.)
         const bool alone = u.begin >= from && u.end <= to;  // the unit's only piece
-        float* const slot = a.partials + (place + b * H_kv + g) * int64_t(G) * (D + 2);
+        float* const slot = a.partials + (share + b * H_kv + g) * int64_t(G) * (D + 2);
 #pragma unroll
         for (int h0 = 0; h0 < C::HEADS; h0 += C::MH) {
           if (h0 >= G) break;

@@ -124,6 +124,8 @@ def test_largest_batch(sfi):
     (32, 8, 64, BF16, 20, [24001] * 4),              # shares in four parts, gathered rows
     (8, 8, 128, BF16, 64, [24576] * 12),             # the same by boxes, one head a group
     (2, 2, 64, F32, 16, [90000, 40003, 90001]),
+    (8, 2, 128, BF16, 16, [200000, 160001, 0, 280000]),  # the first in four parts, of more than 16 pieces
+    (8, 8, 128, BF16, 32, [16390] * 10),                 # and of a few
 ])
 def test_long_shares_are_cut_and_joined(sfi, hq, hkv, d, dtype, page, lens):
     """Lengths at which a CTA's share is cut into parts, and units into many pieces: the first,
