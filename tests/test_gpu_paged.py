@@ -121,14 +121,14 @@ def test_largest_batch(sfi):
 
 @pytest.mark.parametrize("hq,hkv,d,dtype,page,lens", [
     (4, 2, 64, BF16, 16, [70000, 8191, 0, 130001]),  # units of far more than 16 pieces
-    (32, 8, 64, BF16, 20, [24001] * 4),              # shares in four parts, gathered rows
+    (32, 8, 64, BF16, 20, [24001] * 4),              # several units a share, gathered rows
     (8, 8, 128, BF16, 64, [24576] * 12),             # the same by boxes, one head a group
     (2, 2, 64, F32, 16, [90000, 40003, 90001]),
-    (8, 2, 128, BF16, 16, [200000, 160001, 0, 280000]),  # the first in four parts, of more than 16 pieces
-    (8, 8, 128, BF16, 32, [16390] * 10),                 # and of a few
+    (8, 2, 128, BF16, 16, [200000, 160001, 0, 280000]),  # large shares, units of up to 34
+    (8, 8, 128, BF16, 32, [16390] * 10),                 # and of a few pieces
 ])
-def test_long_shares_are_cut_and_joined(sfi, hq, hkv, d, dtype, page, lens):
-    """Lengths at which a CTA's share is cut into parts, and units into many pieces: the first,
+def test_long_units_are_cut_and_joined(sfi, hq, hkv, d, dtype, page, lens):
+    """Lengths at which units are cut into many pieces, and shares hold several units: the first,
     a middle and the last sequence, and the first and last KV head of each."""
     c = Cache(hq, hkv, d, dtype, page, lens, seed=60)
     out, lse = c.run(sfi)
