@@ -343,7 +343,9 @@ sfi_status sfi_fast_attn_noalloc(const sfi_layout* layout, const sfi_params* par
  *  - total_q = 0 is a call that does nothing; total_k = 0 (k and v may then be
  *    NULL) gives every row no key.
  * The workspace (sfi_prefill_attn_workspace_size, 0 for invalid arguments)
- * follows the shared rules, and so do the waits (sfi_set_wait_limit). */
+ * follows the shared rules and serves every layout for which it is large enough; one
+ * that is large enough for both may serve this call and the paged ones in turn.
+ * The waits have the limit of sfi_set_wait_limit. */
 typedef struct {
   int32_t batch;
   int32_t n_q_heads;

@@ -136,7 +136,7 @@ struct PagedPlan {
 PagedPlan plan_paged(const sfi_paged_layout* L) {
   const size_t units = size_t(L->batch) * L->n_kv_heads, G = L->n_q_heads / L->n_kv_heads;
   PagedPlan p;
-  size_t off = 256;  // the status word
+  size_t off = 512;  // the status word, and the prompt attention's counters, which may share the workspace
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off += align256(bytes);

@@ -351,3 +351,29 @@ def test_prompt_to_tokens(sfi, page):
                 a, _, sc, sz = P.attend(f64(qt)[b, h], K[b][:, h // 4], V[b][:, h // 4], len(K[b]))
                 close(f64(o)[b, h], a, f32_tolerance(a, sc, np.array(sz), d, 100, True), f"step {step}")
     assert sfi.sfi_read_status(ws) == 0
+
+
+def test_one_workspace_for_prompts_and_tokens(sfi):
+    """Prompt attention and paged calls in turn on one workspace: neither spoils the other's."""
+    hq, hkv, d, page, lens = 8, 2, 128, 16, [3000, 700]
+    cu = offsets([400, 900, 37])
+    q, kn = normal((cu[-1], hq, d), BF16, 1), normal((cu[-1], hkv, d), BF16, 2)
+    prompts = sfi.PackedLayout(hq, hkv, d, BF16, ints(cu), ints(cu), cu[-1], cu[-1])
+    n_pages = sum(-(-n // page) for n in lens)
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda")
+    rows = torch.full((2, 200), -1, dtype=torch.int32, device="cuda")
+    rows[0, :188], rows[1, :44] = table[:188], table[188:]
+    lay = sfi.PagedLayout(hq, hkv, d, BF16, page, n_pages, rows, ints(lens))
+    k, v = normal((n_pages, hkv, page, d), BF16, 3), normal((n_pages, hkv, page, d), BF16, 4)
+    own = sfi.prefill_workspace(prompts), sfi.paged_workspace(lay)
+    both = torch.zeros(max(x.numel() for x in own), dtype=torch.uint8, device="cuda")
+    outs = []
+    for ws in (own, (both, both)):
+        for _ in range(3):
+            out, o = torch.full_like(q, 7.0), torch.full((2, hq, d), 7.0, device="cuda")
+            sfi.sfi_prefill_attn(prompts, q, kn, kn, out, None, ws[0])
+            sfi.sfi_paged_attn(lay, q[:2], k, v, o, None, ws[1])
+            outs.append((out, o))
+        assert sfi.sfi_read_status(ws[0]) == 0 and sfi.sfi_read_status(ws[1]) == 0
+    for out, o in outs[1:]:
+        assert torch.equal(out, outs[0][0]) and torch.equal(o, outs[0][1])
