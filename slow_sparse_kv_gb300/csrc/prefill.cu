@@ -18,7 +18,8 @@
 // row maxima take longer than the products.  Measured, 32 / 8 heads of 128: 16384
 // tokens in 1.32 ms (1.66 PFLOP/s; a library's matrix product reaches 1.88), 3
 // chunks of ~900 tokens after ~10000 in 309 us (1.46), 16 prompts of 260 to 4000
-// tokens in 312 us (1.30); with d = 64, 8192 tokens and 16 / 4 heads, 0.73.  A pair
+// tokens in 312 us (1.30); with d = 64, 0.73 (8192 tokens, 16 / 4 heads) to 0.96
+// (6 x 4096, 32 / 8).  A pair
 // of blocks takes 1.4 us, a tile's start and output another 2.  (A warpgroup of
 // its own for the output was tried: 176 registers for the softmax threads instead
 // of 216, and a tile's products wait for the output of both halves of the last
@@ -44,7 +45,8 @@ constexpr int kThreads = 384;  // 2 softmax warpgroups; a load, an MMA, a schedu
 constexpr int kRows = 128;     // query rows per tile
 constexpr int kKeys = 128;     // keys per block
 // P of a block is handed over in parts, the first 64 keys, then twice 32: the
-// products start early and the scores behind them wait for a short last part.
+// products start early and the scores behind them wait for a short last part.  (16
+// packed prompts: 218 us; in halves 224, 96 and 32 keys 226, whole 231.)
 constexpr int kParts = 3;
 __host__ __device__ constexpr int part_end(int part) { return part == 0 ? 64 : part == 1 ? 96 : kKeys; }
 constexpr float kGrow = 8.0f;  // growth of the maximum (log2) that moves m
