@@ -11,7 +11,7 @@
 // heads of 128 in pages of 16: 8 x 32768 positions (1.07 GB) in 164 us, 6.56 TB/s,
 // where a copy reaches 6.78; fp32, 4 x 32768, 164 us; 32 sequences of 4096 to
 // 65536 (2.57 GB) in 379 us, 6.79 TB/s; 256 x 300 (0.31 GB) in 70 us; one of 700 in
-// 9.9 us, the two launches.
+// 9.1 us, the two launches.
 //
 // What a CTA saw of one (sequence, KV head) is a piece, a softmax state (m, l,
 // o), merged over the warps through shared memory.  The only piece of its unit is
