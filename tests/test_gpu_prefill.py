@@ -266,3 +266,25 @@ def test_expanded_rows_are_refused(sfi):
               (q, k, k[:1].expand(9, 2, 64), out), (q, k, k, out[:1].expand(9, 4, 64))):
         with pytest.raises(ValueError):
             sfi.sfi_prefill_attn(lay, *a, None, ws)
+
+
+@pytest.mark.parametrize("hq,hkv", [(128, 8), (100, 10)])  # output by boxes, and by rows
+def test_offsets_past_32_bits(sfi, hq, hkv):
+    """A short sequence behind more than 2^31 elements of q and out, and of k and v by their strides."""
+    d, first, n = 128, (1 << 31) // (hq * 128) + 100, 150
+    cu, ck = [first, first + n], [70000, 70000 + n]
+    q = torch.empty(first + n + 3, hq, d, dtype=BF16, device="cuda")
+    wide = torch.empty(70000 + n, 40000, dtype=BF16, device="cuda")
+    k, v = (wide[:, i * hkv * d:(i + 1) * hkv * d].unflatten(1, (hkv, d)) for i in range(2))
+    qs, ks, vs = normal((n, hq, d), BF16, 1), normal((n, hkv, d), BF16, 2), normal((n, hkv, d), BF16, 3)
+    q[first:first + n], k[70000:], v[70000:] = qs, ks, vs
+    lay = sfi.PackedLayout(hq, hkv, d, BF16, ints(cu), ints(ck), q.shape[0], k.shape[0])
+    ws, out = sfi.prefill_workspace(lay), torch.full_like(q, 7.0)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    sfi.sfi_prefill_attn(lay, q, k, v, out, lse, ws)
+    assert sfi.sfi_read_status(ws) == 0
+    rows = np.array([0, 1, 63, 64, 127, 128, n - 1])
+    ref, rl, scale, size = P.prefill(f64(qs), f64(ks), f64(vs), [0, n], [0, n], set(rows.tolist()))
+    close(f64(out[first:first + n])[rows], ref[rows], bf16_tolerance(ref, scale, size, d)[rows], "out")
+    close_lse(f64(lse[first:first + n])[rows], rl[rows], size[rows], d)
+    assert bool((out[:first] == 7).all()) and bool((out[first + n:] == 7).all())
