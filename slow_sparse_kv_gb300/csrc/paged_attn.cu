@@ -9,7 +9,7 @@
 // times as long).  A tile's place in the line says which warp takes it.
 // Bound by HBM: 2 d e bytes a position and 4 d G flops, G <= 16.  Measured, 32 / 8
 // heads of 128 in pages of 16: 8 x 32768 positions (1.07 GB) in 164 us, 6.56 TB/s,
-// where a copy reaches 6.78; fp32, 4 x 32768, 164 us; 32 sequences of 4096 to
+// where a copy reaches 6.78; fp32, 4 x 32768, 165 us; 32 sequences of 4096 to
 // 65536 (2.57 GB) in 379 us, 6.79 TB/s; 256 x 300 (0.31 GB) in 70 us; one of 700 in
 // 9.1 us, the two launches.
 //
@@ -30,12 +30,16 @@
 // long chain of MMAs the output's error was 1.5e-6 at 700 positions and 4.3e-6 at
 // 32768).  tcgen05 would leave 128 - G of its 128 rows empty; the kernel waits for
 // HBM either way.
-// fp32: CUDA cores, d spread over the lanes, dots by transpose-reduction.
+// fp32: CUDA cores, d spread over the lanes, dots by transpose-reduction, products and
+// sums in pairs (f32x2; without: 4 x 32768, 16 heads a group 379 us against 349, 8 heads 194
+// against 180, d = 64 with 4 heads, 8 x 32768, 176 against 170; 4 heads of 128, which
+// HBM bounds, 161 against 165).
 #include <cuda_runtime.h>
 
 #include <atomic>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "paged.h"
 #include "pdl.cuh"
 
@@ -120,6 +124,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
+}
+
+// Four fp32 values of shared memory as two pairs.
+__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t& x, uint64_t& y) {
+  asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(addr));
 }
 
 // 16 bytes, of which `bytes` (0 or 16) are read and the rest are zero.
@@ -415,9 +424,10 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
     // the lane's part of a unit's queries, and the sequence's length
     uint32_t qb[F32 ? 1 : NT][KS][2];
     // (fp32 with more than 8 heads: both q and o would not fit, so the queries are read
-    // from L1 again for each tile: 379 us instead of 639 for 4 x 32768, 16 heads a group)
+    // from L1 again for each tile: 379 us instead of 639 for 4 x 32768, 16 heads a group,
+    // when that was measured)
     constexpr bool Q_REGS = NT == 1;
-    float qf[F32 && Q_REGS ? NS * 4 : 1][4];
+    uint64_t qf[F32 && Q_REGS ? NS * 4 : 1][2];
     auto load_unit = [&](const Unit& u) {
       const int64_t qrow = (int64_t(u.b) * a.H_q + int64_t(u.g) * G) * D;
       if constexpr (!F32) {
@@ -434,9 +444,9 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
       } else if constexpr (Q_REGS) {
 #pragma unroll
         for (int h = 0; h < NS * 4; ++h) {
-          float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (h < G) w = reinterpret_cast<const float4*>(static_cast<const T*>(a.q) + qrow + h * D)[li];
-          qf[h][0] = w.x, qf[h][1] = w.y, qf[h][2] = w.z, qf[h][3] = w.w;
+          ulonglong2 w = make_ulonglong2(0, 0);
+          if (h < G) w = reinterpret_cast<const ulonglong2*>(static_cast<const T*>(a.q) + qrow + h * D)[li];
+          qf[h][0] = w.x, qf[h][1] = w.y;
         }
       }
       return min(geo.len[u.b], cap);
@@ -458,7 +468,8 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
 #pragma unroll
           for (int e = 0; e < NE; ++e) m[h][e] = -INFINITY, l[h][e] = 0.f;
 
-        float o[F32 ? 1 : KS][F32 ? 1 : NT][4], of[F32 ? NS * 4 : 1][4];
+        float o[F32 ? 1 : KS][F32 ? 1 : NT][4];
+        uint64_t of[F32 ? NS * 4 : 1][2];  // fp32: a pair of dimensions each
         if constexpr (!F32) {
 #pragma unroll
           for (int kk = 0; kk < KS; ++kk)
@@ -468,9 +479,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
               for (int e = 0; e < 4; ++e) o[kk][h][e] = 0.f;
         } else {
 #pragma unroll
-          for (int h = 0; h < NS * 4; ++h)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) of[h][e] = 0.f;
+          for (int h = 0; h < NS * 4; ++h) of[h][0] = of[h][1] = 0;
         }
 
         for (; x < pe; x += kWarps) {
@@ -571,26 +580,27 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
             for (int h = 0; h < NS; ++h) {
               if (h * 4 >= G) break;
               float v[PASS * 4];
-              float qt[4][4];
+              uint64_t qt[4][2];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 if constexpr (Q_REGS) {
-#pragma unroll
-                  for (int y = 0; y < 4; ++y) qt[e][y] = qf[h * 4 + e][y];
+                  qt[e][0] = qf[h * 4 + e][0], qt[e][1] = qf[h * 4 + e][1];
                 } else {
-                  float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-                  if (h * 4 + e < G) w = reinterpret_cast<const float4*>(static_cast<const T*>(a.q) + qrow + (h * 4 + e) * D)[li];
-                  qt[e][0] = w.x, qt[e][1] = w.y, qt[e][2] = w.z, qt[e][3] = w.w;
+                  ulonglong2 w = make_ulonglong2(0, 0);
+                  if (h * 4 + e < G)
+                    w = reinterpret_cast<const ulonglong2*>(static_cast<const T*>(a.q) + qrow + (h * 4 + e) * D)[li];
+                  qt[e][0] = w.x, qt[e][1] = w.y;
                 }
               }
 #pragma unroll
               for (int i = 0; i < PASS; ++i) {
-                const uint4 w = lds128(ks + (i * RPP + half) * C::ROW + li * 16);
-                const float k0 = __uint_as_float(w.x), k1 = __uint_as_float(w.y), k2 = __uint_as_float(w.z),
-                            k3 = __uint_as_float(w.w);
+                uint64_t k0, k1;
+                lds_pairs(ks + (i * RPP + half) * C::ROW + li * 16, k0, k1);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  v[i * 4 + e] = k0 * qt[e][0] + k1 * qt[e][1] + k2 * qt[e][2] + k3 * qt[e][3];
+                for (int e = 0; e < 4; ++e) {
+                  const uint64_t t = fma2(k1, qt[e][1], mul2(k0, qt[e][0]));
+                  v[i * 4 + e] = lo(t) + hi(t);
+                }
               }
               // lane li of a row group: the dot of pass li / 4 and head 4 h + li % 4
               transpose_reduce<LPR>(v, li);
@@ -607,23 +617,22 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const float fe = __shfl_sync(kFull, f, e);
-#pragma unroll
-                  for (int y = 0; y < 4; ++y) of[h * 4 + e][y] *= fe;
+                  of[h * 4 + e][0] = mul2(of[h * 4 + e][0], pair(fe, fe));
+                  of[h * 4 + e][1] = mul2(of[h * 4 + e][1], pair(fe, fe));
                 }
               }
               const float p = ex2(fmaf(s, c, -(m[h][0] == -INFINITY ? 0.f : m[h][0] * c)));
               l[h][0] += p;
 #pragma unroll
               for (int i = 0; i < PASS; ++i) {
-                uint4 w = lds128(vs + (i * RPP + half) * C::ROW + li * 16);
-                if (i * RPP + half >= left) w = make_uint4(0, 0, 0, 0);  // 0 * NaN is not 0
+                uint64_t v0, v1;
+                lds_pairs(vs + (i * RPP + half) * C::ROW + li * 16, v0, v1);
+                if (i * RPP + half >= left) v0 = v1 = 0;  // 0 * NaN is not 0
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const float pe_ = __shfl_sync(kFull, p, half * LPR + i * 4 + e);
-                  of[h * 4 + e][0] = fmaf(pe_, __uint_as_float(w.x), of[h * 4 + e][0]);
-                  of[h * 4 + e][1] = fmaf(pe_, __uint_as_float(w.y), of[h * 4 + e][1]);
-                  of[h * 4 + e][2] = fmaf(pe_, __uint_as_float(w.z), of[h * 4 + e][2]);
-                  of[h * 4 + e][3] = fmaf(pe_, __uint_as_float(w.w), of[h * 4 + e][3]);
+                  of[h * 4 + e][0] = fma2(pair(pe_, pe_), v0, of[h * 4 + e][0]);
+                  of[h * 4 + e][1] = fma2(pair(pe_, pe_), v1, of[h * 4 + e][1]);
                 }
               }
             }
@@ -679,8 +688,9 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
             for (int e = 0; e < 4; ++e) {
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
-                if (RPP == 2) of[h * 4 + e][y] += __shfl_xor_sync(kFull, of[h * 4 + e][y], 16);
-                if (half == 0) mine[e * C::MROW + li * 4 + y] = of[h * 4 + e][y];
+                float x_ = y & 1 ? hi(of[h * 4 + e][y / 2]) : lo(of[h * 4 + e][y / 2]);
+                if (RPP == 2) x_ += __shfl_xor_sync(kFull, x_, 16);
+                if (half == 0) mine[e * C::MROW + li * 4 + y] = x_;
               }
             }
           }

@@ -34,6 +34,7 @@
 
 #include <atomic>
 
+#include "f32x2.cuh"
 #include "pdl.cuh"
 #include "prefill.h"
 #include "tc5.cuh"
@@ -120,25 +121,6 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   float m;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
   return m;
-}
-
-// Two fp32 values in one 64-bit register, and the packed arithmetic on them.
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-  uint64_t p;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
-  return p;
-}
-__device__ __forceinline__ float lo(uint64_t p) { return __uint_as_float(uint32_t(p)); }
-__device__ __forceinline__ float hi(uint64_t p) { return __uint_as_float(uint32_t(p >> 32)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
-  return d;
 }
 
 // Part H of a block's probabilities: p = 2^(c s - c m) summed in fp32 (four
