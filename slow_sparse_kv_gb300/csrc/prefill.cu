@@ -158,29 +158,43 @@ __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
 // tiles start first; within a level by sequence, and the KV heads of a tile are
 // neighbours.  A CTA asks for growing ranks, so the walk goes on from where it
 // stood.
+struct Seq {
+  int q0, nq, k0, nk;  // first row and rows, of q and of k
+};
 struct Ranks {
   const PrefillArgs& a;
   // (up to 32 sequences stay in registers, a lane each: reading them back from
-  // memory for every step of the search took 10 to 15 us at a kernel's start)
+  // memory for every step of the search took 10 to 15 us at a kernel's start, and for
+  // a tile's offsets another 0.4)
+  Seq one = {0, 0, 0, 0};
   int span1 = 0, lvl1 = 0;
+  bool bad = false;  // this lane's offsets are out of order
   int level, before, here;  // the level it stands at, tiles above it and on it
 
   // Stands above the highest level.
   __device__ __forceinline__ explicit Ranks(const PrefillArgs& a_) : a(a_) {
     const int lane = threadIdx.x & 31;
-    if (a.B <= 32 && lane < a.B) sequence(a, lane, &span1, &lvl1);
+    if (a.B <= 32 && lane < a.B) bad = !sequence(a, lane, &one, &span1, &lvl1);
     int t = 0;
     each([&](int, int span, int lvl) { t = max(t, span > 0 ? lvl + span : 0); });
     level = __reduce_max_sync(kFull, t);
     before = here = 0;
   }
-  // CTA tiles and first level of sequence b; false if its offsets are out of order
-  static __device__ __forceinline__ bool sequence(const PrefillArgs& a, int b, int* span, int* lvl) {
+  // rows, CTA tiles and first level of sequence b; false if its offsets are out of order
+  static __device__ __forceinline__ bool sequence(const PrefillArgs& a, int b, Seq* s, int* span, int* lvl) {
     const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1], tokens = 2 * a.tok;
     const bool ok = q0 >= 0 && q0 <= q1 && q1 <= a.total_q && k0 >= 0 && k0 <= k1 && k1 <= a.total_k;
+    *s = Seq{q0, q1 - q0, k0, k1 - k0};
     *span = ok ? (q1 - q0 + tokens - 1) / tokens : 0;
     *lvl = ok ? max(0, (k1 - k0) - (q1 - q0)) / tokens : 0;
     return ok;
+  }
+  // the rows of sequence b, one that is in order
+  __device__ __forceinline__ Seq rows_of(int b) const {
+    if (a.B <= 32)
+      return Seq{__shfl_sync(kFull, one.q0, b), __shfl_sync(kFull, one.nq, b), __shfl_sync(kFull, one.k0, b),
+                 __shfl_sync(kFull, one.nk, b)};
+    return Seq{a.cu_q[b], a.cu_q[b + 1] - a.cu_q[b], a.cu_k[b], a.cu_k[b + 1] - a.cu_k[b]};
   }
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
@@ -229,15 +243,14 @@ struct Ranks {
   }
 };
 
-__device__ __forceinline__ Tile make_tile(const PrefillArgs& a, int g, int seq, int tile) {
+__device__ __forceinline__ Tile make_tile(const PrefillArgs& a, int g, const Seq& seq, int tile) {
   Tile t;
-  const int span = 2 * a.tok, first = tile * span;
-  const int q0 = a.cu_q[seq], nq = a.cu_q[seq + 1] - q0;
+  const int span = 2 * a.tok, first = tile * span, nq = seq.nq;
   t.g = g;
-  t.k0 = a.cu_k[seq];
-  t.nk = a.cu_k[seq + 1] - t.k0;
+  t.k0 = seq.k0;
+  t.nk = seq.nk;
   t.slot = -1;
-  t.q0 = q0 + first;
+  t.q0 = seq.q0 + first;
   t.rows = min(span, nq - first);
   t.seen = t.nk - nq + first + 1;
 #pragma unroll
@@ -259,8 +272,7 @@ struct Split {
   int tiles, parts;
 };
 
-__device__ __forceinline__ Split split_of(const PrefillArgs& a, int grid) {  // one warp
-  Ranks r(a);
+__device__ __forceinline__ Split split_of(const PrefillArgs& a, Ranks r, int grid) {  // one warp
   Split s;
   s.total = s.first = (long long)r.from(0) * a.H_kv;
   s.tiles = 0;
@@ -271,9 +283,9 @@ __device__ __forceinline__ Split split_of(const PrefillArgs& a, int grid) {  // 
   if (rest == 0) return s;
   int seq = 0, tile = 0;
   r.find(0, &seq, &tile);
-  const Tile longest = make_tile(a, 0, seq, tile);
+  const Tile longest = make_tile(a, 0, r.rows_of(seq), tile);
   r.find(int(uint32_t(s.total - 1) / uint32_t(a.H_kv)), &seq, &tile);
-  const Tile shortest = make_tile(a, 0, seq, tile);
+  const Tile shortest = make_tile(a, 0, r.rows_of(seq), tile);
   const int most = max(longest.n[0], longest.n[1]), least = max(shortest.n[0], shortest.n[1]);
   if (s.total > grid && 2 * least < most) return s;
   const int parts = min(min(kMaxParts, grid / rest), (s.total > grid ? least : most) / 4);
@@ -335,13 +347,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   }
   pdl_launch();
   pdl_wait();
-  if (blockIdx.x == 0 || a.B > 32)
+  if (a.B > 32)
     for (int b = tid; b < a.B; b += kThreads) {
+      Seq seq;
       int span, lvl;
-      const bool ok = Ranks::sequence(a, b, &span, &lvl);
+      const bool ok = Ranks::sequence(a, b, &seq, &span, &lvl);
       if (!ok && blockIdx.x == 0) set_status(a.status, SFI_DEV_LEN_OVER_CAP);
       // (every CTA writes the same values and reads its own)
-      if (a.B > 32) a.span[b] = span, a.lvl[b] = lvl;
+      a.span[b] = span, a.lvl[b] = lvl;
     }
   __syncthreads();
   tc5::fence_after();
@@ -479,9 +492,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     } else if (warp == 10) {
       // ---- which tiles: the CTA's own index first, then by a shared counter
       long long rank = blockIdx.x;
-      const Split split = split_of(a, gridDim.x);
-      if (blockIdx.x == 0 && lane == 0 && a.partials != nullptr) a.cut_count[0] = split.tiles, a.cut_count[1] = split.parts;
       Ranks ranks(a);
+      const Split split = split_of(a, ranks, gridDim.x);
+      if (blockIdx.x == 0 && lane == 0 && a.partials != nullptr) a.cut_count[0] = split.tiles, a.cut_count[1] = split.parts;
+      if (blockIdx.x == 0 && ranks.bad) set_status(a.status, SFI_DEV_LEN_OVER_CAP);
       for (int k = 0;; ++k) {
         Tile t;
         t.rows = 0;
@@ -491,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           const int whole = int(rank < split.first ? rank : split.first + cut / split.parts);
           int seq = 0, tile = 0;
           ranks.find(whole / a.H_kv, &seq, &tile);
-          t = make_tile(a, whole % a.H_kv, seq, tile);
+          t = make_tile(a, whole % a.H_kv, ranks.rows_of(seq), tile);
           if (rank >= split.first) {
             if (lane == 0 && cut % split.parts == 0) a.cuts[cut / split.parts] = t;
             take_part(t, cut % split.parts, split.parts, cut);
