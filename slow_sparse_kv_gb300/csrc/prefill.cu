@@ -797,7 +797,13 @@ cudaError_t launch_t(const PrefillArgs& a, cudaStream_t st) {
   const long long least = (long long)a.total_q / (2 * a.tok) * a.H_kv, most = least + (long long)a.B * a.H_kv;
   const int sms = device_sm_count() < kPrefillMaxGrid ? device_sm_count() : kPrefillMaxGrid;
   PrefillArgs b = a;
-  if (least >= (long long)kSplitWaves * sms) b.partials = nullptr;
+  // No tile is cut, and no joining kernel needed (45 -> 40 us for 2048 tokens), with
+  //  - many waves of tiles;
+  //  - one wave that takes more than half of the SMs: no tile would get two;
+  //  - more tiles than SMs and no more keys than queries: some sequence has no context,
+  //    and its first tile is too short to be cut with the others.
+  if (least >= (long long)kSplitWaves * sms || (2 * least > sms && (most <= sms || a.total_k <= a.total_q)))
+    b.partials = nullptr;
   // (which tiles are cut depends on the grid: the SMs' number wherever some may be)
   const int grid = b.partials != nullptr || most > sms ? sms : int(most);
   const cudaError_t e2 = launch_pdl(prefill_kernel<D>, dim3(grid), kThreads, Cfg<D>::SMEM, st, b);
