@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant
   const int row = i * a.tok + tt;
   if (tt >= a.tok || row >= t.rows) return;
   // (after a wait that gave up, the tile may be one that an earlier call left)
-  if (t.q0 < 0 || t.q0 + row >= a.total_q || t.g < 0 || t.g >= a.H_kv || parts > kMaxParts) return;
+  if (t.q0 < 0 || t.q0 >= a.total_q - row || t.g < 0 || t.g >= a.H_kv || parts > kMaxParts) return;
   const float* const p = slot_of<D>(a, blockIdx.x * parts) + at;
   constexpr int64_t STEP = 2 * kRows * (D + 2);
   float f[kMaxParts], M = -INFINITY, L = 0.f;
