@@ -72,7 +72,14 @@ constexpr int kTileReaders = 11;  // loads, MMAs, the cleaning warp, 8 softmax w
 
 struct Shared {
   uint64_t q_full[2], q_empty[2], s_full[2], o_full[2], p_ready[2][kParts], tile_full[2], tile_empty[2];
-  uint64_t kv_full[6], kv_empty[6], v_clean, drained;
+  uint64_t kv_full[6], kv_empty[6], drained;
+  // The cleaned last V blocks, one barrier after the other: the cleaning warp may be
+  // done with two tiles of which the MMA lane has waited for neither (a short one
+  // behind another, both in the ring), and a barrier two phases ahead looks like one
+  // that is still to come.  More than two it cannot be ahead: a tile is handed out when
+  // the one two before it has been given back by the softmax warps, behind its output
+  // and so behind the products with its last V block.
+  uint64_t v_clean[2];
   Tile tile[2];
   uint32_t tmem;
   volatile int abort;
@@ -337,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         mbar_init(smem_addr(&sh.kv_full[i]), 1);
         mbar_init(smem_addr(&sh.kv_empty[i]), 2);  // its last product, and the cleaning warp
       }
-      mbar_init(smem_addr(&sh.v_clean), 1);
+      for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&sh.v_clean[i]), 1);
       mbar_init(smem_addr(&sh.drained), 1);
       fence_mbar_init();
     }
@@ -450,7 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             if (i == 1 || t.n[1] == 0) tc5::commit(smem_addr(&sh.kv_empty[stage(x)]));
           }
           auto v_landed = [&](int j, int y) {
-            return (j + 1) * kKeys > t.nk ? wait_for(&sh.v_clean, cleaned++) : full(y);
+            if ((j + 1) * kKeys <= t.nk) return full(y);
+            const int c = cleaned++;
+            return wait_for(&sh.v_clean[c & 1], c >> 1);
           };
           for (int j = 0; j < n && ok; ++j, x += 2) {
             ok = v_landed(j, x + 1);
@@ -529,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     } else if (warp == 11) {
       // ---- the rows of a sequence's last V block that lie behind it belong to
       // nobody or to the next one: P is zero there, but 0 * NaN is not
-      int x = 0;
+      int x = 0, cleaned = 0;
       bool ok = true;
       Tile t;
       for (int k = 0; ok && __all_sync(kFull, take(k, t)); ++k) {
@@ -548,7 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                              : "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.v_clean));
+            if (lane == 0) mbar_arrive(smem_addr(&sh.v_clean[cleaned & 1]));
+            ++cleaned;
           }
           if (lane == 0) mbar_arrive(smem_addr(&sh.kv_empty[stage(x)]));
         }
