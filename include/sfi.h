@@ -387,7 +387,10 @@ sfi_status sfi_prefill_attn(const sfi_packed_layout* layout, const void* q, cons
  *    is (the others); a page outside [0, n_pages) sets SFI_DEV_BAD_INDEX and is
  *    read as page 0, and never written.
  * One workspace (sfi_paged_workspace_size, 0 for invalid arguments) serves all
- * calls of a geometry and follows the shared rules. */
+ * calls of a geometry and follows the shared rules.  Flags other than
+ * SFI_DEV_WAIT_TIMEOUT leave it ready for the next call as it is.  It remembers which
+ * sequences sfi_pages_extend refused (for sfi_paged_append; zero-filled, it has
+ * forgotten), so caches with tables of their own have workspaces of their own too. */
 typedef struct {
   int32_t batch;
   int32_t n_q_heads; /* read by sfi_paged_attn only; a multiple of n_kv_heads */
@@ -428,7 +431,10 @@ sfi_status sfi_paged_attn(const sfi_paged_layout* layout, const void* q, const v
  * be NULL: one row per sequence, total_new = B.  A sequence whose rows leave
  * [0, total_new] or outnumber len[b] is flagged (SFI_DEV_LEN_OVER_CAP) and left
  * out; with cu_new NULL one with len[b] = 0 is an idle slot, whose row is not
- * stored.  k_new and v_new are 16-byte aligned and apart from the pool.  The rows
+ * stored.  A sequence that sfi_pages_extend refused on this workspace, and that has
+ * rows to store, is flagged (SFI_DEV_NO_PAGES) and left out until an extension serves it
+ * or it is freed: its length does not count the rows, which would go over its last ones.
+ * k_new and v_new are 16-byte aligned and apart from the pool.  The rows
  * go to the pages that the table names, whoever else holds them: only positions
  * added by the last sfi_pages_extend are sure to be the sequence's own. */
 sfi_status sfi_paged_append(const sfi_paged_layout* layout, int32_t total_new, const void* k_new,
@@ -457,7 +463,8 @@ typedef struct {
  * anything), with pages for the positions that need new ones.  Sequences are
  * served in order; one that needs more pages than are left, or more entries
  * than its row has, stays as it is and sets SFI_DEV_NO_PAGES; a negative n_new
- * sets SFI_DEV_LEN_OVER_CAP. */
+ * sets SFI_DEV_LEN_OVER_CAP.  sfi_paged_append on the same workspace leaves out the
+ * sequences that stayed as they were, so the two may follow each other unseen. */
 sfi_status sfi_pages_extend(const sfi_paged_layout* layout, const sfi_page_store* store,
                             const int32_t* n_new, void* ws, size_t ws_bytes, sfi_stream stream);
 

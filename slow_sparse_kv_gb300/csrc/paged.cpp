@@ -17,6 +17,8 @@ namespace {
 // The prompt attention's workspace: the status word, the counters of the tiles, two
 // numbers for each sequence, and where tiles may be cut along their keys, the
 // states of their parts.
+// (Bytes 384 to 512 belong to the paged calls, which may use the same workspace.)
+constexpr size_t kRefusedAt = 384;
 constexpr size_t kPrefillWs = 512 + 8 * kMaxBatch;
 constexpr size_t kCutWs = 256 + kPrefillMaxGrid * 64;  // the cut tiles
 static_assert(sizeof(PrefillTile) <= 64, "kCutWs");
@@ -136,7 +138,10 @@ struct PagedPlan {
 PagedPlan plan_paged(const sfi_paged_layout* L) {
   const size_t units = size_t(L->batch) * L->n_kv_heads, G = L->n_q_heads / L->n_kv_heads;
   PagedPlan p;
-  size_t off = 512;  // the status word, and the prompt attention's counters, which may share the workspace
+  // the status word, the prompt attention's counters, which may share the workspace, and
+  // the bits of the refused sequences, which it leaves alone
+  static_assert(kRefusedAt % 4 == 0 && kRefusedAt + kMaxBatch / 8 <= 512, "refused");
+  size_t off = 512;
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off += align256(bytes);
@@ -154,7 +159,8 @@ PagedPlan plan_paged(const sfi_paged_layout* L) {
 
 PagedGeo geo_of(const sfi_paged_layout* L, void* ws) {
   return PagedGeo{L->batch,  L->n_kv_heads, L->page_size, L->n_pages,
-                  L->max_pages, page_elems(L), L->page_table, L->len, static_cast<uint32_t*>(ws)};
+                  L->max_pages, page_elems(L), L->page_table, L->len, static_cast<uint32_t*>(ws),
+                  reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + kRefusedAt)};
 }
 
 sfi_status check_store(const sfi_paged_layout* L, const sfi_page_store* S, bool rows) {

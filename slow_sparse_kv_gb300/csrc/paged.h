@@ -15,6 +15,7 @@ struct PagedGeo {
   int32_t* table;
   int32_t* len;
   uint32_t* status;
+  uint32_t* refused;  // a bit for each sequence that an extension left as it was
 };
 
 struct PagedAttnArgs {

@@ -77,6 +77,9 @@ __device__ __forceinline__ int find_free(const int32_t* ref, int n_pages, long l
 
 __device__ __forceinline__ int pages_of(int n, int P) { return n / P + (n % P != 0); }
 
+// Sequence b is no longer one that an extension refused.
+__device__ __forceinline__ void forget_refusal(const PagedGeo& g, int b) { atomicAnd(g.refused + (b >> 5), ~(1u << (b & 31))); }
+
 __global__ void __launch_bounds__(kPlan) extend_kernel(PagedGeo g, int32_t* ref, const int32_t* n_new,
                                                        int32_t* fresh) {
   __shared__ long long part[32];
@@ -126,6 +129,9 @@ __global__ void __launch_bounds__(kPlan) extend_kernel(PagedGeo g, int32_t* ref,
   }
   if (b < g.B && more > 0) g.len[b] = n + more;
   if (flags) set_status(g.status, flags);
+  // whom an append has to leave out: who asked and was refused, until it is served
+  const uint32_t bad = __ballot_sync(kFull, flags != 0), served = __ballot_sync(kFull, more > 0);
+  if (lane == 0 && (bad | served)) g.refused[warp] = (g.refused[warp] & ~served) | bad;
   for (int s = warp; s < g.B; s += kPlan / 32)
     for (int i = lane; i < need[s]; i += 32) {
       const int p = fresh[at[s] + i];
@@ -173,7 +179,7 @@ __global__ void __launch_bounds__(kPlan) fork_kernel(PagedGeo g, int32_t* ref, c
       ref[to] = 1;
     }
     jobs[i] = job;
-    if (in) g.len[t] = len;
+    if (in) g.len[t] = len, forget_refusal(g, t);
     if (flags) set_status(g.status, flags);
   }
   __syncthreads();
@@ -211,7 +217,7 @@ __global__ void __launch_bounds__(kCopy) free_kernel(PagedGeo g, int32_t* ref, c
     if (bad) set_status(g.status, SFI_DEV_BAD_INDEX);
   }
   __syncthreads();
-  if (threadIdx.x == 0) g.len[b] = 0;
+  if (threadIdx.x == 0) g.len[b] = 0, forget_refusal(g, b);
 }
 
 // x / y for 0 <= x, 0 < y: in 32 bits where they do (a tenth of the time).
@@ -366,7 +372,9 @@ __global__ void __launch_bounds__(kCopy) compact_kernel(const __grid_constant__ 
   }
 }
 
-// New rows into their pages: a warp takes one token's K and V.
+// New rows into their pages: a warp takes one token's K and V.  A sequence that an
+// extension refused holds the length from before it: the rows would go over its last
+// ones, which may lie in pages that others share, so it is left out.
 __global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ AppendArgs a) {
   const PagedGeo& g = a.geo;
   pdl_launch();
@@ -376,12 +384,13 @@ __global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ A
     // every sequence's rows and length, once
     for (int b = threadIdx.x; b < g.B; b += kCopy) {
       const int n = g.len[b];
-      bool bad = n < 0 || n > cap;
+      bool bad = n < 0 || n > cap, refused = g.refused[b >> 5] >> (b & 31) & 1;
       if (a.cu) {
         const int c0 = a.cu[b], c1 = a.cu[b + 1];
-        bad = bad || c0 < 0 || c1 < c0 || c1 > a.total || c1 - c0 > n;
+        refused = refused && c0 < c1;
+        bad = bad || c0 < 0 || c1 < c0 || c1 > a.total || (c1 - c0 > n && !refused);
       }
-      if (bad) set_status(g.status, SFI_DEV_LEN_OVER_CAP);
+      if (bad || refused) set_status(g.status, (bad ? SFI_DEV_LEN_OVER_CAP : 0u) | (refused ? SFI_DEV_NO_PAGES : 0u));
     }
   }
   const int t = blockIdx.x * (kCopy / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -398,7 +407,7 @@ __global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ A
     if (c0 < 0 || t < c0 || t >= c1 || c1 > a.total) return;
   }
   const int n = g.len[b];
-  if (n < 0 || n > cap || c1 - c0 > n) return;
+  if (n < 0 || n > cap || c1 - c0 > n || (g.refused[b >> 5] >> (b & 31) & 1)) return;
   const int pos = n - (c1 - t);
   const int page = g.table[int64_t(b) * g.max_pages + pos / g.P];
   if (page < 0 || page >= g.n_pages) {
