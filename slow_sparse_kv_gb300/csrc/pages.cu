@@ -372,43 +372,12 @@ __global__ void __launch_bounds__(kCopy) compact_kernel(const __grid_constant__ 
   }
 }
 
-// New rows into their pages: a warp takes one token's K and V.  A sequence that an
-// extension refused holds the length from before it: the rows would go over its last
-// ones, which may lie in pages that others share, so it is left out.
-__global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ AppendArgs a) {
+// Row t of the new ones, the `back`-th last of the m of sequence b, by one warp.
+__device__ __forceinline__ void append_row(const AppendArgs& a, int b, int m, int back, int t, int cap, int lane) {
   const PagedGeo& g = a.geo;
-  pdl_launch();
-  pdl_wait();
-  const int cap = g.max_pages * g.P;
-  if (blockIdx.x == 0) {
-    // every sequence's rows and length, once
-    for (int b = threadIdx.x; b < g.B; b += kCopy) {
-      const int n = g.len[b];
-      bool bad = n < 0 || n > cap, refused = g.refused[b >> 5] >> (b & 31) & 1;
-      if (a.cu) {
-        const int c0 = a.cu[b], c1 = a.cu[b + 1];
-        refused = refused && c0 < c1;
-        bad = bad || c0 < 0 || c1 < c0 || c1 > a.total || (c1 - c0 > n && !refused);
-      }
-      if (bad || refused) set_status(g.status, (bad ? SFI_DEV_LEN_OVER_CAP : 0u) | (refused ? SFI_DEV_NO_PAGES : 0u));
-    }
-  }
-  const int t = blockIdx.x * (kCopy / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (t >= a.total) return;
-  int b = t, c0 = t, c1 = t + 1;
-  if (a.cu) {
-    int lo = 0, hi = g.B;  // last b with cu[b] <= t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.cu[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    b = lo, c0 = a.cu[b], c1 = a.cu[b + 1];
-    if (c0 < 0 || t < c0 || t >= c1 || c1 > a.total) return;
-  }
   const int n = g.len[b];
-  if (n < 0 || n > cap || c1 - c0 > n || (g.refused[b >> 5] >> (b & 31) & 1)) return;
-  const int pos = n - (c1 - t);
+  if (n < 0 || n > cap || m > n || (g.refused[b >> 5] >> (b & 31) & 1)) return;
+  const int pos = n - back;
   const int page = g.table[int64_t(b) * g.max_pages + pos / g.P];
   if (page < 0 || page >= g.n_pages) {
     if (lane == 0) set_status(g.status, SFI_DEV_BAD_INDEX);
@@ -435,6 +404,68 @@ __global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ A
   }
 }
 
+// New rows into their pages: a warp takes one token's K and V, for each sequence that
+// holds the token: one, where the offsets ascend; where some do not, those that are in
+// order are stored all the same, so all pairs are looked through (by each warp for its
+// token up to 32 sequences, else by the CTA for its eight; a search by halves would miss
+// some).  A sequence that an extension refused holds the length from before it: the rows would go over its last
+// ones, which may lie in pages that others share, so it is left out.
+__global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kWarps = kCopy / 32;
+  __shared__ uint32_t mask[kMaxBatch / 32];  // sequences with rows among the CTA's tokens
+  static_assert(kMaxBatch / 32 == 32, "a lane for every word");
+  const PagedGeo& g = a.geo;
+  pdl_launch();
+  pdl_wait();
+  const int cap = g.max_pages * g.P;
+  if (blockIdx.x == 0) {
+    // every sequence's rows and length, once
+    for (int b = threadIdx.x; b < g.B; b += kCopy) {
+      const int n = g.len[b];
+      bool bad = n < 0 || n > cap, refused = g.refused[b >> 5] >> (b & 31) & 1;
+      if (a.cu) {
+        const int c0 = a.cu[b], c1 = a.cu[b + 1];
+        refused = refused && c0 < c1;
+        bad = bad || c0 < 0 || c1 < c0 || c1 > a.total || (c1 - c0 > n && !refused);
+      }
+      if (bad || refused) set_status(g.status, (bad ? SFI_DEV_LEN_OVER_CAP : 0u) | (refused ? SFI_DEV_NO_PAGES : 0u));
+    }
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t0 = blockIdx.x * kWarps, t = t0 + warp;
+  if (!a.cu) {
+    if (t < a.total) append_row(a, t, 1, 1, t, cap, lane);
+    return;
+  }
+  // of the pairs that are in order, does b's hold some of the rows [from, from + n)?
+  auto holds = [&](int b, int from, int n) {
+    if (b >= g.B) return false;
+    const int c0 = a.cu[b], c1 = a.cu[b + 1];
+    return c0 >= 0 && c1 <= a.total && c0 < c1 && c0 - from < n && c1 > from;
+  };
+  uint32_t word;  // the lane's 32 sequences
+  if (g.B <= 32) {
+    const uint32_t in = __ballot_sync(kFull, holds(lane, t, 1));
+    word = lane == 0 ? in : 0;
+  } else {
+#pragma unroll
+    for (int w = warp; w < 32; w += kWarps) {
+      const uint32_t in = __ballot_sync(kFull, holds(w * 32 + lane, t0, kWarps));
+      if (lane == 0) mask[w] = in;
+    }
+    __syncthreads();
+    word = mask[lane];
+  }
+  if (t >= a.total) return;
+  for (uint32_t words = __ballot_sync(kFull, word != 0); words; words &= words - 1) {
+    const int w = __ffs(words) - 1;
+    for (uint32_t bits = __shfl_sync(kFull, word, w); bits; bits &= bits - 1) {
+      const int b = w * 32 + __ffs(bits) - 1, c0 = a.cu[b], c1 = a.cu[b + 1];
+      if (t >= c0 && t < c1) append_row(a, b, c1 - c0, c1 - t, t, cap, lane);
+    }
+  }
+}
+
 // CTAs of a copy of at most `items` slices: eight to an SM keep HBM busy.
 int copy_grid(long long items) {
   const long long most = 8LL * device_sm_count();
@@ -448,7 +479,7 @@ long long page_slices(const PageMove& mv) {
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
-  return launch_pdl(append_kernel, dim3((a.total + kCopy / 32 - 1) / (kCopy / 32)), kCopy, 0, st, a);
+  return launch_pdl(append_kernel, dim3((a.total - 1) / (kCopy / 32) + 1), kCopy, 0, st, a);
 }
 
 cudaError_t launch_extend(const PagedGeo& g, int32_t* ref, const int32_t* n_new, int32_t* fresh, cudaStream_t st) {
