@@ -472,8 +472,9 @@ sfi_status sfi_pages_extend(const sfi_paged_layout* layout, const sfi_page_store
  * copy of src[i]: it shares the full pages, and the rows of the last, partly
  * filled one are copied, in every layer, to a new page.  src and dst are host
  * arrays of n sequences; no dst twice and none that is a src too
- * (SFI_ERR_INVALID_ARG).  A dst that is not empty sets SFI_DEV_BAD_INDEX, one
- * for which no page is left SFI_DEV_NO_PAGES; both stay as they are. */
+ * (SFI_ERR_INVALID_ARG).  A dst that is not empty, or whose src holds a page outside
+ * the pool, sets SFI_DEV_BAD_INDEX, one for which no page is left SFI_DEV_NO_PAGES; they
+ * stay as they are. */
 sfi_status sfi_pages_fork(const sfi_paged_layout* layout, const sfi_page_store* store,
                           const int32_t* src, const int32_t* dst, int32_t n, void* ws,
                           size_t ws_bytes, sfi_stream stream);

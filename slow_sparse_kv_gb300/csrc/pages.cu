@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(kPlan) fork_kernel(PagedGeo g, int32_t* ref, c
                                                      const __grid_constant__ SeqList dst, int n, int4* jobs) {
   __shared__ long long part[32];
   __shared__ int32_t fresh[kMaxBatch];
-  __shared__ int full[kMaxBatch];  // full pages to share, -1: a pair that stays out
+  __shared__ int full[kMaxBatch];  // first the pages that the source holds; then the full ones to share
+  __shared__ bool outside[kMaxBatch];  // a page of the source lies outside the pool
   const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
   pdl_launch();
   pdl_wait();
@@ -157,6 +158,36 @@ __global__ void __launch_bounds__(kPlan) fork_kernel(PagedGeo g, int32_t* ref, c
     if (len < 0 || len > g.max_pages * g.P) flags = SFI_DEV_LEN_OVER_CAP;
     else if (g.len[t] != 0) flags = SFI_DEV_BAD_INDEX;
     else in = true;
+    full[i] = in ? pages_of(len, g.P) : 0;
+  }
+  __syncthreads();
+  // (a warp reads the first pages of four pairs at once: 100 forks of 300 positions 10.8 us,
+  // pair by pair 11.9)
+  constexpr int W = kPlan / 32, AT_ONCE = 4;
+  for (int j0 = warp; j0 < n; j0 += AT_ONCE * W) {
+    int page[AT_ONCE];
+#pragma unroll
+    for (int e = 0; e < AT_ONCE; ++e) {
+      const int j = j0 + e * W;
+      page[e] = j < n && lane < full[j] ? g.table[int64_t(src.id[j]) * g.max_pages + lane] : 0;
+    }
+#pragma unroll
+    for (int e = 0; e < AT_ONCE; ++e) {
+      const int j = j0 + e * W;
+      if (j >= n) break;
+      const int32_t* const from = g.table + int64_t(src.id[j]) * g.max_pages;
+      bool bad = uint32_t(page[e]) >= uint32_t(g.n_pages);
+      for (int k = 32 + lane; k < full[j]; k += 32) bad |= uint32_t(from[k]) >= uint32_t(g.n_pages);
+      bad = __any_sync(kFull, bad);
+      if (lane == 0) outside[j] = bad;
+    }
+  }
+  __syncthreads();
+  if (i < n) {
+    if (outside[i]) {
+      flags = SFI_DEV_BAD_INDEX;
+      in = false;
+    }
     need = in && len % g.P != 0;
   }
   const int rank = int(block_scan(need, part)) - need;
@@ -168,13 +199,11 @@ __global__ void __launch_bounds__(kPlan) fork_kernel(PagedGeo g, int32_t* ref, c
       flags |= SFI_DEV_NO_PAGES;
       in = false;
     }
-    full[i] = in ? len / g.P : -1;
+    full[i] = in ? len / g.P : 0;
     int4 job = make_int4(0, 0, 0, 0);
     if (in && need) {
-      const int from = g.table[int64_t(s) * g.max_pages + len / g.P];
       const int to = fresh[rank];
-      if (from < 0 || from >= g.n_pages) flags |= SFI_DEV_BAD_INDEX;
-      else job = make_int4(from, to, len % g.P, 0);
+      job = make_int4(g.table[int64_t(s) * g.max_pages + len / g.P], to, len % g.P, 0);
       g.table[int64_t(t) * g.max_pages + len / g.P] = to;
       ref[to] = 1;
     }
@@ -189,8 +218,7 @@ __global__ void __launch_bounds__(kPlan) fork_kernel(PagedGeo g, int32_t* ref, c
     for (int k = lane; k < full[j]; k += 32) {
       const int p = from[k];
       to[k] = p;
-      if (p < 0 || p >= g.n_pages) set_status(g.status, SFI_DEV_BAD_INDEX);
-      else atomicAdd(ref + p, 1);
+      atomicAdd(ref + p, 1);
     }
   }
 }
@@ -208,7 +236,8 @@ __global__ void __launch_bounds__(kCopy) free_kernel(PagedGeo g, int32_t* ref, c
   for (int i = threadIdx.x; i < pages_of(n, g.P); i += kCopy) {
     const int p = row[i];
     row[i] = -1;
-    // (a count never falls below zero, whatever the order of the decrements)
+    // (a count that is zero gets back what was taken off, whatever the order of the
+    // decrements; between the two it may read as less)
     bool bad = p < 0 || p >= g.n_pages;
     if (!bad && atomicSub(ref + p, 1) <= 0) {
       atomicAdd(ref + p, 1);
