@@ -322,8 +322,10 @@ sfi_status sfi_fast_attn_noalloc(const sfi_layout* layout, const sfi_params* par
  * lse = -infinity.  Rows outside every sequence (behind cu_q[B], before
  * cu_q[0]) are left untouched, and what lies in k and v outside a sequence's
  * rows never reaches its outputs, NaN included.  Within a sequence V must be
- * finite: a non-finite V row may also spoil rows at most 127 positions before
- * its own (a K row only reaches the rows that attend to it).
+ * finite: a non-finite V row may also spoil rows up to 126 + 128 / G (rounded down,
+ * G = H_q / H_kv) positions before its own, as far as tokens share a tile and the keys
+ * of its last block; lse it leaves alone, and a K row only reaches the rows that attend
+ * to it.
  *  - bf16 only.  out is bf16 too, unlike the decode calls' fp32: it is the
  *    next matrix product's input.  Scores, softmax and sums are fp32, the
  *    probabilities are rounded to bf16 for the product with V.  lse is fp32
