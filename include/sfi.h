@@ -337,7 +337,9 @@ sfi_status sfi_fast_attn_noalloc(const sfi_layout* layout, const sfi_params* par
  *  - Any group size G = H_q / H_kv from 1 to 16; head_dim 64 or 128.
  *  - cu_q and cu_k are ascending; an entry pair that descends or leaves
  *    [0, total_q] ([0, total_k]) sets SFI_DEV_LEN_OVER_CAP and that sequence's
- *    rows are not computed.
+ *    rows are not computed (a row that two sequences hold, as cu_q
+ *    descends between them, gets the output of either; more than 2^31 - 1 tiles in all
+ *    set the bit too and nothing is computed).
  *  - The same call gives the same bits.  With few query rows over many keys (1024
  *    or more in all) some rows are computed in up to 8 parts of their keys that
  *    are joined in fp32; which ones, and so the rounding, depends on the whole

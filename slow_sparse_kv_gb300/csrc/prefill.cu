@@ -274,16 +274,25 @@ __device__ __forceinline__ Tile make_tile(const PrefillArgs& a, int g, const Seq
 // key blocks, so that all SMs get one.  (A whole prompt's last tiles are its short
 // ones and fill the gaps as they are.)
 struct Split {
-  long long total;  // tiles
+  long long total;  // tiles, -1: too many for ranks of 31 bits
   long long first;  // ranks from here on are cut
   int tiles, parts;
 };
 
 __device__ __forceinline__ Split split_of(const PrefillArgs& a, Ranks r, int grid) {  // one warp
   Split s;
-  s.total = s.first = (long long)r.from(0) * a.H_kv;
+  // (offsets that descend between two sequences let both hold the same rows, and so have
+  // more tiles than the call has reckoned with by its rows; 2^32, which this sum could
+  // not show, would take 270 GB of queries)
+  const int tiles = r.from(0);
+  s.total = s.first = (long long)tiles * a.H_kv;
   s.tiles = 0;
   s.parts = 1;
+  if (tiles < 0 || s.total > 0x7fffffffLL) {
+    s.total = -1;
+    s.first = 0;
+    return s;
+  }
   if (a.partials == nullptr || s.total == 0 || s.total >= kSplitWaves * grid) return s;
   // (below 2^31: kSplitWaves * grid)
   const int rest = int(uint32_t(s.total) % uint32_t(grid));
@@ -504,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       Ranks ranks(a);
       const Split split = split_of(a, ranks, gridDim.x);
       if (blockIdx.x == 0 && lane == 0 && a.partials != nullptr) a.cut_count[0] = split.tiles, a.cut_count[1] = split.parts;
-      if (blockIdx.x == 0 && ranks.bad) set_status(a.status, SFI_DEV_LEN_OVER_CAP);
+      if (blockIdx.x == 0 && (ranks.bad || split.total < 0)) set_status(a.status, SFI_DEV_LEN_OVER_CAP);
       for (int k = 0;; ++k) {
         Tile t;
         t.rows = 0;
