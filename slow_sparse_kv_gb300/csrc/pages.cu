@@ -131,7 +131,10 @@ __global__ void __launch_bounds__(kPlan) extend_kernel(PagedGeo g, int32_t* ref,
   if (flags) set_status(g.status, flags);
   // whom an append has to leave out: who asked and was refused, until it is served
   const uint32_t bad = __ballot_sync(kFull, flags != 0), served = __ballot_sync(kFull, more > 0);
-  if (lane == 0 && (bad | served)) g.refused[warp] = (g.refused[warp] & ~served) | bad;
+  if (lane == 0) {
+    if (served) atomicAnd(g.refused + warp, ~served);
+    if (bad) atomicOr(g.refused + warp, bad);
+  }
   for (int s = warp; s < g.B; s += kPlan / 32)
     for (int i = lane; i < need[s]; i += 32) {
       const int p = fresh[at[s] + i];
@@ -405,7 +408,8 @@ __global__ void __launch_bounds__(kCopy) compact_kernel(const __grid_constant__ 
 __device__ __forceinline__ void append_row(const AppendArgs& a, int b, int m, int back, int t, int cap, int lane) {
   const PagedGeo& g = a.geo;
   const int n = g.len[b];
-  if (n < 0 || n > cap || m > n || (g.refused[b >> 5] >> (b & 31) & 1)) return;
+  const uint32_t refused = g.refused[b >> 5] >> (b & 31) & 1;  // (read beside the length, not behind its check)
+  if ((n < 0) | (n > cap) | (m > n) | refused) return;
   const int pos = n - back;
   const int page = g.table[int64_t(b) * g.max_pages + pos / g.P];
   if (page < 0 || page >= g.n_pages) {
@@ -437,8 +441,9 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, int b, int m, in
 // holds the token: one, where the offsets ascend; where some do not, those that are in
 // order are stored all the same, so all pairs are looked through (by each warp for its
 // token up to 32 sequences, else by the CTA for its eight; a search by halves would miss
-// some).  A sequence that an extension refused holds the length from before it: the rows would go over its last
-// ones, which may lie in pages that others share, so it is left out.
+// some).  A sequence that an extension refused holds the length from before it: the rows
+// would go over its last ones, which may lie in pages that others share, so it is left
+// out.  The last CTA only looks for what is to be flagged.
 __global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kWarps = kCopy / 32;
   __shared__ uint32_t mask[kMaxBatch / 32];  // sequences with rows among the CTA's tokens
@@ -447,8 +452,7 @@ __global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ A
   pdl_launch();
   pdl_wait();
   const int cap = g.max_pages * g.P;
-  if (blockIdx.x == 0) {
-    // every sequence's rows and length, once
+  if (blockIdx.x == gridDim.x - 1) {
     for (int b = threadIdx.x; b < g.B; b += kCopy) {
       const int n = g.len[b];
       bool bad = n < 0 || n > cap, refused = g.refused[b >> 5] >> (b & 31) & 1;
@@ -459,13 +463,10 @@ __global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ A
       }
       if (bad || refused) set_status(g.status, (bad ? SFI_DEV_LEN_OVER_CAP : 0u) | (refused ? SFI_DEV_NO_PAGES : 0u));
     }
+    return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t0 = blockIdx.x * kWarps, t = t0 + warp;
-  if (!a.cu) {
-    if (t < a.total) append_row(a, t, 1, 1, t, cap, lane);
-    return;
-  }
   // of the pairs that are in order, does b's hold some of the rows [from, from + n)?
   auto holds = [&](int b, int from, int n) {
     if (b >= g.B) return false;
@@ -473,7 +474,9 @@ __global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ A
     return c0 >= 0 && c1 <= a.total && c0 < c1 && c0 - from < n && c1 > from;
   };
   uint32_t word;  // the lane's 32 sequences
-  if (g.B <= 32) {
+  if (!a.cu) {
+    word = lane == t >> 5 ? 1u << (t & 31) : 0;
+  } else if (g.B <= 32) {
     const uint32_t in = __ballot_sync(kFull, holds(lane, t, 1));
     word = lane == 0 ? in : 0;
   } else {
@@ -489,7 +492,8 @@ __global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ A
   for (uint32_t words = __ballot_sync(kFull, word != 0); words; words &= words - 1) {
     const int w = __ffs(words) - 1;
     for (uint32_t bits = __shfl_sync(kFull, word, w); bits; bits &= bits - 1) {
-      const int b = w * 32 + __ffs(bits) - 1, c0 = a.cu[b], c1 = a.cu[b + 1];
+      const int b = w * 32 + __ffs(bits) - 1;
+      const int c0 = a.cu ? a.cu[b] : t, c1 = a.cu ? a.cu[b + 1] : t + 1;
       if (t >= c0 && t < c1) append_row(a, b, c1 - c0, c1 - t, t, cap, lane);
     }
   }
@@ -508,7 +512,7 @@ long long page_slices(const PageMove& mv) {
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
-  return launch_pdl(append_kernel, dim3((a.total - 1) / (kCopy / 32) + 1), kCopy, 0, st, a);
+  return launch_pdl(append_kernel, dim3((a.total - 1) / (kCopy / 32) + 2), kCopy, 0, st, a);
 }
 
 cudaError_t launch_extend(const PagedGeo& g, int32_t* ref, const int32_t* n_new, int32_t* fresh, cudaStream_t st) {
