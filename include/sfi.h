@@ -417,11 +417,13 @@ size_t sfi_paged_workspace_size(const sfi_paged_layout* layout);
  * len[b] includes the token, whose K and V are in the cache already
  * (sfi_paged_append).  q: [B][H_q][d] (dtype), 16-byte aligned; out and lse_out
  * fp32.  len[b] = 0 gives out = 0 and lse = -infinity.  Rows of a page at or
- * past len[b] may hold anything.  Two launches: all rows of all sequences are dealt
- * over the SMs, and a small second kernel joins the pieces of each split
- * (sequence, KV head) in a fixed order: the same call gives the same bits, but
- * where a sequence is split, and so the order of its fp32 sums, depends on all
- * lengths of the batch.  The waits for copies have the limit of
+ * past len[b] may hold anything.  An element of V before it that is not finite makes
+ * its column of the outputs that attend to it not finite, and no other: in bf16 it may
+ * be NaN where the sum is infinite (a probability is added in terms of both signs).
+ * Two launches: all rows of all sequences are dealt over the SMs, and a small second
+ * kernel joins the pieces of each split (sequence, KV head) in a fixed order: the same
+ * call gives the same bits, but where a sequence is split, and so the order of its fp32
+ * sums, depends on all lengths of the batch.  The waits for copies have the limit of
  * sfi_set_wait_limit. */
 sfi_status sfi_paged_attn(const sfi_paged_layout* layout, const void* q, const void* k,
                           const void* v, float* out, float* lse_out, void* ws, size_t ws_bytes,

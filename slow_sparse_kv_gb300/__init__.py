@@ -474,7 +474,8 @@ def sfi_paged_attn(layout: PagedLayout, q, k, v, out, lse_out=None, ws=None, str
 
 def sfi_paged_append(layout: PagedLayout, k_new, v_new, k, v, cu_new=None, ws=None, stream=None):
     """k_new, v_new [rows, H_kv, d] (heads dense, any row stride) into the pools k, v; cu_new
-    [B + 1] int32, or None: one row per sequence."""
+    [B + 1] int32, or None: one row per sequence.  Sequences that sfi_pages_extend refused on the
+    same workspace are left out."""
     L = layout
     _here(L.device, stream)
     new = (k_new.shape[0], L.n_kv_heads, L.head_dim)

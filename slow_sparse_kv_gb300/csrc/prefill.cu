@@ -13,17 +13,22 @@
 // tiles alternate: while one's softmax runs, the tensor cores work on the
 // other's products.  Tensor memory: S0/P0, S1/P1, O0, O1 (4 x 128 columns).
 //
-// Bound by the tensor cores (4 d flops per row and visible key) as long as the
-// exponentials keep up: one for each 4 d flops, so that with d = 64 they and the
-// row maxima take longer than the products.  Measured, 32 / 8 heads of 128: 16384
-// tokens in 1.32 ms (1.66 PFLOP/s; a library's matrix product reaches 1.88), 3
-// chunks of ~900 tokens after ~10000 in 309 us (1.46), 16 prompts of 260 to 4000
-// tokens in 312 us (1.30); with d = 64, 0.73 (8192 tokens, 16 / 4 heads) to 0.96
-// (6 x 4096, 32 / 8).  A pair
-// of blocks takes 1.4 us, a tile's start and output another 2.  (A warpgroup of
-// its own for the output was tried: 176 registers for the softmax threads instead
-// of 216, and a tile's products wait for the output of both halves of the last
-// one, 239 us against 223 for 16 other prompts and no gain for long ones.)
+// With d = 128 bound by the tensor cores (4 d flops per row and visible key; active for
+// 75% of the cycles of a launch over 8192 tokens).  With d = 64 by the serial chain of a
+// half: scores, row maximum, exponentials, P over the scores' columns, its last products,
+// and only then the next scores.  A pair of blocks takes 1.33 us, nearly the 1.4 of
+// d = 128, though its products halved; tensor pipe, exponentials and issue slots are
+// active for 41, 41 and 50% of the cycles (6 x 4096 tokens, 32 / 8 heads).
+// Measured, 32 / 8 heads of 128: 16384 tokens in 1.32 to 1.36 ms (1.62 to 1.66 PFLOP/s; a
+// library's matrix product reaches 1.88), 3 chunks of ~900 tokens after ~10000 in 309 us
+// (1.46), 16 prompts of 260 to 4000 tokens in 310 us (1.31); with d = 64, 0.73 to 0.77
+// (8192 tokens, 16 / 4 heads) and 0.98 (6 x 4096, 32 / 8).  A tile's start and output
+// take another 2 us.  (A warpgroup of its own for the output was tried: 176 registers
+// for the softmax threads instead of 216, and a tile's products wait for the output of
+// both halves of the last one, 239 us against 223 for set B and no gain for long ones.)
+// Set B, here and below, on which the steps were compared: 16 other prompts, of 85 to
+// 3521 tokens, 17592 in all, 32 / 8 heads of 128, calls back to back with nothing
+// flushed between; 216 us now.
 //
 // Online softmax: out = sum_j 2^(c (s_j - m)) v_j / sum_j 2^(c (s_j - m)) with
 // c = log2(e) / sqrt(d) holds for any m, so m only follows the row maximum when
@@ -46,8 +51,8 @@ constexpr int kThreads = 384;  // 2 softmax warpgroups; a load, an MMA, a schedu
 constexpr int kRows = 128;     // query rows per tile
 constexpr int kKeys = 128;     // keys per block
 // P of a block is handed over in parts, the first 64 keys, then twice 32: the
-// products start early and the scores behind them wait for a short last part.  (16
-// packed prompts: 218 us; in halves 224, 96 and 32 keys 226, whole 231.)
+// products start early and the scores behind them wait for a short last part.  (Set B:
+// 218 us; in halves 224, 96 and 32 keys 226, whole 231.)
 constexpr int kParts = 3;
 __host__ __device__ constexpr int part_end(int part) { return part == 0 ? 64 : part == 1 ? 96 : kKeys; }
 constexpr float kGrow = 8.0f;  // growth of the maximum (log2) that moves m
@@ -61,7 +66,7 @@ struct Cfg {
   static constexpr uint32_t SMEM = 1024 + (2 + STAGES) * TILE + OUT;
   // Registers a thread: launched with 168; the softmax threads hold a whole row of
   // scores, the third warpgroup gives up what they take.  (d = 128: 208 and 88
-  // against 216 and 72, 16 packed prompts 220 against 224 us; d = 64: 186 against
+  // against 216 and 72, set B 220 against 224 us; d = 64: 186 against
   // 180, 8192 tokens; with 200 the row spills, 233 us.)
   static constexpr int SOFTMAX_REGS = D == 128 ? 208 : 216, OTHER_REGS = 504 - 2 * SOFTMAX_REGS;
 };
@@ -682,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       // (Stores from registers, a row to a lane or rows by 8 lanes, hold up the
       // load/store unit, and with it every wait of the CTA, for 3000 clocks.  A loop,
       // not unrolled: this code runs once a tile, and fetching it costs more than
-      // running it; 220 -> 216 us for 16 packed prompts.)
+      // running it; 220 -> 216 us for set B.)
       const bool whole = 32 % a.G == 0 && __all_sync(kFull, valid);
 #pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {

@@ -153,3 +153,21 @@ def test_long_sums_are_not_truncated(sfi):
         print("relative error", h, err, "bound", bound)
         assert err <= bound
         assert abs(float(lse[0, h]) - float(torch.logsumexp(s, 0))) <= bound + 8 * ULP * 20
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype,page", [(8, 2, 128, BF16, 16), (16, 1, 64, BF16, 20), (12, 2, 64, F32, 7)])
+@pytest.mark.parametrize("x", [float("nan"), float("inf"), float("-inf")])
+def test_non_finite_value_keeps_to_its_column(sfi, hq, hkv, d, dtype, page, x):
+    lens = [700, 33]
+    table, n, n_pages = cache(hkv, d, dtype, page, lens, 11)
+    g = torch.Generator("cuda").manual_seed(7)
+    k, v = (torch.randn((n_pages, hkv, page, d), generator=g, device="cuda", dtype=dtype) for _ in range(2))
+    q = torch.randn(2, hq, d, generator=g, device="cuda", dtype=dtype)
+    clean, lse = run(sfi, hq, hkv, d, dtype, page, table, n, n_pages, q, k, v)
+    at, head, col = 345, hkv - 1, 37
+    v[table[0, at // page].long(), head, at % page, col] = x
+    out, lse2 = run(sfi, hq, hkv, d, dtype, page, table, n, n_pages, q, k, v)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[0, head * (hq // hkv):, col] = True
+    assert not torch.isfinite(out[hit]).any()
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse, lse2)
