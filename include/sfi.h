@@ -435,13 +435,14 @@ sfi_status sfi_paged_attn(const sfi_paged_layout* layout, const void* q, const v
  * of 16 bytes and at least a row) become positions len[b] - m .. len[b] - 1;
  * len[b] counts them already (sfi_pages_extend).  cu_new (device [B + 1]) may
  * be NULL: one row per sequence, total_new = B.  A sequence whose rows leave
- * [0, total_new], descend or outnumber len[b] is flagged (SFI_DEV_LEN_OVER_CAP) and left
- * out, the others are stored; with cu_new NULL one with len[b] = 0 is an idle slot, whose row is not
- * stored.  A sequence that sfi_pages_extend refused on this workspace, and that has
- * rows to store, is flagged (SFI_DEV_NO_PAGES) and left out until an extension serves it
- * or it is freed: its length does not count the rows, which would go over its last ones.
- * k_new and v_new are 16-byte aligned and apart from the pool.  The rows
- * go to the pages that the table names, whoever else holds them: only positions
+ * [0, total_new], descend or outnumber len[b] is flagged (SFI_DEV_LEN_OVER_CAP)
+ * and left out, the others are stored; with cu_new NULL one with len[b] = 0 is an
+ * idle slot, whose row is not stored.  A sequence that sfi_pages_extend refused on
+ * this workspace, and that has rows to store, is flagged (SFI_DEV_NO_PAGES) and left
+ * out until an extension serves it, it is freed or forked into: its length does not
+ * count the rows, which would go over its last ones.  k_new and v_new are 16-byte
+ * aligned and apart from the pool.  The rows go to the pages that the table names,
+ * whoever else holds them: only positions
  * added by the last sfi_pages_extend are sure to be the sequence's own. */
 sfi_status sfi_paged_append(const sfi_paged_layout* layout, int32_t total_new, const void* k_new,
                             const void* v_new, int64_t k_stride, int64_t v_stride,
