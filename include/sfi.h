@@ -68,7 +68,8 @@ typedef enum {
   SFI_ERR_CUDA = 5         /* a CUDA runtime call failed */
 } sfi_status;
 
-typedef enum { SFI_F32 = 0, SFI_BF16 = 1 } sfi_dtype;
+/* SFI_I8 and SFI_E4M3 are types of paged pools only (see there). */
+typedef enum { SFI_F32 = 0, SFI_BF16 = 1, SFI_I8 = 4, SFI_E4M3 = 5 } sfi_dtype;
 
 /* Device status bits (sfi_read_status). */
 #define SFI_DEV_LEN_OVER_CAP   0x1u  /* len[b] > kv_cap[b] or len[b] > max_len */
@@ -305,6 +306,54 @@ sfi_status sfi_fast_attn_noalloc(const sfi_layout* layout, const sfi_params* par
                                  const int32_t* idx, const int32_t* count, float* out,
                                  sfi_stream stream);
 
+/* ---------------------------------------------------------------- norm and rotation of heads */
+
+/* RMS norm of each query and key head, and its rotation by the position, in one pass: what
+ * lies between a projection and sfi_prefill_attn, sfi_paged_append or the decode calls (no
+ * counterpart on the pages, whose q and k come rotated).
+ *
+ * For each of `total` rows and each head x of d elements (n_q_heads of q, n_kv_heads of k):
+ *   n_i = x_i / sqrt(sum_j x_j^2 / d + eps) * w_i       (norm != 0; else n = x)
+ *   a_i = (pos[row] + pos_offset) * inv_freq[i],  i < rotary_dim / 2
+ *   (y_i, y_j) = (n_i cos a_i - n_j sin a_i, n_i sin a_i + n_j cos a_i)
+ * for the pairs (i, j) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) where `interleaved`;
+ * elements from rotary_dim on are y = n.  fp32 inside, rounded once to the rows' type.
+ *  - q_weight, k_weight: d elements of the rows' type (device; NULL: ones; NULL where norm
+ *    is 0).
+ *  - rotary_dim: a multiple of 8 in [0, d]; 0 rotates nothing (pos and inv_freq may be NULL).
+ *  - inv_freq: host array of rotary_dim / 2 finite numbers, read before the call returns;
+ *    whatever scheme makes them (theta^(-2 i / rotary_dim), scaled for longer contexts).
+ *    The angle is taken modulo a turn without loss: any int32 position and offset, negative
+ *    ones too, is off by less than 2^-24 turns.
+ *  - pos: device [total].  A decode step's positions are len with pos_offset -1.
+ *  - Row t of q starts q_stride elements after row t - 1 and holds its heads one after
+ *    another (0: nothing between the rows); the same for k and the outputs.  Strides are at
+ *    least a row and multiples of 16 bytes; all pointers are 16-byte aligned.
+ *  - q_out may be q, and k_out k (with the same stride); else outputs and inputs are apart.
+ *  - dtype SFI_F32 or SFI_BF16; head_dim 64 or 128; up to 4096 heads each.  n_kv_heads = 0
+ *    (or n_q_heads = 0) leaves k (q) out; its pointers are not read.
+ *  - total = 0 is a call that does nothing.
+ * One launch, no workspace.  A head whose sum of squares leaves fp32 is 0. */
+typedef struct {
+  int32_t total; /* rows */
+  int32_t n_q_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t dtype; /* SFI_F32 or SFI_BF16 */
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t norm;
+  float eps;
+  int32_t pos_offset;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride; /* elements; 0: rows without gaps */
+  const int32_t* pos;     /* device [total] */
+  const double* inv_freq; /* host [rotary_dim / 2] */
+} sfi_rotary_layout;
+
+sfi_status sfi_qk_norm_rope(const sfi_rotary_layout* layout, const void* q, const void* k,
+                            const void* q_weight, const void* k_weight, void* q_out, void* k_out,
+                            sfi_stream stream);
+
 /* ---------------------------------------------------------------- prompt attention */
 
 /* Causal attention over whole prompts, packed one after another (no
@@ -508,6 +557,40 @@ sfi_status sfi_pages_compact(const sfi_paged_layout* layout, const sfi_page_stor
 sfi_status sfi_pages_copy(const sfi_paged_layout* layout, const sfi_page_store* store,
                           const int32_t* src, const int32_t* dst, int32_t n, void* ws,
                           size_t ws_bytes, sfi_stream stream);
+
+/* ---------------------------------------------------------------- paged cache in 8 bits */
+
+/* A paged cache whose layout has dtype SFI_I8 or SFI_E4M3 holds each row (a position of a KV
+ * head) of k and of v as d codes of one byte and one fp32 scale; the row's values are
+ * scale * code:
+ *   SFI_I8:   scale = max|x| / 127 (rounded to fp32), code = x / scale rounded to the
+ *             nearest integer, ties to even, -127 to 127 (two's complement);
+ *   SFI_E4M3: scale = the smallest power of two for which max|x| / scale <= 448, code =
+ *             x / scale rounded to the nearest e4m3 number, ties to even.
+ * The quotient is rounded as if it were exact: the same row gives the same bits everywhere.
+ * A row of zeros (or of numbers so small that the scale is below 2^-149) has scale 0 and
+ * codes 0.  A row with an infinity or a NaN has scale NaN and codes 0: reading it gives NaN.
+ *
+ * A page is [H_kv][page_size][d] codes and behind them [H_kv][page_size] scales, so that it
+ * can be copied as a whole: H_kv * page_size * (d + 4) bytes, rounded up to 16 (page_stride
+ * 0).  An element is a byte here: page_stride is a multiple of 16 (not of head_dim),
+ * layer_stride too.  The pool of all pages is below 2^42 bytes.  All else is as above:
+ * sfi_paged_workspace_size, sfi_pages_extend, _fork, _free, _compact and _copy take such
+ * layouts, and sfi_paged_attn and sfi_paged_append refuse them (SFI_ERR_UNSUPPORTED). */
+
+/* sfi_paged_append of rows of new_dtype (SFI_F32 or SFI_BF16; strides in elements of it)
+ * into an 8-bit pool, quantised on the way; the rest as there. */
+sfi_status sfi_paged_append_q8(const sfi_paged_layout* layout, int32_t new_dtype,
+                               int32_t total_new, const void* k_new, const void* v_new,
+                               int64_t k_stride, int64_t v_stride, const int32_t* cu_new, void* k,
+                               void* v, void* ws, size_t ws_bytes, sfi_stream stream);
+
+/* sfi_paged_attn over an 8-bit pool, for q of q_dtype (SFI_F32 or SFI_BF16); out and lse_out
+ * fp32.  K and V enter as the numbers that they stand for; scores, softmax and sums are
+ * fp32.  Rows at or past len[b] may hold anything.  The rest as there. */
+sfi_status sfi_paged_attn_q8(const sfi_paged_layout* layout, int32_t q_dtype, const void* q,
+                             const void* k, const void* v, float* out, float* lse_out, void* ws,
+                             size_t ws_bytes, sfi_stream stream);
 
 /* ---------------------------------------------------------------- decode driver */
 

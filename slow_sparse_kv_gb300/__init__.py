@@ -23,7 +23,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libsfi.so")
 
 SFI_OK, SFI_ERR_INVALID_ARG, SFI_ERR_UNSUPPORTED, SFI_ERR_CAPACITY, SFI_ERR_WORKSPACE, SFI_ERR_CUDA = range(6)
-SFI_F32, SFI_BF16 = 0, 1
+SFI_F32, SFI_BF16, SFI_I8, SFI_E4M3 = 0, 1, 4, 5
 SFI_SELECT_FUSED, SFI_SELECT_LOGIT_SUM_SEQ, SFI_SELECT_LOGIT_SUM_HEAD = 0, 1, 2
 SFI_DEV_LEN_OVER_CAP, SFI_DEV_BAD_INDEX, SFI_DEV_WAIT_TIMEOUT, SFI_DEV_ITEMS_OVERFLOW = 1, 2, 4, 8
 SFI_DEV_REFINE, SFI_DEV_NO_PAGES = 16, 32
@@ -66,6 +66,15 @@ class sfi_paged_layout(ctypes.Structure):
                 ("page_table", c_void_p), ("len", c_void_p)]
 
 
+class sfi_rotary_layout(ctypes.Structure):
+    _fields_ = [("total", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32),
+                ("head_dim", c_int32), ("dtype", c_int32), ("rotary_dim", c_int32),
+                ("interleaved", c_int32), ("norm", c_int32), ("eps", c_float),
+                ("pos_offset", c_int32), ("q_stride", c_int64), ("k_stride", c_int64),
+                ("q_out_stride", c_int64), ("k_out_stride", c_int64), ("pos", c_void_p),
+                ("inv_freq", c_void_p)]
+
+
 class sfi_page_store(ctypes.Structure):
     _fields_ = [("ref", c_void_p), ("k", c_void_p), ("v", c_void_p), ("n_layers", c_int32),
                 ("layer_stride", c_int64)]
@@ -105,6 +114,12 @@ EXPORTS = {
                                  c_size_t, c_void_p]),
     "sfi_paged_append": (c_int32, [_PL, c_int32, c_void_p, c_void_p, c_int64, c_int64, c_void_p,
                                    c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "sfi_paged_attn_q8": (c_int32, [_PL, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                    c_void_p, c_size_t, c_void_p]),
+    "sfi_paged_append_q8": (c_int32, [_PL, c_int32, c_int32, c_void_p, c_void_p, c_int64, c_int64,
+                                      c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "sfi_qk_norm_rope": (c_int32, [POINTER(sfi_rotary_layout), c_void_p, c_void_p, c_void_p, c_void_p,
+                                   c_void_p, c_void_p, c_void_p]),
     "sfi_pages_extend": (c_int32, [_PL, _PS, c_void_p, c_void_p, c_size_t, c_void_p]),
     "sfi_pages_fork": (c_int32, [_PL, _PS, c_void_p, c_void_p, c_int32, c_void_p, c_size_t, c_void_p]),
     "sfi_pages_free": (c_int32, [_PL, _PS, c_void_p, c_int32, c_void_p, c_size_t, c_void_p]),
@@ -181,6 +196,9 @@ def dtype_code(dt: torch.dtype) -> int:
     if dt == torch.bfloat16:
         return SFI_BF16
     raise ValueError(f"unsupported dtype {dt}")
+
+
+_POOL_CODES = {torch.int8: SFI_I8, torch.float8_e4m3fn: SFI_E4M3}  # pools of 8 bits
 
 
 class Layout:
@@ -386,7 +404,11 @@ class PagedLayout:
     page page_table[b, i // page_size] (page_table [B, max_pages], len [B], int32
     device tensors, shared with the caller).  One layer's pool is
     [n_pages, H_kv, page_size, d]; ``page_stride`` is the distance of its pages in
-    elements where they are not one after another (0: they are)."""
+    elements where they are not one after another (0: they are).
+
+    With dtype torch.int8 or torch.float8_e4m3fn the rows are held in 8 bits with a scale for
+    each, and a pool is [n_pages, page_bytes] of torch.uint8; ``codes`` and ``scales`` are
+    views of one."""
 
     def __init__(self, n_q_heads: int, n_kv_heads: int, head_dim: int, dtype: torch.dtype,
                  page_size: int, n_pages: int, page_table: torch.Tensor, len: torch.Tensor,
@@ -400,36 +422,57 @@ class PagedLayout:
         self.n_q_heads, self.n_kv_heads, self.head_dim, self.dtype = n_q_heads, n_kv_heads, head_dim, dtype
         self.page_size, self.n_pages, self.page_stride = page_size, n_pages, page_stride
         self.page_table, self.len = page_table, len
-        self._pool_shape = (n_pages, n_kv_heads, page_size, head_dim)
-        self._page_strides = (page_size * head_dim, head_dim, 1)
-        self.c = sfi_paged_layout(self.B, n_q_heads, n_kv_heads, head_dim, dtype_code(dtype), page_size,
+        self.q8 = dtype in _POOL_CODES
+        rows = n_kv_heads * page_size
+        #: elements of a page (bytes of an 8-bit one)
+        self.page_bytes = -(-rows * (head_dim + 4) // 16) * 16 if self.q8 else rows * head_dim
+        self._pool_shape = (n_pages, self.page_bytes) if self.q8 else (n_pages, n_kv_heads, page_size, head_dim)
+        self._page_strides = (1,) if self.q8 else (page_size * head_dim, head_dim, 1)
+        code = _POOL_CODES[dtype] if self.q8 else dtype_code(dtype)
+        self.c = sfi_paged_layout(self.B, n_q_heads, n_kv_heads, head_dim, code, page_size,
                                   n_pages, self.max_pages, page_stride, page_table.data_ptr(),
                                   len.data_ptr())
 
     def _pool(self, name: str, t: torch.Tensor, layers: int = 0) -> torch.Tensor:
         """Refuse a tensor that is not a pool ([layers,] n_pages, H_kv, page_size, d) of this layout."""
         want = (layers,) + self._pool_shape if layers else self._pool_shape
-        if t.dtype is not self.dtype or t.shape != want or t.device != self.device:
-            raise ValueError(f"{name}: expected {self.dtype} {want} on {self.device}, "
+        held = torch.uint8 if self.q8 else self.dtype
+        if t.dtype is not held or t.shape != want or t.device != self.device:
+            raise ValueError(f"{name}: expected {held} {want} on {self.device}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-        apart = self.page_stride or self.n_kv_heads * self.page_size * self.head_dim
-        strides = t.stride()[-4:]
-        if strides[1:] != self._page_strides and not t[(0,) * (t.dim() - 3)].is_contiguous():
+        apart = self.page_stride or self.page_bytes
+        strides = t.stride()[-len(self._pool_shape):]
+        if strides[1:] != self._page_strides and not t[(0,) * (1 + bool(layers))].is_contiguous():
             raise ValueError(f"{name}: a page must be dense")
         if self.n_pages > 1 and strides[0] != apart:
             raise ValueError(f"{name}: pages lie {strides[0]} elements apart, the layout says {apart}")
         return t
 
 
+    def codes(self, pool: torch.Tensor) -> torch.Tensor:
+        """The codes [..., n_pages, H_kv, page_size, d] of an 8-bit pool, as a view of it."""
+        rows = self.n_kv_heads * self.page_size
+        return pool[..., :rows * self.head_dim].view(self.dtype).unflatten(
+            -1, (self.n_kv_heads, self.page_size, self.head_dim))
+
+    def scales(self, pool: torch.Tensor) -> torch.Tensor:
+        """The scales [..., n_pages, H_kv, page_size] of an 8-bit pool, as a view of it."""
+        rows = self.n_kv_heads * self.page_size
+        return pool[..., rows * self.head_dim:rows * (self.head_dim + 4)].view(torch.float32).unflatten(
+            -1, (self.n_kv_heads, self.page_size))
+
+
 class PageStore:
     """The page counts ref [n_pages] (int32) and the pools k, v of the layers that the
-    bookkeeping moves: [n_pages, H_kv, page_size, d] or [layers, n_pages, H_kv, page_size, d]."""
+    bookkeeping moves: [n_pages, H_kv, page_size, d] or [layers, n_pages, H_kv, page_size, d];
+    [n_pages, page_bytes] or [layers, n_pages, page_bytes] in 8 bits."""
 
     def __init__(self, ref: torch.Tensor, k: torch.Tensor, v: torch.Tensor):
         self.ref, self.k, self.v = ref, k, v
-        if k.shape != v.shape or k.stride() != v.stride() or k.dim() not in (4, 5):
+        dims = 2 if k.dtype is torch.uint8 else 4  # of a layer's pool
+        if k.shape != v.shape or k.stride() != v.stride() or k.dim() not in (dims, dims + 1):
             raise ValueError("k and v must be pools of the same shape and strides")
-        self.layers = k.shape[0] if k.dim() == 5 else 0
+        self.layers = k.shape[0] if k.dim() > dims else 0
         self.c = sfi_page_store(_ptr(ref), _ptr(k), _ptr(v), max(1, self.layers),
                                 k.stride(0) if self.layers > 1 else 0)
 
@@ -489,6 +532,118 @@ def sfi_paged_append(layout: PagedLayout, k_new, v_new, k, v, cu_new=None, ws=No
     _check("sfi_paged_append", lib.sfi_paged_append(
         ctypes.byref(L.c), new[0], _ptr(k_new), _ptr(v_new), ks, vs, _ptr(cu_new), _ptr(k), _ptr(v),
         *_ws(ws, L.device), _stream(stream)))
+
+
+def _rows_code(name: str, t: torch.Tensor) -> int:
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name}: expected torch.float32 or torch.bfloat16, got {t.dtype}")
+    return dtype_code(t.dtype)
+
+
+def _want_q8(layout: PagedLayout) -> PagedLayout:
+    if not layout.q8:
+        raise ValueError(f"the layout's pool is of {layout.dtype}, not of 8 bits")
+    return layout
+
+
+def sfi_paged_attn_q8(layout: PagedLayout, q, k, v, out, lse_out=None, ws=None, stream=None):
+    """sfi_paged_attn over an 8-bit pool; q [B, H_q, d] is fp32 or bf16."""
+    L = _want_q8(layout)
+    _here(L.device, stream)
+    rq = (L.B, L.n_q_heads, L.head_dim)
+    code = _rows_code("q", q)
+    _want("q", q, rq, q.dtype, L.device)
+    L._pool("k", k)
+    L._pool("v", v)
+    _want("out", out, rq, torch.float32, L.device)
+    if lse_out is not None:
+        _want("lse_out", lse_out, rq[:2], torch.float32, L.device)
+    _check("sfi_paged_attn_q8", lib.sfi_paged_attn_q8(
+        ctypes.byref(L.c), code, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse_out),
+        *_ws(ws, L.device), _stream(stream)))
+
+
+def sfi_paged_append_q8(layout: PagedLayout, k_new, v_new, k, v, cu_new=None, ws=None, stream=None):
+    """sfi_paged_append into an 8-bit pool; k_new and v_new are both fp32 or both bf16."""
+    L = _want_q8(layout)
+    _here(L.device, stream)
+    new = (k_new.shape[0], L.n_kv_heads, L.head_dim)
+    code = _rows_code("k_new", k_new)
+    _want("k_new", k_new, new, k_new.dtype, L.device, True)
+    _want("v_new", v_new, new, k_new.dtype, L.device, True)
+    L._pool("k", k)
+    L._pool("v", v)
+    if cu_new is not None:
+        _want("cu_new", cu_new, (L.B + 1,), torch.int32, L.device)
+    ks, vs = (t.stride(0) if new[0] > 1 else 0 for t in (k_new, v_new))
+    _check("sfi_paged_append_q8", lib.sfi_paged_append_q8(
+        ctypes.byref(L.c), code, new[0], _ptr(k_new), _ptr(v_new), ks, vs, _ptr(cu_new), _ptr(k),
+        _ptr(v), *_ws(ws, L.device), _stream(stream)))
+
+
+class RotaryLayout:
+    """Rows of query and key heads that are normed and rotated: pos int32 [rows] (device; None
+    where nothing is rotated).  The frequencies are theta^(-2 i / rotary_dim), or inv_freq
+    (rotary_dim / 2 numbers); rotary_dim None is the whole head, 0 no rotation.  eps None
+    leaves the norm out.  Pairs are (i, i + rotary_dim / 2), or neighbours if ``interleaved``."""
+
+    def __init__(self, n_q_heads: int, n_kv_heads: int, head_dim: int, dtype: torch.dtype,
+                 pos: Optional[torch.Tensor], rotary_dim: Optional[int] = None, theta: float = 10000.0,
+                 inv_freq: Optional[Sequence[float]] = None, interleaved: bool = False,
+                 eps: Optional[float] = 1e-6, pos_offset: int = 0):
+        r = head_dim if rotary_dim is None else int(rotary_dim)
+        if inv_freq is None:
+            inv_freq = [float(theta) ** (-2.0 * i / r) for i in range(r // 2)]
+        if len(inv_freq) != r // 2:
+            raise ValueError(f"inv_freq: expected {r // 2} numbers, got {len(inv_freq)}")
+        if r > 0:
+            if pos is None:
+                raise ValueError("pos: positions are needed to rotate")
+            self.device = _device_of("pos", pos)
+            _want("pos", pos, (pos.numel(),), torch.int32, self.device)
+        else:
+            self.device = pos.device if pos is not None else None
+        self.n_q_heads, self.n_kv_heads, self.head_dim, self.dtype = n_q_heads, n_kv_heads, head_dim, dtype
+        self.pos, self.norm = pos, eps is not None
+        self._freq = array.array("d", [float(x) for x in inv_freq])
+        self._c = sfi_rotary_layout(0 if pos is None else pos.numel(), n_q_heads, n_kv_heads, head_dim,
+                                    dtype_code(dtype), r, int(bool(interleaved)), int(self.norm),
+                                    eps if self.norm else 0.0, int(pos_offset), 0, 0, 0, 0,
+                                    None if pos is None else pos.data_ptr(),
+                                    self._freq.buffer_info()[0] if r else None)
+
+
+def sfi_qk_norm_rope(layout: RotaryLayout, q, k, q_out, k_out, q_weight=None, k_weight=None, stream=None):
+    """q, q_out [rows, H_q, d], k, k_out [rows, H_kv, d] (heads dense, any row stride: slices of a
+    joint projection); q_weight, k_weight [d] or None.  q_out may be q and k_out k.  With no query
+    (or KV) heads in the layout, q (or k) and its output are None."""
+    L, c = layout, sfi_rotary_layout.from_buffer_copy(layout._c)
+    there = [t for t in (q, k) if t is not None]
+    if not there:
+        raise ValueError("q or k must be given")
+    device = _device_of("q" if q is not None else "k", there[0])
+    if L.device is not None and L.device != device:
+        raise ValueError(f"the rows lie on {device}, the layout on {L.device}")
+    _here(device, stream)
+    rows = there[0].shape[0]
+    if L.pos is not None and L.pos.numel() != rows:
+        raise ValueError(f"{rows} rows, but {L.pos.numel()} positions")
+    for name, heads, x, y, w in (("q", L.n_q_heads, q, q_out, q_weight), ("k", L.n_kv_heads, k, k_out, k_weight)):
+        if heads == 0 and x is None and y is None and w is None:
+            continue
+        if x is None or y is None:
+            raise ValueError(f"{name} and {name}_out must be given, with {heads} heads")
+        _want(name, x, (rows, heads, L.head_dim), L.dtype, device, True)
+        _want(f"{name}_out", y, (rows, heads, L.head_dim), L.dtype, device, True)
+        if w is not None:
+            _want(f"{name}_weight", w, (L.head_dim,), L.dtype, device)
+        if rows > 1:  # (a row stride only means something where there is a second row)
+            setattr(c, f"{name}_stride", x.stride(0))
+            setattr(c, f"{name}_out_stride", y.stride(0))
+    c.total = rows
+    _check("sfi_qk_norm_rope", lib.sfi_qk_norm_rope(
+        ctypes.byref(c), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(q_out), _ptr(k_out),
+        _stream(stream)))
 
 
 def _ids(v):

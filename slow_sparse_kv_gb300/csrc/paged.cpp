@@ -88,26 +88,38 @@ bool encode_heads(CUtensorMap* m, const void* base, int D, int heads, int rows, 
   return encode_bf16_3d(m, base, dims, st, box);
 }
 
-int64_t elem_bytes(int dtype) { return dtype == SFI_F32 ? 4 : 2; }
+int64_t elem_bytes(int dtype) { return dtype == SFI_F32 ? 4 : dtype == SFI_BF16 ? 2 : 1; }
+bool is_q8(int dtype) { return dtype == SFI_I8 || dtype == SFI_E4M3; }
+
+// Elements of a page: its rows, and in 8 bits (bytes) the scales behind them, in units of 16.
+int64_t whole_page(const sfi_paged_layout* L) {
+  const int64_t rows = int64_t(L->n_kv_heads) * L->page_size;
+  return is_q8(L->dtype) ? (rows * (L->head_dim + 4) + 15) / 16 * 16 : rows * L->head_dim;
+}
+
+// Bytes from an 8-bit page's start to its scales.
+int scale_at(const sfi_paged_layout* L) { return L->n_kv_heads * L->page_size * L->head_dim; }
 
 // Elements between pages (page_stride, or a page where it is 0).
-int64_t page_elems(const sfi_paged_layout* L) {
-  return L->page_stride ? L->page_stride : int64_t(L->n_kv_heads) * L->page_size * L->head_dim;
-}
+int64_t page_elems(const sfi_paged_layout* L) { return L->page_stride ? L->page_stride : whole_page(L); }
 
 // Rows of d elements from the pool's first to its last.
 int64_t pool_rows(const sfi_paged_layout* L) {
   return (L->n_pages - 1) * (page_elems(L) / L->head_dim) + int64_t(L->n_kv_heads) * L->page_size;
 }
 
-sfi_status check_paged(const sfi_paged_layout* L) {
+enum Pool { kPlain = 1, kQ8 = 2, kAny = 3 };  // the types of pool that a call takes
+
+sfi_status check_paged(const sfi_paged_layout* L, Pool takes) {
   if (!L) return fail(SFI_ERR_INVALID_ARG, "layout is NULL");
   if (L->batch < 1) return fail(SFI_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", L->batch);
   if (L->batch > kMaxBatch) return fail(SFI_ERR_CAPACITY, "batch %d exceeds the limit %d", L->batch, kMaxBatch);
   const sfi_status s = check_heads(L->n_q_heads, L->n_kv_heads, L->head_dim);
   if (s != SFI_OK) return s;
-  if (L->dtype != SFI_F32 && L->dtype != SFI_BF16)
-    return fail(SFI_ERR_UNSUPPORTED, "dtype must be SFI_F32 or SFI_BF16 (got %d)", L->dtype);
+  const bool q8 = is_q8(L->dtype), plain = L->dtype == SFI_F32 || L->dtype == SFI_BF16;
+  if (!(plain && (takes & kPlain)) && !(q8 && (takes & kQ8)))
+    return fail(SFI_ERR_UNSUPPORTED, "dtype must be %s%s%s (got %d)", takes & kPlain ? "SFI_F32 or SFI_BF16" : "",
+                takes == kAny ? ", " : "", takes & kQ8 ? "SFI_I8 or SFI_E4M3" : "", L->dtype);
   if ((long long)L->batch * L->n_kv_heads > kMaxUnits)
     return fail(SFI_ERR_CAPACITY, "batch * n_kv_heads = %lld exceeds the limit %d", (long long)L->batch * L->n_kv_heads,
                 kMaxUnits);
@@ -118,13 +130,15 @@ sfi_status check_paged(const sfi_paged_layout* L) {
     return fail(SFI_ERR_CAPACITY,
                 "page_size <= 1024, n_pages <= 2^24, max_pages * page_size <= 2^30 (got %d, %d, %lld)", L->page_size,
                 L->n_pages, (long long)L->max_pages * L->page_size);
-  const int64_t page = int64_t(L->n_kv_heads) * L->page_size * L->head_dim;
-  if (L->page_stride != 0 && (L->page_stride < page || L->page_stride % L->head_dim != 0))
+  const int64_t page = whole_page(L);
+  if (L->page_stride != 0 && (L->page_stride < page || L->page_stride % (q8 ? 16 : L->head_dim) != 0))
     return fail(SFI_ERR_INVALID_ARG,
-                "page_stride (%lld) must be 0, or at least a page of %lld elements and a multiple of head_dim",
-                (long long)L->page_stride, (long long)page);
+                "page_stride (%lld) must be 0, or at least a page of %lld elements and a multiple of %s",
+                (long long)L->page_stride, (long long)page, q8 ? "16" : "head_dim");
   if (page * 4 >= (1LL << 31)) return fail(SFI_ERR_CAPACITY, "a page of %lld elements is too large", (long long)page);
-  if (page_elems(L) >= (1LL << 38) || pool_rows(L) >= (1LL << 31))
+  if (q8 && (page_elems(L) >= (1LL << 38) || L->n_pages * page_elems(L) >= (1LL << 42)))
+    return fail(SFI_ERR_CAPACITY, "the pool spans 2^42 bytes or more");
+  if (!q8 && (page_elems(L) >= (1LL << 38) || pool_rows(L) >= (1LL << 31)))
     return fail(SFI_ERR_CAPACITY, "the pool spans 2^31 rows of head_dim elements or more");
   if (!L->page_table || !L->len) return fail(SFI_ERR_INVALID_ARG, "page_table and len must be device pointers");
   return SFI_OK;
@@ -171,9 +185,10 @@ sfi_status check_store(const sfi_paged_layout* L, const sfi_page_store* S, bool 
   if (misaligned16(S->k) || misaligned16(S->v)) return fail(SFI_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
   if (S->n_layers < 1) return fail(SFI_ERR_INVALID_ARG, "n_layers must be >= 1 (got %d)", S->n_layers);
   if (S->n_layers > 4096) return fail(SFI_ERR_CAPACITY, "n_layers %d exceeds the limit 4096", S->n_layers);
-  if (S->layer_stride < 0 || S->layer_stride % L->head_dim != 0 || (S->n_layers > 1 && S->layer_stride == 0))
-    return fail(SFI_ERR_INVALID_ARG, "layer_stride (%lld) must be a positive multiple of head_dim",
-                (long long)S->layer_stride);
+  const bool q8 = is_q8(L->dtype);
+  if (S->layer_stride < 0 || S->layer_stride % (q8 ? 16 : L->head_dim) != 0 || (S->n_layers > 1 && S->layer_stride == 0))
+    return fail(SFI_ERR_INVALID_ARG, "layer_stride (%lld) must be a positive multiple of %s",
+                (long long)S->layer_stride, q8 ? "16" : "head_dim");
   if (S->layer_stride >= (1LL << 42)) return fail(SFI_ERR_CAPACITY, "layer_stride exceeds 2^42 elements");
   return SFI_OK;
 }
@@ -190,6 +205,8 @@ PageMove move_of(const sfi_paged_layout* L, const sfi_page_store* S, void* ws) {
   m.P = L->page_size;
   m.row_bytes = int(L->head_dim * e);
   m.n_pages = L->n_pages;
+  m.whole = int(whole_page(L) * e);
+  m.scale_at = is_q8(L->dtype) ? scale_at(L) : 0;
   m.status = static_cast<uint32_t*>(ws);
   return m;
 }
@@ -203,6 +220,107 @@ sfi_status take_list(const char* name, const int32_t* v, int n, int batch, bool 
     seen[v[i]] = true;
     out->id[i] = int16_t(v[i]);
   }
+  return SFI_OK;
+}
+
+// Rows that go into an 8-bit pool, or that are multiplied with it.
+sfi_status check_rows_dtype(const char* name, int dtype) {
+  if (dtype != SFI_F32 && dtype != SFI_BF16)
+    return fail(SFI_ERR_UNSUPPORTED, "%s must be SFI_F32 or SFI_BF16 (got %d)", name, dtype);
+  return SFI_OK;
+}
+
+// sfi_paged_attn and sfi_paged_attn_q8, behind the layout's checks.
+sfi_status run_attn(const sfi_paged_layout* L, int q_dtype, const void* q, const void* k, const void* v, float* out,
+                    float* lse_out, void* ws, size_t ws_bytes, sfi_stream stream) {
+  sfi_status s;
+  if (!q || !k || !v || !out) return fail(SFI_ERR_INVALID_ARG, "q, k, v and out must be set");
+  if (misaligned16(q) || misaligned16(k) || misaligned16(v))
+    return fail(SFI_ERR_INVALID_ARG, "q, k and v must be 16-byte aligned");
+  const PagedPlan p = plan_paged(L);
+  if ((s = check_workspace(ws, ws_bytes, p.total)) != SFI_OK) return s;
+  const int D = L->head_dim;
+  char* w = static_cast<char*>(ws);
+  PagedAttnArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.geo = geo_of(L, ws);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.lse = lse_out;
+  a.H_q = L->n_q_heads;
+  a.G = L->n_q_heads / L->n_kv_heads;
+  a.scale_log2 = float(1.4426950408889634 / std::sqrt(double(D)));
+  a.partials = reinterpret_cast<float*>(w + p.partials);
+  a.wait_cycles = wait_limit_cycles();
+  // A tile of 16 positions that lies in one page is one box per tensor; other
+  // page sizes are gathered row by row.
+  bool use_tma = false;
+  if (L->dtype == SFI_BF16 && L->page_size % 16 == 0) {
+    const uint64_t dims[3] = {64, uint64_t(pool_rows(L)), uint64_t(D / 64)};
+    const uint64_t st[2] = {uint64_t(D) * 2, 128};
+    const uint32_t box[3] = {64, 16, uint32_t(D / 64)};
+    use_tma = encode_bf16_3d(&a.tmk, k, dims, st, box) && encode_bf16_3d(&a.tmv, v, dims, st, box);
+    if (!use_tma) return fail(SFI_ERR_CUDA, "encoding the tensor maps of k and v failed");
+  }
+  const int grid = std::min(device_sm_count(), kPagedMaxGrid);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (is_q8(L->dtype)) {
+    a.scale_at = scale_at(L);
+    // (tiles of 32 positions: one box, or two where a page holds an odd number of 16)
+    if (L->page_size % 16 == 0) {
+      a.box = L->page_size % 32 == 0 ? 32 : 16;
+      const uint64_t dims[3] = {uint64_t(D), uint64_t(L->n_kv_heads) * L->page_size, uint64_t(L->n_pages)};
+      const uint64_t strides[2] = {uint64_t(D), uint64_t(page_elems(L))};
+      const uint32_t box[3] = {uint32_t(D), uint32_t(a.box), 1};
+      use_tma = encode_u8_3d(&a.tmk, k, dims, strides, box) && encode_u8_3d(&a.tmv, v, dims, strides, box);
+      if (!use_tma) return fail(SFI_ERR_CUDA, "encoding the tensor maps of k and v failed");
+    }
+    e = launch_paged_attn_q8(a, D, L->dtype == SFI_E4M3, q_dtype == SFI_F32, use_tma, grid, st);
+  } else {
+    e = launch_paged_attn(a, D, L->dtype == SFI_F32, use_tma, grid, st);
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+  return SFI_OK;
+}
+
+// sfi_paged_append and sfi_paged_append_q8, behind the layout's checks.
+sfi_status run_append(const sfi_paged_layout* L, int new_dtype, int32_t total_new, const void* k_new,
+                      const void* v_new, int64_t k_stride, int64_t v_stride, const int32_t* cu_new, void* k, void* v,
+                      void* ws, size_t ws_bytes, sfi_stream stream) {
+  sfi_status s;
+  if (total_new < 0) return fail(SFI_ERR_INVALID_ARG, "total_new must be >= 0 (got %d)", total_new);
+  if (!cu_new && total_new != L->batch)
+    return fail(SFI_ERR_INVALID_ARG, "without cu_new there is a row for each of the %d sequences (got %d)", L->batch,
+                total_new);
+  const int64_t e = elem_bytes(new_dtype), row = int64_t(L->n_kv_heads) * L->head_dim;
+  int64_t ks, vs;
+  if ((s = row_stride("k_stride", k_stride, row, 16 / e, &ks)) != SFI_OK) return s;
+  if ((s = row_stride("v_stride", v_stride, row, 16 / e, &vs)) != SFI_OK) return s;
+  if ((s = check_workspace(ws, ws_bytes, plan_paged(L).total)) != SFI_OK) return s;
+  if (!k || !v || (total_new > 0 && (!k_new || !v_new)))
+    return fail(SFI_ERR_INVALID_ARG, "k_new, v_new, k and v must be set");
+  if (misaligned16(k) || misaligned16(v) || (total_new > 0 && (misaligned16(k_new) || misaligned16(v_new))))
+    return fail(SFI_ERR_INVALID_ARG, "k_new, v_new, k and v must be 16-byte aligned");
+  if (total_new == 0) return SFI_OK;
+  QuantArgs a;
+  a.geo = geo_of(L, ws);
+  a.k_new = static_cast<const uint8_t*>(k_new);
+  a.v_new = static_cast<const uint8_t*>(v_new);
+  a.k = static_cast<uint8_t*>(k);
+  a.v = static_cast<uint8_t*>(v);
+  a.k_stride = ks * e;
+  a.v_stride = vs * e;
+  a.page_bytes = page_elems(L) * elem_bytes(L->dtype);
+  a.cu = cu_new;
+  a.total = total_new;
+  a.row_bytes = int(L->head_dim * elem_bytes(L->dtype));
+  a.scale_at = scale_at(L);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t err = is_q8(L->dtype) ? launch_append_q8(a, new_dtype == SFI_F32, L->dtype == SFI_E4M3, st) : launch_append(a, st);
+  if (err != cudaSuccess) return cuda_fail(err, "append launch");
   return SFI_OK;
 }
 
@@ -276,88 +394,40 @@ sfi_status sfi_prefill_attn(const sfi_packed_layout* L, const void* q, const voi
 }
 
 size_t sfi_paged_workspace_size(const sfi_paged_layout* L) {
-  return check_paged(L) == SFI_OK ? plan_paged(L).total : 0;
+  return check_paged(L, kAny) == SFI_OK ? plan_paged(L).total : 0;
 }
 
 sfi_status sfi_paged_attn(const sfi_paged_layout* L, const void* q, const void* k, const void* v, float* out,
                           float* lse_out, void* ws, size_t ws_bytes, sfi_stream stream) {
-  sfi_status s = check_paged(L);
-  if (s != SFI_OK) return s;
-  if (!q || !k || !v || !out) return fail(SFI_ERR_INVALID_ARG, "q, k, v and out must be set");
-  if (misaligned16(q) || misaligned16(k) || misaligned16(v))
-    return fail(SFI_ERR_INVALID_ARG, "q, k and v must be 16-byte aligned");
-  const PagedPlan p = plan_paged(L);
-  if ((s = check_workspace(ws, ws_bytes, p.total)) != SFI_OK) return s;
-  const int D = L->head_dim;
-  char* w = static_cast<char*>(ws);
-  PagedAttnArgs a;
-  std::memset(&a, 0, sizeof(a));
-  a.geo = geo_of(L, ws);
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.out = out;
-  a.lse = lse_out;
-  a.H_q = L->n_q_heads;
-  a.G = L->n_q_heads / L->n_kv_heads;
-  a.scale_log2 = float(1.4426950408889634 / std::sqrt(double(D)));
-  a.partials = reinterpret_cast<float*>(w + p.partials);
-  a.wait_cycles = wait_limit_cycles();
-  // A tile of 16 positions that lies in one page is one box per tensor; other
-  // page sizes are gathered row by row.
-  bool use_tma = false;
-  if (L->dtype == SFI_BF16 && L->page_size % 16 == 0) {
-    const uint64_t dims[3] = {64, uint64_t(pool_rows(L)), uint64_t(D / 64)};
-    const uint64_t st[2] = {uint64_t(D) * 2, 128};
-    const uint32_t box[3] = {64, 16, uint32_t(D / 64)};
-    use_tma = encode_bf16_3d(&a.tmk, k, dims, st, box) && encode_bf16_3d(&a.tmv, v, dims, st, box);
-    if (!use_tma) return fail(SFI_ERR_CUDA, "encoding the tensor maps of k and v failed");
-  }
-  const int grid = std::min(device_sm_count(), kPagedMaxGrid);
-  const cudaError_t e = launch_paged_attn(a, D, L->dtype == SFI_F32, use_tma, grid, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
-  return SFI_OK;
+  const sfi_status s = check_paged(L, kPlain);
+  return s != SFI_OK ? s : run_attn(L, L->dtype, q, k, v, out, lse_out, ws, ws_bytes, stream);
+}
+
+sfi_status sfi_paged_attn_q8(const sfi_paged_layout* L, int32_t q_dtype, const void* q, const void* k, const void* v,
+                             float* out, float* lse_out, void* ws, size_t ws_bytes, sfi_stream stream) {
+  sfi_status s = check_paged(L, kQ8);
+  if (s == SFI_OK) s = check_rows_dtype("q_dtype", q_dtype);
+  return s != SFI_OK ? s : run_attn(L, q_dtype, q, k, v, out, lse_out, ws, ws_bytes, stream);
 }
 
 sfi_status sfi_paged_append(const sfi_paged_layout* L, int32_t total_new, const void* k_new, const void* v_new,
                             int64_t k_stride, int64_t v_stride, const int32_t* cu_new, void* k, void* v, void* ws,
                             size_t ws_bytes, sfi_stream stream) {
-  sfi_status s = check_paged(L);
-  if (s != SFI_OK) return s;
-  if (total_new < 0) return fail(SFI_ERR_INVALID_ARG, "total_new must be >= 0 (got %d)", total_new);
-  if (!cu_new && total_new != L->batch)
-    return fail(SFI_ERR_INVALID_ARG, "without cu_new there is a row for each of the %d sequences (got %d)", L->batch,
-                total_new);
-  const int64_t e = elem_bytes(L->dtype), row = int64_t(L->n_kv_heads) * L->head_dim;
-  int64_t ks, vs;
-  if ((s = row_stride("k_stride", k_stride, row, 16 / e, &ks)) != SFI_OK) return s;
-  if ((s = row_stride("v_stride", v_stride, row, 16 / e, &vs)) != SFI_OK) return s;
-  if ((s = check_workspace(ws, ws_bytes, plan_paged(L).total)) != SFI_OK) return s;
-  if (!k || !v || (total_new > 0 && (!k_new || !v_new)))
-    return fail(SFI_ERR_INVALID_ARG, "k_new, v_new, k and v must be set");
-  if (misaligned16(k) || misaligned16(v) || (total_new > 0 && (misaligned16(k_new) || misaligned16(v_new))))
-    return fail(SFI_ERR_INVALID_ARG, "k_new, v_new, k and v must be 16-byte aligned");
-  if (total_new == 0) return SFI_OK;
-  AppendArgs a;
-  a.geo = geo_of(L, ws);
-  a.k_new = static_cast<const uint8_t*>(k_new);
-  a.v_new = static_cast<const uint8_t*>(v_new);
-  a.k = static_cast<uint8_t*>(k);
-  a.v = static_cast<uint8_t*>(v);
-  a.k_stride = ks * e;
-  a.v_stride = vs * e;
-  a.page_bytes = page_elems(L) * e;
-  a.cu = cu_new;
-  a.total = total_new;
-  a.row_bytes = int(L->head_dim * e);
-  const cudaError_t err = launch_append(a, static_cast<cudaStream_t>(stream));
-  if (err != cudaSuccess) return cuda_fail(err, "append launch");
-  return SFI_OK;
+  const sfi_status s = check_paged(L, kPlain);
+  return s != SFI_OK ? s : run_append(L, L->dtype, total_new, k_new, v_new, k_stride, v_stride, cu_new, k, v, ws, ws_bytes, stream);
+}
+
+sfi_status sfi_paged_append_q8(const sfi_paged_layout* L, int32_t new_dtype, int32_t total_new, const void* k_new,
+                               const void* v_new, int64_t k_stride, int64_t v_stride, const int32_t* cu_new, void* k,
+                               void* v, void* ws, size_t ws_bytes, sfi_stream stream) {
+  sfi_status s = check_paged(L, kQ8);
+  if (s == SFI_OK) s = check_rows_dtype("new_dtype", new_dtype);
+  return s != SFI_OK ? s : run_append(L, new_dtype, total_new, k_new, v_new, k_stride, v_stride, cu_new, k, v, ws, ws_bytes, stream);
 }
 
 sfi_status sfi_pages_extend(const sfi_paged_layout* L, const sfi_page_store* S, const int32_t* n_new, void* ws,
                             size_t ws_bytes, sfi_stream stream) {
-  sfi_status s = check_paged(L);
+  sfi_status s = check_paged(L, kAny);
   if (s != SFI_OK) return s;
   if ((s = check_store(L, S, false)) != SFI_OK) return s;
   const PagedPlan p = plan_paged(L);
@@ -370,7 +440,7 @@ sfi_status sfi_pages_extend(const sfi_paged_layout* L, const sfi_page_store* S, 
 
 sfi_status sfi_pages_fork(const sfi_paged_layout* L, const sfi_page_store* S, const int32_t* src, const int32_t* dst,
                           int32_t n, void* ws, size_t ws_bytes, sfi_stream stream) {
-  sfi_status s = check_paged(L);
+  sfi_status s = check_paged(L, kAny);
   if (s != SFI_OK) return s;
   if ((s = check_store(L, S, true)) != SFI_OK) return s;
   if ((s = check_list_size(n, L->batch)) != SFI_OK) return s;
@@ -394,7 +464,7 @@ sfi_status sfi_pages_fork(const sfi_paged_layout* L, const sfi_page_store* S, co
 
 sfi_status sfi_pages_free(const sfi_paged_layout* L, const sfi_page_store* S, const int32_t* seqs, int32_t n, void* ws,
                           size_t ws_bytes, sfi_stream stream) {
-  sfi_status s = check_paged(L);
+  sfi_status s = check_paged(L, kAny);
   if (s != SFI_OK) return s;
   if ((s = check_store(L, S, false)) != SFI_OK) return s;
   if ((s = check_list_size(n, L->batch)) != SFI_OK) return s;
@@ -410,7 +480,7 @@ sfi_status sfi_pages_free(const sfi_paged_layout* L, const sfi_page_store* S, co
 
 sfi_status sfi_pages_compact(const sfi_paged_layout* L, const sfi_page_store* S, int32_t* new_id, void* ws,
                              size_t ws_bytes, sfi_stream stream) {
-  sfi_status s = check_paged(L);
+  sfi_status s = check_paged(L, kAny);
   if (s != SFI_OK) return s;
   if ((s = check_store(L, S, true)) != SFI_OK) return s;
   const PagedPlan p = plan_paged(L);
@@ -426,7 +496,7 @@ sfi_status sfi_pages_compact(const sfi_paged_layout* L, const sfi_page_store* S,
 
 sfi_status sfi_pages_copy(const sfi_paged_layout* L, const sfi_page_store* S, const int32_t* src, const int32_t* dst,
                           int32_t n, void* ws, size_t ws_bytes, sfi_stream stream) {
-  sfi_status s = check_paged(L);
+  sfi_status s = check_paged(L, kAny);
   if (s != SFI_OK) return s;
   if ((s = check_store(L, S, true)) != SFI_OK) return s;
   if (n < 0 || n > L->n_pages) return fail(SFI_ERR_INVALID_ARG, "n must lie in [0, n_pages] (got %d)", n);

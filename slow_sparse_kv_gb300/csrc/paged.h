@@ -11,7 +11,7 @@ constexpr int kPagedMaxGrid = 256;  // CTAs of a paged-attention launch, at most
 // Geometry of a paged cache on the device.
 struct PagedGeo {
   int32_t B, H_kv, P, n_pages, max_pages;
-  int64_t page_stride;  // elements
+  int64_t page_stride;  // elements (bytes of an 8-bit pool)
   int32_t* table;
   int32_t* len;
   uint32_t* status;
@@ -32,7 +32,15 @@ struct PagedAttnArgs {
   float scale_log2;   // log2(e) / sqrt(d)
   float* partials;    // [grid + B * H_kv][G][d + 2]
   long long wait_cycles;
+  // 8-bit pools
+  int32_t scale_at;   // bytes from a page's start to its scales
+  int32_t box;        // rows of the maps' boxes (where there are maps): 32 or 16
 };
+
+// The same over an 8-bit pool.  use_tma: the maps are set, 3-D maps (d bytes, row of a page, page)
+// with a swizzle of d bytes.
+cudaError_t launch_paged_attn_q8(const PagedAttnArgs& a, int D, bool e4m3, bool q_f32, bool use_tma, int grid,
+                                 cudaStream_t st);
 
 // use_tma: the maps are set
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int D, bool f32, bool use_tma, int grid,
@@ -52,6 +60,12 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st);
 
+// The same into an 8-bit pool: row_bytes is that of codes, the strides are bytes of the new rows.
+struct QuantArgs : AppendArgs {
+  int32_t scale_at;  // bytes from a page's start to its scales
+};
+cudaError_t launch_append_q8(const QuantArgs& a, bool f32, bool e4m3, cudaStream_t st);
+
 // Sequences named by the host, passed by value.
 struct SeqList {
   int16_t id[kMaxBatch];
@@ -63,6 +77,8 @@ struct PageMove {
   uint8_t* v;
   int64_t layer_bytes, page_bytes;  // strides
   int32_t n_layers, H_kv, P, row_bytes, n_pages;
+  int32_t whole;     // bytes of a page
+  int32_t scale_at;  // 8-bit pools: bytes from a page's start to its scales; 0: none
   uint32_t* status;
 };
 

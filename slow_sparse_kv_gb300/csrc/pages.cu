@@ -302,6 +302,12 @@ __global__ void __launch_bounds__(kCopy) fork_copy_kernel(const __grid_constant_
     y /= mv.H_kv;
     const int bytes = job.z * mv.row_bytes - sl * kSlice;
     if (bytes <= 0) continue;
+    if (mv.scale_at && sl == 0) {
+      uint8_t* const scales = ((y & 1) ? mv.v : mv.k) + (y >> 1) * mv.layer_bytes + mv.scale_at + int64_t(h) * mv.P * 4;
+      for (int r = threadIdx.x; r < job.z; r += kCopy)
+        reinterpret_cast<float*>(scales + job.y * mv.page_bytes)[r] =
+            reinterpret_cast<const float*>(scales + job.x * mv.page_bytes)[r];
+    }
     uint8_t* const pool = ((y & 1) ? mv.v : mv.k) + (y >> 1) * mv.layer_bytes + int64_t(h) * mv.P * mv.row_bytes +
                           int64_t(sl) * kSlice;
     copy_slice(pool + job.y * mv.page_bytes, pool + job.x * mv.page_bytes, min(kSlice, bytes));
@@ -312,7 +318,7 @@ __global__ void __launch_bounds__(kCopy) page_copy_kernel(const __grid_constant_
                                                           const int32_t* dst, int n) {
   pdl_launch();
   pdl_wait();
-  const int bytes = mv.H_kv * mv.P * mv.row_bytes, slices = (bytes + kSlice - 1) / kSlice;
+  const int bytes = mv.whole, slices = (bytes + kSlice - 1) / kSlice;
   const int per = mv.n_layers * 2 * slices;
   for (long long x = blockIdx.x; x < (long long)per * n; x += gridDim.x) {
     const int i = int(div_fast(x, per)), from = src[i], to = dst[i];
@@ -399,7 +405,7 @@ __global__ void __launch_bounds__(kCopy) compact_kernel(const __grid_constant__ 
       else if (m < -1) row[i] = holes[-2 - m];
     }
   }
-  const int bytes = mv.H_kv * mv.P * mv.row_bytes, slices = (bytes + kSlice - 1) / kSlice;
+  const int bytes = mv.whole, slices = (bytes + kSlice - 1) / kSlice;
   const int per = mv.n_layers * 2 * slices;
   for (long long x = blockIdx.x; x < (long long)per * n; x += gridDim.x) {
     const int i = int(div_fast(x, per));
@@ -440,6 +446,135 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, int b, int m, in
   }
 }
 
+// The largest magnitude of a row's elements, 8 in each of LPH lanes, as its bits (those of
+// an infinity or a NaN are larger than any number's).
+template <int LPH>
+__device__ __forceinline__ uint32_t row_top(const float (&x)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+  for (int w = 1; w < LPH; w <<= 1) top = max(top, __shfl_xor_sync(kFull, top, w));
+  return top;
+}
+
+// Codes of 8 elements of a row whose largest magnitude is `top` (bits), and the row's scale.
+//
+// int8: x / s is rounded as if it were exact.  n = rint(x * (1 / s)) is off by one at most, and
+// only next to a tie; e = x - n s is exact in fp32 (a multiple of the smaller of both
+// last places, below s in magnitude), so comparing it with s / 2 decides: half of the maximum
+// is such a tie in every row (63.5), and the rounded quotient would put it on either side.
+// (Rows below 2^-60 are scaled up by 2^80 with their scale, so that nothing underflows.)
+// e4m3: the scale is a power of two, so x / s is exact and the conversion rounds once.
+template <bool E4M3>
+__device__ __forceinline__ uint2 quantise(float (&x)[8], uint32_t top, float* scale) {
+  if (top >= 0x7f800000u) {
+    *scale = __uint_as_float(0x7fc00000u);
+    return make_uint2(0, 0);
+  }
+  const float amax = __uint_as_float(top);
+  uint32_t w[2] = {0, 0};
+  if constexpr (E4M3) {
+    // amax = m 2^e, 1 <= m < 2, and 448 = 1.75 * 2^8 (subnormal maxima are scaled up for this)
+    const bool tiny = amax < 0x1p-126f;
+    const uint32_t bits = tiny ? __float_as_uint(amax * 0x1p64f) : top;
+    const int k = int(bits >> 23) - 127 - (tiny ? 64 : 0) - 8 + ((bits & 0x7fffffu) > 0x600000u);
+    const float s = amax == 0.f || k < -149 ? 0.f : k < -126 ? __uint_as_float(1u << (k + 149)) : __uint_as_float(uint32_t(k + 127) << 23);
+    *scale = s;
+    if (s == 0.f) return make_uint2(0, 0);
+    const int k0 = -k / 2, k1 = -k - k0;  // (1 / s may be beyond fp32)
+    const float f0 = __uint_as_float(uint32_t(k0 + 127) << 23), f1 = __uint_as_float(uint32_t(k1 + 127) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint16_t c;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(x[2 * i + 1] * f0 * f1), "f"(x[2 * i] * f0 * f1));
+      w[i / 2] |= uint32_t(c) << (i % 2 * 16);
+    }
+  } else {
+    float s = amax / 127.f;
+    *scale = s;
+    if (s == 0.f) return make_uint2(0, 0);
+    const float up = amax < 0x1p-60f ? 0x1p80f : 1.f;
+    s *= up;
+    const float inv = 1.f / s, half = 0.5f * s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = x[i] * up;
+      float n = rintf(y * inv);
+      const float e = fmaf(-n, s, y);
+      const int odd = int(n) & 1;
+      if (fabsf(e) > half || (fabsf(e) == half && odd)) n += copysignf(1.f, e);
+      n = fminf(fmaxf(n, -127.f), 127.f);
+      w[i / 4] |= (uint32_t(int(n)) & 0xffu) << (i % 4 * 8);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]);
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void load8<bf16_t>(const bf16_t* p, float (&x)[8]) {
+  Unpack<bf16_t>::run(__ldcs(reinterpret_cast<const uint4*>(p)), x);
+}
+
+// A token's rows into an 8-bit pool: d / 8 lanes a head, K and V of `AHEAD` heads read at once.
+template <typename T, bool E4M3, int D>
+struct Quant : QuantArgs {};
+
+template <typename T, bool E4M3, int D>
+__device__ __forceinline__ void append_row(const Quant<T, E4M3, D>& a, int b, int m, int back, int t, int cap, int lane) {
+  constexpr int LPH = D / 8, HPW = 32 / LPH, AHEAD = sizeof(T) == 4 ? 1 : 2;
+  const PagedGeo& g = a.geo;
+  const int n = g.len[b];
+  const uint32_t refused = g.refused[b >> 5] >> (b & 31) & 1;
+  if ((n < 0) | (n > cap) | (m > n) | refused) return;
+  const int pos = n - back;
+  const int page = g.table[int64_t(b) * g.max_pages + pos / g.P];
+  if (page < 0 || page >= g.n_pages) {
+    if (lane == 0) set_status(g.status, SFI_DEV_BAD_INDEX);
+    return;
+  }
+  const T* const src[2] = {reinterpret_cast<const T*>(a.k_new + t * a.k_stride),
+                           reinterpret_cast<const T*>(a.v_new + t * a.v_stride)};
+  const int64_t at = page * a.page_bytes;
+  uint8_t* const dst[2] = {a.k + at, a.v + at};
+  const int in = pos % g.P, u = lane % LPH;
+  for (int h0 = lane / LPH; h0 - lane / LPH < g.H_kv; h0 += AHEAD * HPW) {
+    float x[AHEAD][2][8];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int h = h0 + i * HPW;
+        if (h < g.H_kv) {
+          load8<T>(src[y] + h * D + u * 8, x[i][y]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[i][y][e] = 0.f;
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const uint32_t top = row_top<LPH>(x[i][y]);
+        float scale;
+        const uint2 codes = quantise<E4M3>(x[i][y], top, &scale);
+        const int h = h0 + i * HPW;
+        if (h >= g.H_kv) continue;
+        const int64_t row = int64_t(h) * g.P + in;
+        *reinterpret_cast<uint2*>(dst[y] + row * D + u * 8) = codes;
+        if (u == 0) *reinterpret_cast<float*>(dst[y] + a.scale_at + row * 4) = scale;
+      }
+  }
+}
+
 // New rows into their pages: a warp takes one token's K and V, for each sequence that
 // holds the token: one, where the offsets ascend; where some do not, those that are in
 // order are stored all the same, so all pairs are looked through (by each warp for its
@@ -447,7 +582,8 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, int b, int m, in
 // some).  A sequence that an extension refused holds the length from before it: the rows
 // would go over its last ones, which may lie in pages that others share, so it is left
 // out.  The last CTA only looks for what is to be flagged.
-__global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ AppendArgs a) {
+template <typename Args>
+__global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ Args a) {
   constexpr int kWarps = kCopy / 32;
   __shared__ uint32_t mask[kMaxBatch / 32];  // sequences with rows among the CTA's tokens
   static_assert(kMaxBatch / 32 == 32, "a lane for every word");
@@ -509,13 +645,28 @@ int copy_grid(long long items) {
 }
 
 long long page_slices(const PageMove& mv) {
-  return (long long)mv.n_layers * 2 * (((long long)mv.H_kv * mv.P * mv.row_bytes + kSlice - 1) / kSlice);
+  return (long long)mv.n_layers * 2 * ((mv.whole + kSlice - 1LL) / kSlice);
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
-  return launch_pdl(append_kernel, dim3((a.total - 1) / (kCopy / 32) + 2), kCopy, 0, st, a);
+  return launch_pdl(append_kernel<AppendArgs>, dim3((a.total - 1) / (kCopy / 32) + 2), kCopy, 0, st, a);
+}
+
+template <typename T, bool E4M3, int D>
+static cudaError_t launch_quant(const QuantArgs& a, cudaStream_t st) {
+  return launch_pdl(append_kernel<Quant<T, E4M3, D>>, dim3((a.total - 1) / (kCopy / 32) + 2), kCopy, 0, st,
+                    Quant<T, E4M3, D>{a});
+}
+
+cudaError_t launch_append_q8(const QuantArgs& a, bool f32, bool e4m3, cudaStream_t st) {
+  if (a.row_bytes == 64) {
+    if (f32) return e4m3 ? launch_quant<float, true, 64>(a, st) : launch_quant<float, false, 64>(a, st);
+    return e4m3 ? launch_quant<bf16_t, true, 64>(a, st) : launch_quant<bf16_t, false, 64>(a, st);
+  }
+  if (f32) return e4m3 ? launch_quant<float, true, 128>(a, st) : launch_quant<float, false, 128>(a, st);
+  return e4m3 ? launch_quant<bf16_t, true, 128>(a, st) : launch_quant<bf16_t, false, 128>(a, st);
 }
 
 cudaError_t launch_extend(const PagedGeo& g, int32_t* ref, const int32_t* n_new, int32_t* fresh, cudaStream_t st) {

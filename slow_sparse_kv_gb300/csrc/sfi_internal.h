@@ -185,6 +185,9 @@ void attach_tensor_maps(AttnArgs& a, const sfi_layout* L);
 // the extents read as zero.
 bool encode_bf16_3d(CUtensorMap* m, const void* base, const uint64_t (&dims)[3],
                     const uint64_t (&strides)[2], const uint32_t (&box)[3]);
+// The same of bytes, boxes of 64 or 128 in dimension 0, which is their swizzle.
+bool encode_u8_3d(CUtensorMap* m, const void* base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
+                  const uint32_t (&box)[3]);
 sfi_status fail(sfi_status s, const char* fmt, ...);
 sfi_status cuda_fail(cudaError_t e, const char* what);
 
