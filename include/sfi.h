@@ -478,6 +478,32 @@ sfi_status sfi_paged_attn(const sfi_paged_layout* layout, const void* q, const v
                           const void* v, float* out, float* lse_out, void* ws, size_t ws_bytes,
                           sfi_stream stream);
 
+/* sfi_paged_attn for sequences of which groups share their first pages, as after
+ * sfi_pages_fork: what a group shares is read once for all its sequences.  Group i is the
+ * sequences [cu_group[i], cu_group[i + 1]) (device [n_groups + 1], ascending); they share
+ * their first shared_pages[i] pages (device [n_groups]; full pages, so shared_pages[i] *
+ * page_size <= len[b] for each of them), whose entries the call reads in the first
+ * sequence's row of the table only.  Sequences of no group, a group of one and one that shares
+ * no page are attended to as by sfi_paged_attn.
+ *  - bf16 pools; any page size (multiples of 8 load fastest).  n_groups <= 1024; 0 (the
+ *    two arrays may be NULL) is sfi_paged_attn.  out is 16-byte aligned.
+ *  - Offsets that descend or leave [0, batch] set SFI_DEV_LEN_OVER_CAP, and no group shares
+ *    anything; a number of pages outside [0, max_pages], or more than one of the group's
+ *    sequences holds, sets it too, and that group shares nothing: each then reads its own
+ *    row of the table, and the result is the same.
+ *  - Probabilities of the shared part are the sum of two bf16 terms (16 bits), all else is
+ *    fp32.  An element of V in the shared part that is not finite may make its column of the
+ *    group's outputs NaN where it would be infinite.
+ *  - The same call gives the same bits.
+ * The workspace (sfi_paged_shared_workspace_size, 0 for invalid arguments; it grows with
+ * n_groups, and one for more groups serves fewer) holds that of the paged calls and serves them
+ * too.  Four launches. */
+size_t sfi_paged_shared_workspace_size(const sfi_paged_layout* layout, int32_t n_groups);
+sfi_status sfi_paged_attn_shared(const sfi_paged_layout* layout, int32_t n_groups,
+                                 const int32_t* cu_group, const int32_t* shared_pages,
+                                 const void* q, const void* k, const void* v, float* out,
+                                 float* lse_out, void* ws, size_t ws_bytes, sfi_stream stream);
+
 /* Store new rows: sequence b's m = cu_new[b + 1] - cu_new[b] rows
  * [cu_new[b], cu_new[b + 1]) of k_new and v_new ([total_new] rows of H_kv heads
  * of d, k_stride and v_stride elements apart, 0: without gaps, else a multiple

@@ -114,6 +114,9 @@ EXPORTS = {
                                  c_size_t, c_void_p]),
     "sfi_paged_append": (c_int32, [_PL, c_int32, c_void_p, c_void_p, c_int64, c_int64, c_void_p,
                                    c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "sfi_paged_shared_workspace_size": (c_size_t, [_PL, c_int32]),
+    "sfi_paged_attn_shared": (c_int32, [_PL, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                        c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "sfi_paged_attn_q8": (c_int32, [_PL, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                     c_void_p, c_size_t, c_void_p]),
     "sfi_paged_append_q8": (c_int32, [_PL, c_int32, c_int32, c_void_p, c_void_p, c_int64, c_int64,
@@ -532,6 +535,37 @@ def sfi_paged_append(layout: PagedLayout, k_new, v_new, k, v, cu_new=None, ws=No
     _check("sfi_paged_append", lib.sfi_paged_append(
         ctypes.byref(L.c), new[0], _ptr(k_new), _ptr(v_new), ks, vs, _ptr(cu_new), _ptr(k), _ptr(v),
         *_ws(ws, L.device), _stream(stream)))
+
+
+def paged_shared_workspace(layout: PagedLayout, n_groups: Optional[int] = None) -> torch.Tensor:
+    """A zero-filled workspace for sfi_paged_attn_shared with up to n_groups groups (None: any
+    grouping), which serves the other paged calls of this geometry too."""
+    n_groups = layout.B if n_groups is None else int(n_groups)
+    n = int(lib.sfi_paged_shared_workspace_size(ctypes.byref(layout.c), n_groups))
+    if n == 0:
+        raise SfiError("sfi_paged_shared_workspace_size", SFI_ERR_INVALID_ARG)
+    return torch.zeros(n, dtype=torch.uint8, device=layout.device)
+
+
+def sfi_paged_attn_shared(layout: PagedLayout, cu_group, shared_pages, q, k, v, out, lse_out=None, ws=None,
+                          stream=None):
+    """sfi_paged_attn where the sequences cu_group[i]..cu_group[i + 1] share their first
+    shared_pages[i] pages (int32 device tensors of n_groups + 1 and n_groups entries)."""
+    L = layout
+    _here(L.device, stream)
+    n = shared_pages.numel()
+    _want("shared_pages", shared_pages, (n,), torch.int32, L.device)
+    _want("cu_group", cu_group, (n + 1,), torch.int32, L.device)
+    rq = (L.B, L.n_q_heads, L.head_dim)
+    _want("q", q, rq, L.dtype, L.device)
+    L._pool("k", k)
+    L._pool("v", v)
+    _want("out", out, rq, torch.float32, L.device)
+    if lse_out is not None:
+        _want("lse_out", lse_out, rq[:2], torch.float32, L.device)
+    _check("sfi_paged_attn_shared", lib.sfi_paged_attn_shared(
+        ctypes.byref(L.c), n, _ptr(cu_group), _ptr(shared_pages), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+        _ptr(lse_out), *_ws(ws, L.device), _stream(stream)))
 
 
 def _rows_code(name: str, t: torch.Tensor) -> int:

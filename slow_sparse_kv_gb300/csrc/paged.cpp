@@ -9,6 +9,7 @@
 
 #include "paged.h"
 #include "prefill.h"
+#include "shared.h"
 #include "sfi_internal.h"
 
 namespace sfi {
@@ -174,7 +175,7 @@ PagedPlan plan_paged(const sfi_paged_layout* L) {
 PagedGeo geo_of(const sfi_paged_layout* L, void* ws) {
   return PagedGeo{L->batch,  L->n_kv_heads, L->page_size, L->n_pages,
                   L->max_pages, page_elems(L), L->page_table, L->len, static_cast<uint32_t*>(ws),
-                  reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + kRefusedAt)};
+                  reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + kRefusedAt), nullptr};
 }
 
 sfi_status check_store(const sfi_paged_layout* L, const sfi_page_store* S, bool rows) {
@@ -223,6 +224,46 @@ sfi_status take_list(const char* name, const int32_t* v, int n, int batch, bool 
   return SFI_OK;
 }
 
+// Maps of a bf16 pool's rows of k and v, boxes of `box` rows and `halves` blocks of 64 elements.
+bool encode_pools(CUtensorMap* mk, CUtensorMap* mv, const sfi_paged_layout* L, const void* k, const void* v, int box,
+                  int halves) {
+  const int D = L->head_dim;
+  const uint64_t dims[3] = {64, uint64_t(pool_rows(L)), uint64_t(D / 64)};
+  const uint64_t st[2] = {uint64_t(D) * 2, 128};
+  const uint32_t b[3] = {64, uint32_t(box), uint32_t(halves)};
+  return encode_bf16_3d(mk, k, dims, st, b) && encode_bf16_3d(mv, v, dims, st, b);
+}
+
+// What sfi_paged_attn_shared keeps behind the paged calls' workspace.
+struct SharedWs {
+  size_t skip, plan, states, total;
+  int max_tiles;
+};
+
+SharedWs plan_shared(const sfi_paged_layout* L, int n_groups) {
+  const int per = 2 * (128 / (L->n_q_heads / L->n_kv_heads));  // sequences of a tile
+  SharedWs w;
+  // (a group that shares has two sequences at least)
+  w.max_tiles = std::min(L->batch / 2, n_groups + L->batch / per);
+  if (n_groups == 0) w.max_tiles = 0;
+  w.skip = plan_paged(L).total;
+  w.plan = w.skip + align256(size_t(L->batch) * 4);
+  w.states = w.plan + align256(sizeof(SharedPlan));
+  w.total = w.states;
+  if (w.max_tiles > 0)
+    w.total += (size_t(w.max_tiles) * L->n_kv_heads + kPagedMaxGrid) * kTileRows * (L->head_dim + 2) * 4;
+  return w;
+}
+
+sfi_status check_groups(const sfi_paged_layout* L, int n_groups) {
+  const sfi_status s = check_paged(L, kPlain);
+  if (s != SFI_OK) return s;
+  if (L->dtype != SFI_BF16) return fail(SFI_ERR_UNSUPPORTED, "attention over shared prefixes takes bf16 (dtype %d)", L->dtype);
+  if (n_groups < 0) return fail(SFI_ERR_INVALID_ARG, "n_groups must be >= 0 (got %d)", n_groups);
+  if (n_groups > kMaxBatch) return fail(SFI_ERR_CAPACITY, "n_groups %d exceeds the limit %d", n_groups, kMaxBatch);
+  return SFI_OK;
+}
+
 // Rows that go into an 8-bit pool, or that are multiplied with it.
 sfi_status check_rows_dtype(const char* name, int dtype) {
   if (dtype != SFI_F32 && dtype != SFI_BF16)
@@ -230,18 +271,17 @@ sfi_status check_rows_dtype(const char* name, int dtype) {
   return SFI_OK;
 }
 
-// sfi_paged_attn and sfi_paged_attn_q8, behind the layout's checks.
-sfi_status run_attn(const sfi_paged_layout* L, int q_dtype, const void* q, const void* k, const void* v, float* out,
-                    float* lse_out, void* ws, size_t ws_bytes, sfi_stream stream) {
-  sfi_status s;
+// The arguments of the attentions of one token, behind the layout's checks.
+sfi_status fill_attn(const sfi_paged_layout* L, const void* q, const void* k, const void* v, float* out,
+                     float* lse_out, void* ws, size_t ws_bytes, size_t need, PagedAttnArgs* args, bool* use_tma) {
   if (!q || !k || !v || !out) return fail(SFI_ERR_INVALID_ARG, "q, k, v and out must be set");
   if (misaligned16(q) || misaligned16(k) || misaligned16(v))
     return fail(SFI_ERR_INVALID_ARG, "q, k and v must be 16-byte aligned");
+  const sfi_status s = check_workspace(ws, ws_bytes, need);
+  if (s != SFI_OK) return s;
   const PagedPlan p = plan_paged(L);
-  if ((s = check_workspace(ws, ws_bytes, p.total)) != SFI_OK) return s;
   const int D = L->head_dim;
-  char* w = static_cast<char*>(ws);
-  PagedAttnArgs a;
+  PagedAttnArgs& a = *args;
   std::memset(&a, 0, sizeof(a));
   a.geo = geo_of(L, ws);
   a.q = q;
@@ -252,36 +292,38 @@ sfi_status run_attn(const sfi_paged_layout* L, int q_dtype, const void* q, const
   a.H_q = L->n_q_heads;
   a.G = L->n_q_heads / L->n_kv_heads;
   a.scale_log2 = float(1.4426950408889634 / std::sqrt(double(D)));
-  a.partials = reinterpret_cast<float*>(w + p.partials);
+  a.partials = reinterpret_cast<float*>(static_cast<char*>(ws) + p.partials);
   a.wait_cycles = wait_limit_cycles();
-  // A tile of 16 positions that lies in one page is one box per tensor; other
-  // page sizes are gathered row by row.
-  bool use_tma = false;
-  if (L->dtype == SFI_BF16 && L->page_size % 16 == 0) {
-    const uint64_t dims[3] = {64, uint64_t(pool_rows(L)), uint64_t(D / 64)};
-    const uint64_t st[2] = {uint64_t(D) * 2, 128};
-    const uint32_t box[3] = {64, 16, uint32_t(D / 64)};
-    use_tma = encode_bf16_3d(&a.tmk, k, dims, st, box) && encode_bf16_3d(&a.tmv, v, dims, st, box);
-    if (!use_tma) return fail(SFI_ERR_CUDA, "encoding the tensor maps of k and v failed");
-  }
-  const int grid = std::min(device_sm_count(), kPagedMaxGrid);
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
+  // A tile of 16 positions that lies in one page is one box per tensor (in 8 bits 32: one box,
+  // or two where a page holds an odd number of 16); other page sizes are gathered row by row.
+  *use_tma = L->dtype != SFI_F32 && L->page_size % 16 == 0;
+  bool ok = true;
   if (is_q8(L->dtype)) {
     a.scale_at = scale_at(L);
-    // (tiles of 32 positions: one box, or two where a page holds an odd number of 16)
-    if (L->page_size % 16 == 0) {
-      a.box = L->page_size % 32 == 0 ? 32 : 16;
-      const uint64_t dims[3] = {uint64_t(D), uint64_t(L->n_kv_heads) * L->page_size, uint64_t(L->n_pages)};
-      const uint64_t strides[2] = {uint64_t(D), uint64_t(page_elems(L))};
-      const uint32_t box[3] = {uint32_t(D), uint32_t(a.box), 1};
-      use_tma = encode_u8_3d(&a.tmk, k, dims, strides, box) && encode_u8_3d(&a.tmv, v, dims, strides, box);
-      if (!use_tma) return fail(SFI_ERR_CUDA, "encoding the tensor maps of k and v failed");
-    }
-    e = launch_paged_attn_q8(a, D, L->dtype == SFI_E4M3, q_dtype == SFI_F32, use_tma, grid, st);
-  } else {
-    e = launch_paged_attn(a, D, L->dtype == SFI_F32, use_tma, grid, st);
+    a.box = L->page_size % 32 == 0 ? 32 : 16;
+    const uint64_t dims[3] = {uint64_t(D), uint64_t(L->n_kv_heads) * L->page_size, uint64_t(L->n_pages)};
+    const uint64_t strides[2] = {uint64_t(D), uint64_t(page_elems(L))};
+    const uint32_t box[3] = {uint32_t(D), uint32_t(a.box), 1};
+    if (*use_tma) ok = encode_u8_3d(&a.tmk, k, dims, strides, box) && encode_u8_3d(&a.tmv, v, dims, strides, box);
+  } else if (*use_tma) {
+    ok = encode_pools(&a.tmk, &a.tmv, L, k, v, 16, D / 64);
   }
+  return ok ? SFI_OK : fail(SFI_ERR_CUDA, "encoding the tensor maps of k and v failed");
+}
+
+int attn_grid() { return std::min(device_sm_count(), kPagedMaxGrid); }
+
+// sfi_paged_attn and sfi_paged_attn_q8, behind the layout's checks.
+sfi_status run_attn(const sfi_paged_layout* L, int q_dtype, const void* q, const void* k, const void* v, float* out,
+                    float* lse_out, void* ws, size_t ws_bytes, sfi_stream stream) {
+  PagedAttnArgs a;
+  bool use_tma;
+  const sfi_status s = fill_attn(L, q, k, v, out, lse_out, ws, ws_bytes, plan_paged(L).total, &a, &use_tma);
+  if (s != SFI_OK) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      is_q8(L->dtype) ? launch_paged_attn_q8(a, L->head_dim, L->dtype == SFI_E4M3, q_dtype == SFI_F32, use_tma, attn_grid(), st)
+                      : launch_paged_attn(a, L->head_dim, L->dtype == SFI_F32, use_tma, attn_grid(), st);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   return SFI_OK;
 }
@@ -408,6 +450,51 @@ sfi_status sfi_paged_attn_q8(const sfi_paged_layout* L, int32_t q_dtype, const v
   sfi_status s = check_paged(L, kQ8);
   if (s == SFI_OK) s = check_rows_dtype("q_dtype", q_dtype);
   return s != SFI_OK ? s : run_attn(L, q_dtype, q, k, v, out, lse_out, ws, ws_bytes, stream);
+}
+
+size_t sfi_paged_shared_workspace_size(const sfi_paged_layout* L, int32_t n_groups) {
+  return check_groups(L, n_groups) == SFI_OK ? plan_shared(L, n_groups).total : 0;
+}
+
+sfi_status sfi_paged_attn_shared(const sfi_paged_layout* L, int32_t n_groups, const int32_t* cu_group,
+                                 const int32_t* shared_pages, const void* q, const void* k, const void* v, float* out,
+                                 float* lse_out, void* ws, size_t ws_bytes, sfi_stream stream) {
+  sfi_status s = check_groups(L, n_groups);
+  if (s != SFI_OK) return s;
+  if (n_groups > 0 && (!cu_group || !shared_pages))
+    return fail(SFI_ERR_INVALID_ARG, "cu_group and shared_pages must be device pointers");
+  if (reinterpret_cast<uintptr_t>(out) % 16 != 0) return fail(SFI_ERR_INVALID_ARG, "out must be 16-byte aligned");
+  const SharedWs w = plan_shared(L, n_groups);
+  SharedArgs a;
+  std::memset(&a, 0, sizeof(a));
+  bool use_tma;
+  if ((s = fill_attn(L, q, k, v, out, lse_out, ws, ws_bytes, w.total, &a.own, &use_tma)) != SFI_OK) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int D = L->head_dim, grid = attn_grid();
+  if (w.max_tiles == 0) {  // nobody shares anything
+    const cudaError_t e = launch_paged_attn(a.own, D, false, use_tma, grid, st);
+    return e == cudaSuccess ? SFI_OK : cuda_fail(e, "paged attention launch");
+  }
+  char* const base = static_cast<char*>(ws);
+  a.tok = 128 / a.own.G;
+  a.max_tiles = w.max_tiles;
+  a.n_groups = n_groups;
+  a.cu_group = cu_group;
+  a.shared_pages = shared_pages;
+  a.skip = reinterpret_cast<int32_t*>(base + w.skip);
+  a.own.geo.skip = a.skip;
+  a.plan = reinterpret_cast<SharedPlan*>(base + w.plan);
+  a.states = reinterpret_cast<float*>(base + w.states);
+  a.pool_rows = int(pool_rows(L));
+  // the largest power of two that divides the page size, of 8 rows (the swizzle's period) to a block
+  const int two = L->page_size & -L->page_size;
+  a.box = two >= 8 ? std::min(two, 128) : 0;
+  bool ok = encode_heads(&a.tmq, q, D, L->n_q_heads, L->batch, int64_t(L->n_q_heads) * D, a.own.G, a.tok);
+  if (a.box) ok = ok && encode_pools(&a.tmk, &a.tmv, L, k, v, a.box, 1);
+  if (!ok) return fail(SFI_ERR_CUDA, "encoding the tensor maps of q, k and v failed");
+  const cudaError_t e = launch_shared_attn(a, D, use_tma, grid, st);
+  if (e != cudaSuccess) return cuda_fail(e, "shared attention launch");
+  return SFI_OK;
 }
 
 sfi_status sfi_paged_append(const sfi_paged_layout* L, int32_t total_new, const void* k_new, const void* v_new,

@@ -16,6 +16,9 @@ struct PagedGeo {
   int32_t* len;
   uint32_t* status;
   uint32_t* refused;  // a bit for each sequence that an extension left as it was
+  // attention only, or null: pages at the start of each sequence that another kernel
+  // attends to; such a sequence's pieces are left for that kernel's join
+  const int32_t* skip;
 };
 
 struct PagedAttnArgs {

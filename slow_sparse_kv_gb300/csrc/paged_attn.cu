@@ -101,9 +101,9 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, l
     if (mine) {
       u = unit_at(x, sh.ln, geo.B, H_kv);
       t = int(x - u.begin);
-      n = min(geo.len[u.b], cap);
+      n = min(geo.len[u.b], cap) - skipped(geo, u.b) * P;
     }
-    const int32_t* const row = geo.table + int64_t(u.b) * geo.max_pages;
+    const int32_t* const row = geo.table + int64_t(u.b) * geo.max_pages + skipped(geo, u.b);
     if (LD != kCpAsync) {
       bool bad = false;
 #pragma unroll
@@ -136,7 +136,8 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, l
     int pg = 0, in = -1;
     auto row_of = [&](int i) {
       const int ut = __shfl_sync(kFull, t, i), ug = __shfl_sync(kFull, u.g, i), un = __shfl_sync(kFull, n, i);
-      const int32_t* const urow = geo.table + int64_t(__shfl_sync(kFull, u.b, i)) * geo.max_pages;
+      const int ub = __shfl_sync(kFull, u.b, i);
+      const int32_t* const urow = geo.table + int64_t(ub) * geo.max_pages + skipped(geo, ub);
       const int pos = ut * TR + lane % TR;
       pg = pos < un ? urow[pos / P] : 0;
       in = pos < un ? ug * P + pos % P : -1;
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
           qf[h][0] = w.x, qf[h][1] = w.y;
         }
       }
-      return min(geo.len[u.b], cap);
+      return min(geo.len[u.b], cap) - skipped(geo, u.b) * geo.P;
     };
     if (from < to) {
       long long x = first_of(from, warp, kWarps);  // this warp's next tile
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
         // so that a round is one wait for all.  (With factors by 32 threads between two
         // more of them, and the next queries loaded behind it: 106 us against 84 for
         // 256 x 300 positions, 93 against 88 for 131072.)
-        const bool alone = u.begin >= from && u.end <= to;  // the unit's only piece
+        const bool alone = u.begin >= from && u.end <= to && skipped(geo, b) == 0;  // the unit's only piece
         float* const slot = a.partials + (share + b * H_kv + g) * int64_t(G) * (D + 2);
 #pragma unroll
         for (int h0 = 0; h0 < C::HEADS; h0 += C::MH) {
@@ -582,7 +583,7 @@ cudaError_t launch_t(const PagedAttnArgs& a, int grid, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const cudaError_t e2 = launch_pdl(kernel, dim3(grid), kAllThreads, C::SMEM, st, a);
   if (e2 != cudaSuccess) return e2;
-  return launch_join<C::TR, D>(a, grid, st);
+  return a.geo.skip ? cudaSuccess : launch_join<C::TR, D>(a, grid, st);  // (with `skip` the caller joins)
 }
 
 template <int D, int NT>

@@ -8,6 +8,7 @@
 #include "common.cuh"
 #include "paged.h"
 #include "pdl.cuh"
+#include "tc5_attn.cuh"
 
 namespace sfi {
 namespace {
@@ -34,10 +35,10 @@ struct Cut {
   long long total, per, wide;  // tiles of a share; those before `wide` belong to shares with one more
   int shares, extra;           // extra: shares with one tile more
 
-  __device__ __forceinline__ Cut(long long total_, int grid) {
+  // few tiles: fewer shares, of at least `least` (a tile for each warp)
+  __device__ __forceinline__ Cut(long long total_, int grid, int least = kWarps) {
     total = total_;
-    // few tiles: fewer shares, of a tile for each warp at least
-    const long long most = (total + kWarps - 1) / kWarps;
+    const long long most = (total + least - 1) / least;
     shares = most < grid ? int(most) : grid;
     per = shares > 0 ? total / shares : 0;
     extra = shares > 0 ? int(total - per * shares) : 0;
@@ -51,21 +52,6 @@ struct Cut {
     return int(x < wide ? x / (per + 1) : extra + (x - wide) / per);
   }
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
@@ -114,6 +100,9 @@ __device__ __forceinline__ Unit unit_at(long long x, const Line& ln, int B, int 
   return u;
 }
 
+// Pages at the start of sequence b that are left out.
+__device__ __forceinline__ int skipped(const PagedGeo& geo, int b) { return geo.skip ? geo.skip[b] : 0; }
+
 // Fills `ln` (the first kThreads threads of a CTA); `flag` reports lengths out of
 // range.
 template <int TR>
@@ -126,6 +115,7 @@ __device__ __forceinline__ void scan_lengths(const PagedGeo& geo, Line& ln, bool
       if (flag) set_status(geo.status, SFI_DEV_LEN_OVER_CAP);
       n = n < 0 ? 0 : cap;
     }
+    if (b < B) n -= skipped(geo, b) * geo.P;
     return (n + TR - 1) / TR;
   };
   auto scan = [&](long long x) {
@@ -206,30 +196,27 @@ struct Joined {
   }
 };
 
+// By CTA (bx, by) of nx x ny, behind a launch of `grid` CTAs.
 template <int TR, int D>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int grid) {
+__device__ __forceinline__ void join_units(const PagedAttnArgs& a, const Line& ln, int grid, int bx, int nx, int by, int ny) {
   constexpr int AHEAD = 8;  // pieces read at a time
-  __shared__ Line ln;
   __shared__ float part[3][kWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PagedGeo& geo = a.geo;
   const int B = geo.B, H_kv = geo.H_kv, G = a.G;
   const float c = a.scale_log2;
-  pdl_launch();
-  pdl_wait();
-  scan_lengths<TR>(geo, ln, false);
   const Cut cut(ln.pre[B] * H_kv, grid);
   const int64_t step = int64_t(G) * (D + 2);
-  for (int unit = blockIdx.x; unit < B * H_kv; unit += gridDim.x) {
+  for (int unit = bx; unit < B * H_kv; unit += nx) {
     const int b = unit / H_kv, g = unit - b * H_kv;
     const long long nt = ln.pre[b + 1] - ln.pre[b], begin = ln.pre[b] * H_kv + g * nt;
-    if (nt == 0) continue;
+    if (nt == 0 || skipped(geo, b) > 0) continue;
     const int first = cut.holder(begin), pieces = cut.holder(begin + nt - 1) - first + 1;
     if (pieces == 1) continue;
     const int64_t qrow = (int64_t(b) * a.H_q + int64_t(g) * G) * D;
     const float* const p = a.partials + (first + unit) * step;
     if (pieces <= 2 * AHEAD) {
-      for (int i = blockIdx.y * kThreads + tid; i < G * D; i += gridDim.y * kThreads) {
+      for (int i = by * kThreads + tid; i < G * D; i += ny * kThreads) {
         const int h = i / D, d = i - h * D;
         Joined j;
         for (int w = 0; w < pieces; w += AHEAD) j.add<AHEAD>(p + h * (D + 2) + w * step, step, pieces - w, d, D, c);
@@ -237,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
       }
       continue;
     }
-    for (int y = blockIdx.y; y < G * (D / 32); y += gridDim.y) {
+    for (int y = by; y < G * (D / 32); y += ny) {
       const int h = y / (D / 32), d = y % (D / 32) * 32 + lane;
       // warp w takes the w-th eighth of the pieces
       const int share = (pieces + kWarps - 1) / kWarps, w1 = min(pieces, (warp + 1) * share);
@@ -256,6 +243,15 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
       __syncthreads();
     }
   }
+}
+
+template <int TR, int D>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int grid) {
+  __shared__ Line ln;
+  pdl_launch();
+  pdl_wait();
+  scan_lengths<TR>(a.geo, ln, false);
+  join_units<TR, D>(a, ln, grid, blockIdx.x, gridDim.x, blockIdx.y, gridDim.y);
 }
 
 // The joining kernel behind a launch of `grid` CTAs: a CTA for each unit, and for each 32

@@ -43,6 +43,7 @@
 #include "pdl.cuh"
 #include "prefill.h"
 #include "tc5.cuh"
+#include "tc5_attn.cuh"
 
 namespace sfi {
 namespace {
@@ -90,49 +91,11 @@ struct Shared {
   volatile int abort;
 };
 
-// Bounded wait; false (and the CTA's abort flag and the status bit set) after
-// `limit` clocks, false at once when another thread gave up.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Shared& sh, uint32_t* status,
-                                     long long limit) {
-  if (mbar_test_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
-    if (sh.abort) return false;
-    if (clock64() - t0 > limit) {
-      sh.abort = 1;
-      set_status(status, SFI_DEV_WAIT_TIMEOUT);
-      return false;
-    }
-    if (mbar_try_wait(bar, parity)) return true;
-  }
-}
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-
 __device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                    reinterpret_cast<uint64_t>(tmap)),
                "r"(x), "r"(y), "r"(z), "r"(src)
                : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float max3(float x, float y, float z) {
-  float m;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
-  return m;
 }
 
 // Part H of a block's probabilities: p = 2^(c s - c m) summed in fp32 (four
@@ -146,22 +109,6 @@ __device__ __forceinline__ void exp_part(uint32_t (&s)[kKeys], uint64_t cc, uint
     sum[x & 3] = add2(sum[x & 3], pair(p0, p1));
     s[x] = pack_bf16x2(p0, p1);
   }
-}
-
-// Store a part of P and tell the MMA lane.
-template <typename Store>
-__device__ __forceinline__ void hand_over(uint32_t bar, Store store) {
-  store();
-  tc5::wait_st();
-  tc5::fence_before();
-  mbar_arrive(bar);
-}
-
-// Keeps uses of registers that a tcgen05.ld fills behind its wait.
-template <int N>
-__device__ __forceinline__ void pin(uint32_t (&r)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // Which tile has which rank (one warp).  Levels stand for the keys that a tile

@@ -113,3 +113,27 @@ def test_rotation_restatement_by_hand():
     assert np.allclose(y[:, 0, 0], [-3, 0], atol=1e-12) and np.allclose(y[:, 0, 1], [0, -3], atol=1e-12)
     y, _ = H.norm_rope(np.full((1, 1, 64), 2.0), np.full(64, 0.5), [0], [], False, 0.0)
     assert np.allclose(y, 0.5)
+
+
+def shared(sfi, L, n=1, cu=FAKE, pages=FAKE, q=FAKE, k=FAKE, out=FAKE, ws=FAKE, ws_bytes=1 << 40):
+    return sfi.lib.sfi_paged_attn_shared(ref(L), n, cu, pages, q, k, FAKE, out, None, ws, ws_bytes, None)
+
+
+def test_shared_refusals(sfi):
+    bad, unsup, cap = sfi.SFI_ERR_INVALID_ARG, sfi.SFI_ERR_UNSUPPORTED, sfi.SFI_ERR_CAPACITY
+    for kw, code in [(dict(batch=0), bad), (dict(head_dim=80), unsup), (dict(n_q_heads=34), unsup), (dict(dtype=0), unsup),
+                     (dict(dtype=4), unsup), (dict(dtype=5), unsup), (dict(dtype=2), unsup), (dict(page_size=0), bad), (dict(len=None), bad)]:
+        L = paged(sfi, **kw)
+        assert shared(sfi, L) == code, kw
+        assert sfi.lib.sfi_paged_shared_workspace_size(ref(L), 1) == 0, kw
+    L = paged(sfi)
+    size = sfi.lib.sfi_paged_shared_workspace_size
+    assert shared(sfi, None) == bad and shared(sfi, L, n=-1) == bad and shared(sfi, L, n=1025) == cap
+    assert size(ref(L), -1) == 0 and size(ref(L), 1025) == 0
+    for kw in (dict(cu=None), dict(pages=None), dict(q=None), dict(k=None), dict(out=None), dict(q=FAKE + 8), dict(k=FAKE + 2), dict(out=FAKE + 4)):
+        assert shared(sfi, L, **kw) == bad, kw
+    need = size(ref(L), 1)
+    assert need > size(ref(L), 0) >= sfi.lib.sfi_paged_workspace_size(ref(L)) > 0
+    assert size(ref(L), 1024) >= size(ref(L), 2) >= need
+    for kw in (dict(ws=None), dict(ws=FAKE + 8), dict(ws_bytes=need - 1)):
+        assert shared(sfi, L, **kw) == sfi.SFI_ERR_WORKSPACE, kw
