@@ -236,7 +236,7 @@ bool encode_pools(CUtensorMap* mk, CUtensorMap* mv, const sfi_paged_layout* L, c
 
 // What sfi_paged_attn_shared keeps behind the paged calls' workspace.
 struct SharedWs {
-  size_t skip, plan, states, total;
+  size_t skip, plan, pieces, states, total;
   int max_tiles;
 };
 
@@ -248,9 +248,12 @@ SharedWs plan_shared(const sfi_paged_layout* L, int n_groups) {
   if (n_groups == 0) w.max_tiles = 0;
   w.skip = plan_paged(L).total;
   w.plan = w.skip + align256(size_t(L->batch) * 4);
-  w.states = w.plan + align256(sizeof(SharedPlan));
+  w.pieces = w.plan + align256(sizeof(SharedPlan));
+  const size_t slots = size_t(L->batch) * L->n_kv_heads + kPagedMaxGrid * kPagedWarps;
+  w.states = w.pieces + align256(slots * (L->n_q_heads / L->n_kv_heads) * (L->head_dim + 2) * 4);
   w.total = w.states;
-  if (w.max_tiles > 0)
+  if (w.max_tiles == 0) w.total = w.skip;
+  else
     w.total += (size_t(w.max_tiles) * L->n_kv_heads + kPagedMaxGrid) * kTileRows * (L->head_dim + 2) * 4;
   return w;
 }
@@ -484,11 +487,12 @@ sfi_status sfi_paged_attn_shared(const sfi_paged_layout* L, int32_t n_groups, co
   a.skip = reinterpret_cast<int32_t*>(base + w.skip);
   a.own.geo.skip = a.skip;
   a.plan = reinterpret_cast<SharedPlan*>(base + w.plan);
+  a.own.partials = reinterpret_cast<float*>(base + w.pieces);
   a.states = reinterpret_cast<float*>(base + w.states);
   a.pool_rows = int(pool_rows(L));
-  // the largest power of two that divides the page size, of 8 rows (the swizzle's period) to a block
+  // the largest power of two that divides the page size, of 8 rows (the swizzle's period) to a block's 64
   const int two = L->page_size & -L->page_size;
-  a.box = two >= 8 ? std::min(two, 128) : 0;
+  a.box = two >= 8 ? std::min(two, 64) : 0;
   bool ok = encode_heads(&a.tmq, q, D, L->n_q_heads, L->batch, int64_t(L->n_q_heads) * D, a.own.G, a.tok);
   if (a.box) ok = ok && encode_pools(&a.tmk, &a.tmv, L, k, v, a.box, 1);
   if (!ok) return fail(SFI_ERR_CUDA, "encoding the tensor maps of q, k and v failed");

@@ -16,9 +16,7 @@ struct PagedGeo {
   int32_t* len;
   uint32_t* status;
   uint32_t* refused;  // a bit for each sequence that an extension left as it was
-  // attention only, or null: pages at the start of each sequence that another kernel
-  // attends to; such a sequence's pieces are left for that kernel's join
-  const int32_t* skip;
+  const int32_t* skip;  // pages at the start of each sequence that are left out; null: none
 };
 
 struct PagedAttnArgs {
@@ -48,6 +46,11 @@ cudaError_t launch_paged_attn_q8(const PagedAttnArgs& a, int D, bool e4m3, bool 
 // use_tma: the maps are set
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int D, bool f32, bool use_tma, int grid,
                               cudaStream_t st);
+
+// The same for bf16 pools without the join, each warp with a share of its own: the pieces of all
+// units that hold anything lie in partials, [warps of the grid + B * H_kv][G][d + 2].
+constexpr int kPagedWarps = 8;  // of a CTA, that attend
+cudaError_t launch_paged_pieces(const PagedAttnArgs& a, int D, bool use_tma, int grid, cudaStream_t st);
 
 struct AppendArgs {
   PagedGeo geo;

@@ -79,9 +79,23 @@ struct Shared {
   uint64_t merge_free;                                    // the warps' states have been read
 };
 
-// The copying warps: warp `p` takes the tiles of the attending warps p and p + 4.
-template <typename T, int D, int NT, Load LD>
-__device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, long long from, long long to,
+// A run of tiles.
+struct Run {
+  long long from, to;
+};
+
+// The run of attending warp w, where each warp has a share of its own (neighbouring shares
+// lie in neighbouring CTAs, so that a few tiles are spread over the SMs).
+__device__ __forceinline__ Run warp_run(const Cut& cut, int w) {
+  const int share = w * gridDim.x + blockIdx.x;
+  return share < cut.shares ? Run{cut.start(share), cut.start(share + 1)} : Run{0, 0};
+}
+
+// The copying warps: warp `p` takes the tiles of the attending warps p and p + 4: every
+// fourth one of the CTA's share [from, to), or with SOLO those of the two warps' own shares
+// in turn.
+template <typename T, int D, int NT, Load LD, bool SOLO>
+__device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, const Cut& cut, long long from, long long to,
                                            uint32_t ring, int p) {
   using C = Cfg<T, D, NT>;
   constexpr int TR = C::TR;
@@ -91,10 +105,16 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, l
   const T* const vp = static_cast<const T*>(a.v);
   bool ok = true;
   const long long first[2] = {first_of(from, p, kWarps), first_of(from, p + kProducers, kWarps)};
-  for (long long x0 = first_of(from, p, kProducers); x0 < to && ok; x0 += kProducers * 32) {
+  Run runs[2] = {{0, 0}, {0, 0}};
+  if (SOLO) {
+    runs[0] = warp_run(cut, p), runs[1] = warp_run(cut, p + kProducers);
+    to = 2 * max(runs[0].to - runs[0].from, runs[1].to - runs[1].from);
+  }
+  constexpr int STEP = SOLO ? 1 : kProducers;
+  for (long long x0 = SOLO ? 0 : first_of(from, p, kProducers); x0 < to && ok; x0 += STEP * 32) {
     // 32 tiles: each lane finds the place and the page of its own
-    const long long x = x0 + kProducers * lane;
-    const bool mine = x < to;
+    const long long x = SOLO ? runs[lane & 1].from + ((x0 + lane) >> 1) : x0 + kProducers * lane;
+    const bool mine = SOLO ? x < runs[lane & 1].to : x < to;
     Unit u{0, 0, 0, 0};
     int t = 0, n = 0;
     int page[LD == kBulk ? TR : 1];
@@ -129,7 +149,7 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, l
     }
     const int64_t at0 = page[0] * geo.page_stride + (int64_t(u.g) * P + in0) * D;
     const int row0 = LD == kTma ? int(page[0] * (geo.page_stride / D) + u.g * P + t * TR % P) : 0;
-    const int count = int(min(32LL, (to - x0 + kProducers - 1) / kProducers));
+    const int count = int(min(32LL, (to - x0 + STEP - 1) / STEP));
     // kCpAsync: the i-th tile's row of this lane (lane % TR): its page, and where in it,
     // -1 for no row.  A tile's pages are read while the one before it is copied (waited
     // for before each tile: 136 us against 129 for 8 x ~24000 positions in pages of 20).
@@ -144,9 +164,13 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, l
     };
     if (LD == kCpAsync) row_of(0);
     for (int i = 0; i < count && ok; ++i) {
-      const long long xi = x0 + kProducers * i;
-      const int w = int(xi >> 2) & 1;  // which of the two warps
-      const uint32_t y = uint32_t(xi - first[w]) / kWarps;
+      const long long xi = x0 + STEP * i;
+      const int w = SOLO ? int(xi) & 1 : int(xi >> 2) & 1;  // which of the two warps
+      const uint32_t y = SOLO ? uint32_t(xi >> 1) : uint32_t(xi - first[w]) / kWarps;
+      if (SOLO && !__shfl_sync(kFull, mine, i)) {
+        if (LD == kCpAsync && i + 1 < count) row_of(i + 1);
+        continue;
+      }
       const int slot = (p + w * kProducers) * C::STAGES + int(y % C::STAGES);
       const uint32_t use = y / C::STAGES;
       if (use > 0) ok = warp_ctrl_wait(smem_addr(&sh.empty[slot]), (use - 1) & 1, &sh.abort, geo.status);
@@ -207,7 +231,7 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, l
   if (LD == kCpAsync) asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <typename T, int D, int NT, Load LD>
+template <typename T, int D, int NT, Load LD, bool SOLO>
 __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnArgs a) {
   using C = Cfg<T, D, NT>;
   constexpr bool F32 = C::F32;
@@ -246,14 +270,14 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
     if (a.lse && tid < G) a.lse[row + tid] = -INFINITY;
   }
   // this CTA's share of the line (a CTA beyond the shares has none)
-  const Cut cut(total, gridDim.x);
+  const Cut cut = SOLO ? Cut(total, gridDim.x * kWarps, 1) : Cut(total, gridDim.x);
   const int share = blockIdx.x;
   const long long from = share < cut.shares ? cut.start(share) : total;
   const long long to = share < cut.shares ? cut.start(share + 1) : total;
 
   if (warp >= kWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
-    copy_tiles<T, D, NT, LD>(a, sh, from, to, ring, warp - kWarps);
+    copy_tiles<T, D, NT, LD, SOLO>(a, sh, cut, from, to, ring, warp - kWarps);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAttendRegs));
     const float c = a.scale_log2;
@@ -294,12 +318,14 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
       }
       return min(geo.len[u.b], cap) - skipped(geo, u.b) * geo.P;
     };
-    if (from < to) {
-      long long x = first_of(from, warp, kWarps);  // this warp's next tile
-      Unit u = unit_at(from, ln, B, H_kv);
+    const Run run = SOLO ? warp_run(cut, warp) : Run{from, to};
+    constexpr int STEP = SOLO ? 1 : kWarps;
+    if (run.from < run.to) {
+      long long x = SOLO ? run.from : first_of(run.from, warp, kWarps);  // this warp's next tile
+      Unit u = unit_at(run.from, ln, B, H_kv);
       int n = load_unit(u);
       while (true) {
-        const long long pe = min(u.end, to);
+        const long long pe = min(u.end, run.to);
         const int b = u.b, g = u.g;
         const int64_t qrow = (int64_t(b) * a.H_q + int64_t(g) * G) * D;
 
@@ -325,7 +351,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
           for (int h = 0; h < NS * 4; ++h) of[h][0] = of[h][1] = 0;
         }
 
-        for (; x < pe; x += kWarps) {
+        for (; x < pe; x += STEP) {
           const int slot = warp * C::STAGES + int(y % C::STAGES);
           const uint32_t use = y / C::STAGES;
           ++y;
@@ -487,16 +513,40 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
         // the next unit of the share; its queries are on their way during the merge
         Unit next = u;
         do unit_next(next, ln, B, H_kv);
-        while (next.begin < to && next.end == next.begin);
-        const bool more = next.begin < to;
+        while (next.begin < run.to && next.end == next.begin);
+        const bool more = next.begin < run.to;
         if (more) n = load_unit(next);
 
+        if constexpr (SOLO && !F32) {
+          // the warp's state is a piece by itself
+          float* const slot = a.partials + (warp * int(gridDim.x) + share + b * H_kv + g) * int64_t(G) * (D + 2);
+#pragma unroll
+          for (int h = 0; h < NT; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float t = l[h][e];
+#pragma unroll
+              for (int w = 4; w < 32; w <<= 1) t += __shfl_xor_sync(kFull, t, w);
+              const int head = h * 8 + 2 * (lane & 3) + e;
+              if (head >= G) continue;
+              float* const row = slot + head * (D + 2);
+              if (lane < 4) row[D] = m[h][e], row[D + 1] = t;
+#pragma unroll
+              for (int kk = 0; kk < KS; ++kk) {
+                row[kk * 16 + (lane >> 2)] = o[kk][h][e];
+                row[kk * 16 + 8 + (lane >> 2)] = o[kk][h][2 + e];
+              }
+            }
+          if (!more) break;
+          u = next;
+          continue;
+        }
         // ---- the piece: the warps' states merged, MH heads at a time.  A warp writes
         // when all have read the round before, which they mostly have long since,
         // so that a round is one wait for all.  (With factors by 32 threads between two
         // more of them, and the next queries loaded behind it: 106 us against 84 for
         // 256 x 300 positions, 93 against 88 for 131072.)
-        const bool alone = u.begin >= from && u.end <= to && skipped(geo, b) == 0;  // the unit's only piece
+        const bool alone = u.begin >= from && u.end <= to;  // the unit's only piece
         float* const slot = a.partials + (share + b * H_kv + g) * int64_t(G) * (D + 2);
 #pragma unroll
         for (int h0 = 0; h0 < C::HEADS; h0 += C::MH) {
@@ -574,22 +624,27 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
   }
 }
 
-template <typename T, int D, int NT, Load LD>
+template <typename T, int D, int NT, Load LD, bool SOLO>
 cudaError_t launch_t(const PagedAttnArgs& a, int grid, cudaStream_t st) {
   using C = Cfg<T, D, NT>;
-  auto* const kernel = paged_attn_kernel<T, D, NT, LD>;
+  auto* const kernel = paged_attn_kernel<T, D, NT, LD, SOLO>;
   static std::atomic<uint64_t> allowed{0};  // the devices on which the kernel may use its shared memory
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::SMEM, allowed);
   if (e != cudaSuccess) return e;
   const cudaError_t e2 = launch_pdl(kernel, dim3(grid), kAllThreads, C::SMEM, st, a);
-  if (e2 != cudaSuccess) return e2;
-  return a.geo.skip ? cudaSuccess : launch_join<C::TR, D>(a, grid, st);  // (with `skip` the caller joins)
+  if (e2 != cudaSuccess || SOLO) return e2;
+  return launch_join<C::TR, D>(a, grid, st);
 }
 
 template <int D, int NT>
 cudaError_t launch_n(const PagedAttnArgs& a, bool f32, bool use_tma, int grid, cudaStream_t st) {
-  if (f32) return launch_t<float, D, NT, kBulk>(a, grid, st);
-  return use_tma ? launch_t<bf16_t, D, NT, kTma>(a, grid, st) : launch_t<bf16_t, D, NT, kCpAsync>(a, grid, st);
+  if (f32) return launch_t<float, D, NT, kBulk, false>(a, grid, st);
+  return use_tma ? launch_t<bf16_t, D, NT, kTma, false>(a, grid, st) : launch_t<bf16_t, D, NT, kCpAsync, false>(a, grid, st);
+}
+
+template <int D, int NT>
+cudaError_t launch_solo(const PagedAttnArgs& a, bool use_tma, int grid, cudaStream_t st) {
+  return use_tma ? launch_t<bf16_t, D, NT, kTma, true>(a, grid, st) : launch_t<bf16_t, D, NT, kCpAsync, true>(a, grid, st);
 }
 
 }  // namespace
@@ -597,6 +652,11 @@ cudaError_t launch_n(const PagedAttnArgs& a, bool f32, bool use_tma, int grid, c
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int D, bool f32, bool use_tma, int grid, cudaStream_t st) {
   if (D == 64) return a.G <= 8 ? launch_n<64, 1>(a, f32, use_tma, grid, st) : launch_n<64, 2>(a, f32, use_tma, grid, st);
   return a.G <= 8 ? launch_n<128, 1>(a, f32, use_tma, grid, st) : launch_n<128, 2>(a, f32, use_tma, grid, st);
+}
+
+cudaError_t launch_paged_pieces(const PagedAttnArgs& a, int D, bool use_tma, int grid, cudaStream_t st) {
+  if (D == 64) return a.G <= 8 ? launch_solo<64, 1>(a, use_tma, grid, st) : launch_solo<64, 2>(a, use_tma, grid, st);
+  return a.G <= 8 ? launch_solo<128, 1>(a, use_tma, grid, st) : launch_solo<128, 2>(a, use_tma, grid, st);
 }
 
 }  // namespace sfi

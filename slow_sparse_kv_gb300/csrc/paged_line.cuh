@@ -13,7 +13,7 @@
 namespace sfi {
 namespace {
 
-constexpr int kWarps = 8;                    // that attend
+constexpr int kWarps = kPagedWarps;                    // that attend
 constexpr int kThreads = kWarps * 32;        // of them
 constexpr int kProducers = 4;                // warps that copy
 constexpr int kAllThreads = kThreads + kProducers * 32;
@@ -196,23 +196,23 @@ struct Joined {
   }
 };
 
-// By CTA (bx, by) of nx x ny, behind a launch of `grid` CTAs.
+// By CTA (bx, by) of nx x ny; `whole`: single pieces too, and no units of which something is left out.
 template <int TR, int D>
-__device__ __forceinline__ void join_units(const PagedAttnArgs& a, const Line& ln, int grid, int bx, int nx, int by, int ny) {
+__device__ __forceinline__ void join_units(const PagedAttnArgs& a, const Line& ln, const Cut& cut, bool whole, int bx, int nx,
+                                           int by, int ny) {
   constexpr int AHEAD = 8;  // pieces read at a time
   __shared__ float part[3][kWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PagedGeo& geo = a.geo;
   const int B = geo.B, H_kv = geo.H_kv, G = a.G;
   const float c = a.scale_log2;
-  const Cut cut(ln.pre[B] * H_kv, grid);
   const int64_t step = int64_t(G) * (D + 2);
   for (int unit = bx; unit < B * H_kv; unit += nx) {
     const int b = unit / H_kv, g = unit - b * H_kv;
     const long long nt = ln.pre[b + 1] - ln.pre[b], begin = ln.pre[b] * H_kv + g * nt;
     if (nt == 0 || skipped(geo, b) > 0) continue;
     const int first = cut.holder(begin), pieces = cut.holder(begin + nt - 1) - first + 1;
-    if (pieces == 1) continue;
+    if (pieces == 1 && !whole) continue;
     const int64_t qrow = (int64_t(b) * a.H_q + int64_t(g) * G) * D;
     const float* const p = a.partials + (first + unit) * step;
     if (pieces <= 2 * AHEAD) {
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
   pdl_launch();
   pdl_wait();
   scan_lengths<TR>(a.geo, ln, false);
-  join_units<TR, D>(a, ln, grid, blockIdx.x, gridDim.x, blockIdx.y, gridDim.y);
+  join_units<TR, D>(a, ln, Cut(ln.pre[a.geo.B] * a.geo.H_kv, grid), false, blockIdx.x, gridDim.x, blockIdx.y, gridDim.y);
 }
 
 // The joining kernel behind a launch of `grid` CTAs: a CTA for each unit, and for each 32

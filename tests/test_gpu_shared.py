@@ -139,9 +139,21 @@ def test_long_prefixes_are_cut_and_joined(sfi, hq, hkv, d, page, groups, hi):
     b.check(out, lse, only=sorted({0, 1, b.cu[1] - 1, b.cu[-2], n // 2, n - 1}))
 
 
-def test_many_groups(sfi):
+@pytest.mark.parametrize("page", [16, 12, 20])
+def test_shares_that_hold_several_pieces(sfi, page):
+    """More units than SMs, of several blocks each, in one half and in two: a CTA goes from one to the next."""
+    b = Batch(32, 8, 128, page, [(m, 1 + (7 * m + i) % 19) for i, m in enumerate([2, 9, 40, 3, 33, 64, 5, 2, 70, 8] * 2)],
+              [(i * 5) % 23 for i in range(472)])
+    out, lse = b.run(sfi)
+    again, lse2 = b.run(sfi)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    b.check(out, lse, only=list(range(0, 472, 29)) + [471])
+
+
+@pytest.mark.parametrize("page", [16, 12])
+def test_many_groups(sfi, page):
     """As many groups as a batch may have, each of two sequences: more tiles than SMs."""
-    b = Batch(2, 2, 64, 16, [(2, 1 + i % 3) for i in range(512)], [1 + i % 5 for i in range(1024)])
+    b = Batch(2, 2, 64, page, [(2, 1 + i % 3) for i in range(512)], [1 + i % 5 for i in range(1024)])
     b.check(*b.run(sfi))
 
 
@@ -176,14 +188,14 @@ def test_query_that_is_not_finite_stays_alone(sfi):
 def test_wrong_groups_share_nothing(sfi):
     """Flagged, and every sequence is attended to by its own row of the table."""
     b = Batch(8, 2, 128, 16, [(3, 4), (2, 3)], [5, 0, 40, 1, 9])
-    plain, pl = b.run(sfi, plain=True)
+    alone, al = b.run(sfi, shared=[0, 0])
+    b.check(alone, al)
     for cu in ([0, 4, 3], [-1, 3, 5], [0, 3, 6], [3, 0, 5], [0, 3, 1 << 30], [0, -(1 << 31), 5]):
         out, lse = b.run(sfi, status=sfi.SFI_DEV_LEN_OVER_CAP, cu=cu)
-        assert torch.equal(out, plain) and torch.equal(lse, pl), cu
+        assert torch.equal(out, alone) and torch.equal(lse, al), cu
     # the second group only
     for shared in ([4, 4], [4, -1], [4, 1000], [4, 1 << 30]):
         out, lse = b.run(sfi, status=sfi.SFI_DEV_LEN_OVER_CAP, shared=shared)
-        assert torch.equal(out[3:], plain[3:]) and torch.equal(lse[3:], pl[3:]), shared
         b.check(out, lse)
     for n in (-5, 1 << 20):
         b.len[4] = n
