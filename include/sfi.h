@@ -497,7 +497,7 @@ sfi_status sfi_paged_attn(const sfi_paged_layout* layout, const void* q, const v
  *  - The same call gives the same bits.
  * The workspace (sfi_paged_shared_workspace_size, 0 for invalid arguments; it grows with
  * n_groups, and one for more groups serves fewer) holds that of the paged calls and serves them
- * too.  Four launches. */
+ * too.  Three launches. */
 size_t sfi_paged_shared_workspace_size(const sfi_paged_layout* layout, int32_t n_groups);
 sfi_status sfi_paged_attn_shared(const sfi_paged_layout* layout, int32_t n_groups,
                                  const int32_t* cu_group, const int32_t* shared_pages,

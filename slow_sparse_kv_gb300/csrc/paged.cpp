@@ -490,9 +490,8 @@ sfi_status sfi_paged_attn_shared(const sfi_paged_layout* L, int32_t n_groups, co
   a.own.partials = reinterpret_cast<float*>(base + w.pieces);
   a.states = reinterpret_cast<float*>(base + w.states);
   a.pool_rows = int(pool_rows(L));
-  // the largest power of two that divides the page size, of 8 rows (the swizzle's period) to a block's 64
-  const int two = L->page_size & -L->page_size;
-  a.box = two >= 8 ? std::min(two, 64) : 0;
+  // boxes that divide the page size and a block's 48 keys, of 8 rows (the swizzle's period) at least
+  a.box = L->page_size % 48 == 0 ? 48 : L->page_size % 24 == 0 ? 24 : L->page_size % 16 == 0 ? 16 : L->page_size % 8 == 0 ? 8 : 0;
   bool ok = encode_heads(&a.tmq, q, D, L->n_q_heads, L->batch, int64_t(L->n_q_heads) * D, a.own.G, a.tok);
   if (a.box) ok = ok && encode_pools(&a.tmk, &a.tmv, L, k, v, a.box, 1);
   if (!ok) return fail(SFI_ERR_CUDA, "encoding the tensor maps of q, k and v failed");

@@ -17,8 +17,8 @@
 // Bytes: 4 d n0 a group and KV head; flops 4 d (6 d with the second term) for each row and key.
 // From 64 rows on about the tensor cores bound it, below HBM does.
 //
-// Four launches: the plan (which tiles, from the device's group offsets and lengths), the
-// shared part, the sequences' own part, and one that joins the states of both.
+// Three launches: the shared part, the sequences' own part, and one that joins the states of
+// both.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -36,12 +36,15 @@ namespace {
 
 constexpr int kSharedThreads = 384;  // 2 softmax warpgroups; two loading warps, an MMA warp, one that idles
 constexpr int kRows = 128;           // query rows of a half tile
-constexpr int kKeys = 64;            // keys of a block
-constexpr int kParts = 2;            // P of a block is handed over in halves, of 32 keys
+constexpr int kKeys = 48;            // keys of a block
+// Tensor memory: three regions of a block's scores and, over and behind them, its P, which the
+// steps take in turn, so that scores are ready when a half comes to them; and both halves'
+// sums.  (Blocks of 64 keys leave room for two regions only, and each half then waits for its own
+// products before its next scores.)
+constexpr int kRegions = 3, kRegion = 80, kSums = 256;
 constexpr int kTerms = 3;            // bf16 terms of P
 constexpr int kChain = 4;            // blocks of a half whose products with V are added in tensor memory
 constexpr float kGrow = 8.0f;        // growth of the maximum (log2) that moves m
-constexpr int kPlan = 1024;          // threads of the plan
 template <int D>
 constexpr int kJoinBlocks = kTileRows / 32 * (D / 32);  // CTAs' worth of a tile and KV head in the join
 constexpr int kOwnTile = 16;         // positions of a tile of paged_attn.cu's kernel in bf16
@@ -51,123 +54,132 @@ struct SCfg {
   static constexpr int HALVES = D / 64;
   static constexpr uint32_t QTILE = kRows * 128 * HALVES;  // bytes of 128 rows
   static constexpr uint32_t TILE = kKeys * 128 * HALVES;   // and of a block of K or V
-  static constexpr int STAGES = 8;                         // of them in flight
-  static constexpr uint32_t SMEM = 1024 + 2 * QTILE + STAGES * TILE;
+  static constexpr int STAGES = 5;                         // pairs of them in flight
+  static constexpr uint32_t SMEM = 1024 + 2 * QTILE + STAGES * 2 * TILE;
   static constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 504 - 2 * SOFTMAX_REGS;
 };
 
-// Where term e of half h of a block's P lies behind the block's scores' first column: the
-// first half's next to the second half's scores, which are read again after it.
-__host__ __device__ constexpr int term_at(int h, int e) { return h == 0 ? (e == 0 ? 0 : 48 + 16 * e) : 16 * (e + 1); }
-
-// ---- the plan
-// Inclusive sum over the CTA (kPlan threads).
-__device__ __forceinline__ long long plan_scan(long long x, long long* part) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(kFull, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) part[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    long long y = part[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long z = __shfl_up_sync(kFull, y, o);
-      if (lane >= o) y += z;
-    }
-    part[lane] = y;
-  }
-  __syncthreads();
-  return x + (warp > 0 ? part[warp - 1] : 0);
-}
-
-// Which sequences share what, as tiles.  Offsets that are out of order leave all sequences
-// by themselves; so does, for its group, a number of pages that is out of range or more
-// than a member holds: the result does not depend on what is shared, only the time does.
-__global__ void __launch_bounds__(kPlan) shared_plan_kernel(const __grid_constant__ SharedArgs a) {
-  __shared__ int cu[kMaxBatch + 1], pages[kMaxBatch];
-  __shared__ bool bad[kMaxBatch];
-  __shared__ long long part[32];
-  const PagedGeo& geo = a.own.geo;
-  const int i = threadIdx.x, n = a.n_groups, B = geo.B, cap = geo.max_pages * geo.P;
-  pdl_launch();
-  pdl_wait();
-  if (i <= n) cu[i] = a.cu_group[i];
-  if (i == 0 && n == kPlan) cu[n] = a.cu_group[n];
-  int mine = 0;
-  if (i < n) {
-    mine = a.shared_pages[i];
-    if (mine < 0 || mine > geo.max_pages) {
-      set_status(geo.status, SFI_DEV_LEN_OVER_CAP);
-      mine = 0;
-    }
-    pages[i] = mine;
-    bad[i] = false;
-  }
-  const int len = i < B ? geo.len[i] : 0;
-  __syncthreads();
-  const bool out_of_order = i < n && (cu[i] < 0 || cu[i] > cu[i + 1] || cu[i + 1] > B);
-  const bool none = __syncthreads_or(out_of_order);
-  if (none && i == 0) set_status(geo.status, SFI_DEV_LEN_OVER_CAP);
-  // the group of sequence i: the last one that begins at or before it, if it holds it
-  int group = -1;
-  if (!none && i < B) {
-    int lo = 0, hi = n;  // (as many groups begin at or before i as lie below `lo`)
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (cu[mid] <= i) lo = mid + 1;
-      else hi = mid;
-    }
-    group = lo - 1;
-    if (group >= 0 && i >= cu[group + 1]) group = -1;
-    if (group >= 0 && pages[group] > 0 && (len < 0 || len > cap || len < (long long)pages[group] * geo.P)) {
-      set_status(geo.status, SFI_DEV_LEN_OVER_CAP);
-      bad[group] = true;
-    }
-  }
-  __syncthreads();
-  const int members = !none && i < n ? cu[i + 1] - cu[i] : 0;
-  // (one sequence alone would gain nothing)
-  const int shares = members > 1 && !bad[i] ? pages[i] : 0;
-  if (i < n) pages[i] = shares;
-  __syncthreads();
-  const int skip = i < B && group >= 0 ? pages[group] : 0;
-  if (i < B) a.skip[i] = skip;
-  const bool alone = __syncthreads_or(i < B && skip == 0);
-  const int tiles = shares > 0 ? (members + 2 * a.tok - 1) / (2 * a.tok) : 0;
-  const long long blocks = (shares * (long long)geo.P + kKeys - 1) / kKeys * geo.H_kv;
-  const int first = int(plan_scan(tiles, part)) - tiles;
-  const int all = int(part[31]);
-  const long long start = plan_scan(tiles * blocks, part) - tiles * blocks;
-  for (int t = 0; t < tiles; ++t) {
-    SharedTile tile;
-    tile.b0 = cu[i] + t * 2 * a.tok;
-    tile.seqs = min(2 * a.tok, cu[i + 1] - tile.b0);
-    tile.lead = cu[i];
-    tile.n = shares * geo.P;
-    a.plan->tile[first + t] = tile;
-    a.plan->start[first + t] = start + t * blocks;
-  }
-  if (i == 0) {
-    a.plan->n_tiles = all;
-    a.plan->alone = alone;
-    a.plan->total = a.plan->start[all] = part[31];
-  }
+// Where term e of the z-th 16 keys of a block's P lies behind the block's scores' first column,
+// 8 columns each: that of the first 32 keys where their own scores were and behind them all.
+__host__ __device__ constexpr int term_at(int z, int e) {
+  return z < 2 ? (z * 3 + e < 4 ? 8 * (z * 3 + e) : 48 + 8 * (z * 3 + e - 4)) : (e < 2 ? 32 + 8 * e : 64);
 }
 
 // ---- the shared part
 struct SharedMem {
-  uint64_t q_full[2], q_empty[2], s_full[2], o_full[2], p_ready[2][kParts];
-  uint64_t kv_full[8], kv_empty[8], drained;
+  uint64_t q_full, q_empty;
+  // A stage is a pair: K of a block and V of the one before, since the scores run ahead; the first
+  // pair of a piece has no V, the last one no K.
+  uint64_t kv_full[5], kv_empty[5], drained;
+  // Scores run ahead of the softmax threads, and these ahead of the products: a barrier for each
+  // region.  None may be two phases ahead of who waits for it, nor one behind: it would look
+  // like the other.  The halves take the steps in turn, so who waits for the scores of step s
+  // has seen those of s - 2, behind which those of s - 3, the region's last ones, were complete;
+  // and a region's next scores and P come behind its last products.
+  uint64_t s_full[kRegions], p_ready[kRegions], o_full[kRegions];
   uint32_t tmem;
   volatile int abort;
+  // the plan, and what it is made of
+  long long total;
+  int n_tiles;
   long long start[kMaxTiles + 1];
   SharedTile tile[kMaxTiles];
+  int cu[kMaxBatch + 1], pages[kMaxBatch];
+  bool bad[kMaxBatch];
 };
+
+// Which sequences share what, as tiles; every CTA makes the plan for itself, and the first one
+// leaves it for the kernels behind.  Offsets that are out of order leave all sequences by themselves;
+// so does, for its group, a number of pages that is out of range or more than a member holds:
+// the result does not depend on what is shared, only the time does.  (Loops are not unrolled:
+// this runs once, and its instructions take longer to come than to run.)
+__device__ __forceinline__ void make_plan(const SharedArgs& a, SharedMem& sh, bool first) {
+  const PagedGeo& geo = a.own.geo;
+  const int tid = threadIdx.x, lane = tid & 31, n = a.n_groups, B = geo.B, cap = geo.max_pages * geo.P;
+  const int len0 = tid < B ? geo.len[tid] : 0;
+#pragma unroll 1
+  for (int i = tid; i <= n; i += kSharedThreads) {
+    sh.cu[i] = a.cu_group[i];
+    if (i == n) break;
+    const int pages = a.shared_pages[i];
+    sh.bad[i] = pages < 0 || pages > geo.max_pages;
+    sh.pages[i] = pages;
+    if (sh.bad[i] && first) set_status(geo.status, SFI_DEV_LEN_OVER_CAP);
+  }
+  __syncthreads();
+  bool wrong = false;
+#pragma unroll 1
+  for (int i = tid; i < n; i += kSharedThreads) wrong |= sh.cu[i] < 0 || sh.cu[i] > sh.cu[i + 1] || sh.cu[i + 1] > B;
+  const bool none = __syncthreads_or(wrong);
+  if (none && first && tid == 0) set_status(geo.status, SFI_DEV_LEN_OVER_CAP);
+  // the group of sequence b: the last one that begins at or before it, if it holds it
+  auto group_of = [&](int b) {
+    int lo = 0, hi = none ? 0 : n;  // (as many groups begin at or before b as lie below `lo`)
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sh.cu[mid] <= b) lo = mid + 1;
+      else hi = mid;
+    }
+    return lo > 0 && b < sh.cu[lo] ? lo - 1 : -1;
+  };
+#pragma unroll 1
+  for (int b = tid; b < B; b += kSharedThreads) {
+    const int g = group_of(b), len = b == tid ? len0 : geo.len[b];
+    if (g < 0 || sh.pages[g] <= 0) continue;
+    if (len < 0 || len > cap || len < (long long)sh.pages[g] * geo.P) {
+      if (first) set_status(geo.status, SFI_DEV_LEN_OVER_CAP);
+      sh.bad[g] = true;
+    }
+  }
+  __syncthreads();
+  // pages that group i shares (one sequence alone would gain nothing)
+  auto shares = [&](int i) { return !none && !sh.bad[i] && sh.cu[i + 1] - sh.cu[i] > 1 ? sh.pages[i] : 0; };
+  if (tid < 32) {
+    int t0 = 0;  // tiles and blocks of the groups before
+    long long x0 = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane, pages = i < n ? shares(i) : 0;
+      const int tiles = pages > 0 ? (sh.cu[i + 1] - sh.cu[i] + 2 * a.tok - 1) / (2 * a.tok) : 0;
+      const long long blocks = (long long)((pages * geo.P + kKeys - 1) / kKeys) * geo.H_kv;
+      int t = tiles;
+      long long x = tiles * blocks;
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t1 = __shfl_up_sync(kFull, t, o);
+        const long long x1 = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) t += t1, x += x1;
+      }
+      int at = t0 + t - tiles;
+      long long start = x0 + x - tiles * blocks;
+      t0 += __shfl_sync(kFull, t, 31);
+      x0 += __shfl_sync(kFull, x, 31);
+#pragma unroll 1
+      for (int y = 0; y < tiles; ++y, ++at, start += blocks) {
+        const int b0 = sh.cu[i] + y * 2 * a.tok;
+        sh.tile[at] = SharedTile{b0, min(2 * a.tok, sh.cu[i + 1] - b0), sh.cu[i], pages * geo.P};
+        sh.start[at] = start;
+      }
+    }
+    if (lane == 0) sh.n_tiles = t0, sh.total = sh.start[t0] = x0;
+  }
+  __syncthreads();
+  if (!first) return;
+  bool alone = false;
+#pragma unroll 1
+  for (int b = tid; b < B; b += kSharedThreads) {
+    const int g = group_of(b), skip = g < 0 ? 0 : shares(g);
+    a.skip[b] = skip;
+    alone |= skip == 0;
+  }
+  alone = __syncthreads_or(alone);
+#pragma unroll 1
+  for (int i = tid; i <= sh.n_tiles; i += kSharedThreads) {
+    a.plan->start[i] = sh.start[i];
+    if (i < sh.n_tiles) a.plan->tile[i] = sh.tile[i];
+  }
+  if (tid == 0) a.plan->n_tiles = sh.n_tiles, a.plan->total = sh.total, a.plan->alone = alone;
+}
 
 // The pieces of a CTA's share of the line: blocks [j0, j1) of KV head g of tile t.
 struct Walk {
@@ -243,15 +255,15 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
   if (warp == 9) {
     if (lane == 0) {
       sh.abort = 0;
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(smem_addr(&sh.q_full[i]), 1);
-        mbar_init(smem_addr(&sh.q_empty[i]), 1);
+      mbar_init(smem_addr(&sh.q_full), 1);
+      mbar_init(smem_addr(&sh.q_empty), 1);
+      for (int i = 0; i < kRegions; ++i) {
         mbar_init(smem_addr(&sh.s_full[i]), 1);
+        mbar_init(smem_addr(&sh.p_ready[i]), 128);
         mbar_init(smem_addr(&sh.o_full[i]), 1);
-        for (int h = 0; h < kParts; ++h) mbar_init(smem_addr(&sh.p_ready[i][h]), 128);
       }
       for (int i = 0; i < C::STAGES; ++i) {
-        mbar_init(smem_addr(&sh.kv_full[i]), 1);
+        mbar_init(smem_addr(&sh.kv_full[i]), TMA ? 1 : 2);  // (without maps, a warp for K and one for V)
         mbar_init(smem_addr(&sh.kv_empty[i]), 1);
       }
       mbar_init(smem_addr(&sh.drained), 1);
@@ -261,22 +273,21 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
     tc5::alloc(smem_addr(&sh.tmem), 512);
     tc5::fence_before();
   }
+  if (tid < 3) {
+    const CUtensorMap* const map = tid == 0 ? &a.tmq : tid == 1 ? &a.tmk : &a.tmv;
+    if (tid == 0 || TMA) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+  }
   pdl_launch();
   pdl_wait();
-  const int n_tiles = a.plan->n_tiles;
-  for (int t = tid; t <= n_tiles; t += kSharedThreads) {
-    sh.start[t] = a.plan->start[t];
-    if (t < n_tiles) sh.tile[t] = a.plan->tile[t];
-  }
-  __syncthreads();
+  make_plan(a, sh, blockIdx.x == 0);
+  const int n_tiles = sh.n_tiles;
   tc5::fence_after();
   const uint32_t tmem = sh.tmem;
   const uint32_t q_sm = base, kv_sm = base + 2 * C::QTILE;
-  auto stage = [&](int x) { return x % C::STAGES; };
   auto wait_for = [&](uint64_t* bar, int use) {
     return wait(smem_addr(bar), use & 1, sh, geo.status, wait_cycles);
   };
-  const Cut cut(a.plan->total, gridDim.x, 1);
+  const Cut cut(sh.total, gridDim.x, 1);
   const int share = blockIdx.x;
   const long long from = share < cut.shares ? cut.start(share) : 0, to = share < cut.shares ? cut.start(share + 1) : 0;
   auto halves = [&](const SharedTile& t) { return t.seqs > a.tok ? 2 : 1; };
@@ -284,12 +295,12 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (warp == 8 || (warp == 10 && !TMA)) {
-      // ---- loads: each piece's Q, then K_j, V_j, K_j+1, .. through the ring.  With maps one
-      // warp: a lane looks up the page of its box, a block ahead, and loads it.  Without,
+      // ---- loads: each piece's Q, then its pairs of K and V through the ring.  With maps one
+      // warp: a lane looks up the page of its box, some blocks at a time, and loads it.  Without,
       // a warp for K and one for V copy row by row.
       const bool keys = warp == 8;
-      int x = 0, q_uses[2] = {0, 0};
-      int pending = -1;  // the stage use whose copies have not been waited for (!TMA)
+      int st = 0, uses = 0, q_uses = 0;  // the next stage, and the times that the ring has gone round
+      int pending = -1;                  // the stage whose copies have not been waited for (!TMA)
       bool ok = true;
       auto landed = [&](int left) {  // all but the last `left` groups of copies
         if (left) asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -297,21 +308,21 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
         // (the tensor cores read through the async proxy)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sh.kv_full[stage(pending)]));
+        if (lane == 0) mbar_arrive(smem_addr(&sh.kv_full[pending]));
+        pending = -1;
       };
       for (Walk w(sh, n_tiles, H_kv, from, to); w.more() && ok; w.next(sh, H_kv)) {
         if (keys) {
-          for (int i = 0; i < halves(w.tile) && ok; ++i) {
-            if (q_uses[i] > 0) ok = __all_sync(kFull, wait_for(&sh.q_empty[i], q_uses[i] - 1));
-            if (!ok) break;
-            if (lane == 0) {
-              const uint32_t bar = smem_addr(&sh.q_full[i]);
-              mbar_arrive_expect_tx(bar, uint32_t(a.tok * G) * 128 * C::HALVES);
+          if (q_uses > 0) ok = __all_sync(kFull, wait_for(&sh.q_empty, q_uses - 1));
+          if (!ok) break;
+          if (lane == 0) {
+            const int nh = halves(w.tile);
+            mbar_arrive_expect_tx(smem_addr(&sh.q_full), uint32_t(nh * a.tok * G) * 128 * C::HALVES);
+            for (int i = 0; i < nh; ++i)
               for (int h = 0; h < C::HALVES; ++h)
-                tma_load_3d(q_sm + i * C::QTILE + h * (kRows * 128), &a.tmq, h * 64, w.g * G, w.tile.b0 + i * a.tok, bar);
-            }
-            ++q_uses[i];
+                tma_load_3d(q_sm + i * C::QTILE + h * (kRows * 128), &a.tmq, h * 64, w.g * G, w.tile.b0 + i * a.tok, smem_addr(&sh.q_full));
           }
+          ++q_uses;
         }
         const int32_t* const table = geo.table + int64_t(w.tile.lead) * geo.max_pages;
         auto page_of = [&](int pos) {
@@ -323,128 +334,157 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
           return page;
         };
         if constexpr (TMA) {
-          // the pages of `ahead` blocks at a time: a lane for each box
           const int boxes = kKeys / a.box, ahead = 32 / boxes;
-          int rows = 0;
-          for (int j = w.j0; j < w.j1 && ok; ++j) {
-            const int in = (j - w.j0) % ahead;
-            if (in == 0) {
+          int rows = 0, last = 0, left = 0;  // rows of `left` blocks, a lane for each box; the last block's
+          for (int j = w.j0; j <= w.j1 && ok; ++j) {
+            if (j < w.j1 && left == 0) {
               const int pos = j * kKeys + lane * a.box;
               // (rows behind the shared ones: zeros, since 0 * NaN is not 0)
               rows = pos < w.tile.n ? int(page_of(pos) * (geo.page_stride / D) + w.g * geo.P + pos % geo.P) : a.pool_rows;
+              left = ahead;
             }
-            const int row = __shfl_sync(kFull, rows, in * boxes + lane % boxes);
-            for (int y = 0; y < 2; ++y, ++x) {
-              if (x >= C::STAGES) ok = __all_sync(kFull, wait_for(&sh.kv_empty[stage(x)], x / C::STAGES - 1));
-              if (!ok) break;
-              const uint32_t bar = smem_addr(&sh.kv_full[stage(x)]);
-              if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE);
-              __syncwarp();
-              if (lane < boxes)
-                for (int h = 0; h < C::HALVES; ++h)
-                  tma_load_3d(kv_sm + stage(x) * C::TILE + h * (kKeys * 128) + lane * a.box * 128, y ? &a.tmv : &a.tmk, 0, row, h, bar);
-            }
+            const int row = __shfl_sync(kFull, rows, min((ahead - left) * boxes + lane % boxes, 31));
+            if (uses > 0) ok = __all_sync(kFull, wait_for(&sh.kv_empty[st], uses - 1));
+            if (!ok) break;
+            const uint32_t bar = smem_addr(&sh.kv_full[st]), dst = kv_sm + st * 2 * C::TILE + lane * a.box * 128;
+            if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE * ((j < w.j1) + (j > w.j0)));
+            __syncwarp();
+            if (lane < boxes)
+              for (int h = 0; h < C::HALVES; ++h) {
+                if (j < w.j1) tma_load_3d(dst + h * (kKeys * 128), &a.tmk, 0, row, h, bar);
+                if (j > w.j0) tma_load_3d(dst + C::TILE + h * (kKeys * 128), &a.tmv, 0, last, h, bar);
+              }
+            last = row;
+            --left;
+            if (++st == C::STAGES) st = 0, ++uses;
           }
         } else {
           constexpr int CH = D / 8;  // 16-byte chunks of a row
           const uint8_t* const pool = static_cast<const uint8_t*>(keys ? a.own.k : a.own.v);
-          for (int j = w.j0; j < w.j1; ++j, x += 2) {
-            const int y = x + (keys ? 0 : 1);
-            int64_t at[kKeys / 32];  // bytes from the pool's start to rows lane + 32 i, -1: no row
+          for (int y = w.j0; y <= w.j1; ++y) {
+            const int j = keys ? y : y - 1;  // the block
+            const bool there = j >= w.j0 && j < w.j1;
+            int64_t at[2];  // bytes from the pool's start to rows lane and lane + 32, -1: no row
 #pragma unroll
-            for (int i = 0; i < kKeys / 32; ++i) {
+            for (int i = 0; i < 2; ++i) {
               const int pos = j * kKeys + lane + 32 * i;
-              const int64_t row = page_of(pos) * geo.page_stride + (int64_t(w.g) * geo.P + pos % geo.P) * D;
-              at[i] = pos < w.tile.n ? row * 2 : -1;
+              const bool in = there && pos < w.tile.n && lane + 32 * i < kKeys;
+              const int64_t row = page_of(in ? pos : w.tile.n) * geo.page_stride + (int64_t(w.g) * geo.P + pos % geo.P) * D;
+              at[i] = in ? row * 2 : -1;
             }
-            const int before = y / C::STAGES - 1;  // the stage's last use
-            if (y >= C::STAGES && !__all_sync(kFull, mbar_test_wait(smem_addr(&sh.kv_empty[stage(y)]), before & 1))) {
+            if (uses > 0 && !__all_sync(kFull, mbar_test_wait(smem_addr(&sh.kv_empty[st]), (uses - 1) & 1))) {
               // (whoever has to free it may wait for what is pending)
-              if (pending >= 0) landed(0), pending = -1;
-              ok = __all_sync(kFull, wait_for(&sh.kv_empty[stage(y)], before));
+              if (pending >= 0) landed(0);
+              ok = __all_sync(kFull, wait_for(&sh.kv_empty[st], uses - 1));
             }
             if (!ok) break;
+            if (there) {
 #pragma unroll
-            for (int i = 0; i < kKeys / 32; ++i)
+              for (int i = 0; i < 2; ++i)
 #pragma unroll 8
-              for (int z = 0; z < CH; ++z) {
-                const int r = (z * 32 + lane) / CH, ch = lane % CH;  // of these 32 rows
-                const int64_t src = __shfl_sync(kFull, at[i], r);
-                const uint32_t dst = kv_sm + stage(y) * C::TILE + (ch >> 3) * (kKeys * 128) + (32 * i + r) * 128 + (((ch & 7) ^ (r & 7)) << 4);
-                cp_async16_zfill(dst, pool + max(src, int64_t(0)) + (src >= 0 ? ch * 16 : 0), src >= 0 ? 16 : 0);
-              }
+                for (int z = 0; z < (i == 0 ? CH : CH * (kKeys - 32) / 32); ++z) {
+                  const int r = (z * 32 + lane) / CH, ch = lane % CH;  // of these 32 rows
+                  const int64_t src = __shfl_sync(kFull, at[i], r);
+                  const uint32_t dst = kv_sm + (st * 2 + !keys) * C::TILE + (ch >> 3) * (kKeys * 128) + (32 * i + r) * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                  cp_async16_zfill(dst, pool + max(src, int64_t(0)) + (src >= 0 ? ch * 16 : 0), src >= 0 ? 16 : 0);
+                }
+            }
             asm volatile("cp.async.commit_group;" ::: "memory");
             if (pending >= 0) landed(1);
-            pending = y;
+            pending = st;
+            if (++st == C::STAGES) st = 0, ++uses;
           }
           // (the next piece's Q waits for this one's last scores, and so for its last K)
-          if (pending >= 0) landed(0), pending = -1;
+          if (pending >= 0) landed(0);
         }
       }
       // no copy may be in flight when the CTA exits (after a wait that gave up, some may
       // never have been waited for)
       if (!TMA && pending >= 0) landed(0);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (q_uses[i] > 0) mbar_wait(smem_addr(&sh.q_full[i]), (q_uses[i] - 1) & 1);
+      if (q_uses > 0) mbar_wait(smem_addr(&sh.q_full), (q_uses - 1) & 1);
       if (TMA)
-        for (int y = max(0, x - C::STAGES); y < x; ++y)
-          mbar_wait(smem_addr(&sh.kv_full[stage(y)]), (y / C::STAGES) & 1);
+        for (int y = 0; y < C::STAGES; ++y) {
+          const int last = y < st ? uses : uses - 1;  // the stage's last use
+          if (last >= 0) mbar_wait(smem_addr(&sh.kv_full[y]), last & 1);
+        }
     } else if (warp == 9) {
       // ---- products, all of them from one lane
       if (tc5::elect()) {
+        // The tensor cores hold only a few products in waiting (some 200 clocks), so what lies
+        // between one step's and the next's is kept short: stages, regions and phases are counted
+        // up and not divided, a step has one wait for P, done while the step before is multiplied,
+        // and there is one commit for the scores and one for a pair of K and V.  (With a wait and
+        // a commit for each of K, V and the two parts of P: 1400 clocks a step, of which 910 are
+        // products.)
         constexpr uint32_t kIdS = tc5::idesc_bf16(kRows, kKeys, false);
         constexpr uint32_t kIdO = tc5::idesc_bf16(kRows, D, true);
-        int x = 0, tiles[2] = {0, 0}, steps[2] = {0, 0};  // x: blocks of the pieces before
+        const uint32_t full = smem_addr(&sh.kv_full[0]), empty = smem_addr(&sh.kv_empty[0]);
+        const uint32_t s_full = smem_addr(&sh.s_full[0]), p_ready = smem_addr(&sh.p_ready[0]), o_full = smem_addr(&sh.o_full[0]);
+        const uint64_t q_desc = tc5::desc_sw128(q_sm, 16, 1024), k_desc = tc5::desc_sw128(kv_sm, 16, 1024),
+                       v_desc = tc5::desc_sw128(kv_sm + C::TILE, kKeys * 128, 1024);
+        auto await = [&](uint32_t bar, uint32_t parity) { return wait(bar, parity, sh, geo.status, wait_cycles); };
+        uint32_t ks = 0, k_ph = 0, vs = 0;             // the stages of the next K and V
+        uint32_t rs = 0, rp = 0, p_ph = 0;             // the regions of the next scores and P
+        uint32_t s_half = 0, half = 0, q_ph = 0;       // the halves of the next scores and P
         bool ok = true;
-        auto full = [&](int y) { return wait_for(&sh.kv_full[stage(y)], y / C::STAGES); };
         for (Walk w(sh, n_tiles, H_kv, from, to); w.more() && ok; w.next(sh, H_kv)) {
-          // Steps of a piece: step k is half k % 2 with block k / 2 where both halves have
-          // rows; else both halves have the same rows and take the blocks in turn.
-          const int nh = halves(w.tile), n = (w.j1 - w.j0) * nh;
-          auto block = [&](int k) { return x + (nh == 2 ? k >> 1 : k); };
-          auto scores = [&](int k) {  // S_i = Q_i K^T
-            const int i = k & 1, y = 2 * block(k);
-            ok = ok && full(y);
+          // Steps of a piece: block k / 2 for a half where both halves have rows, else block k,
+          // both halves having the same rows.  The halves take the steps in turn, over all pieces.
+          const bool two = halves(w.tile) == 2;
+          const int n = (w.j1 - w.j0) << two;
+          auto scores = [&](int k) {  // S = Q K^T
+            if (!two || (k & 1) == 0) ok = ok && await(full + ks * 8, k_ph);
             if (!ok) return;
-            const uint64_t qd = tc5::desc_sw128(q_sm + (nh == 2 ? i : 0) * C::QTILE, 16, 1024);
-            const uint64_t kd = tc5::desc_sw128(kv_sm + stage(y) * C::TILE, 16, 1024);
+            const uint64_t qd = q_desc + (two && s_half ? C::QTILE >> 4 : 0), kd = k_desc + ks * (2 * C::TILE >> 4);
+            const uint32_t d = tmem + rs * kRegion;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              tc5::mma_ss(tmem + i * 128, qd + (((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4),
+              tc5::mma_ss(d, qd + (((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4),
                           kd + (((kk / 4) * (kKeys * 128) + (kk % 4) * 32) >> 4), kIdS, kk > 0);
-            tc5::commit(smem_addr(&sh.s_full[i]));
-            if (nh == 1 || i == 1) tc5::commit(smem_addr(&sh.kv_empty[stage(y)]));
-            if (nh == 2 ? k + 2 >= n : k + 1 == n) tc5::commit(smem_addr(&sh.q_empty[nh == 2 ? i : 0]));
-          };
-          for (int i = 0; i < nh; ++i) ok = ok && wait_for(&sh.q_full[i], tiles[i]++);
-          // (S_i's columns are free: the products with P_i, which lay there, were issued before)
-          scores(0);
-          if (n > 1) scores(1);
-          for (int k = 0; k < n && ok; ++k) {
-            const bool fresh = (k >> 1) % kChain == 0;  // the half's sums have been read
-            const int i = k & 1, y = 2 * block(k) + 1;
-            ok = full(y);
-            const uint64_t vd = tc5::desc_sw128(kv_sm + stage(y) * C::TILE, kKeys * 128, 1024);
-#pragma unroll
-            for (int h = 0; h < kParts; ++h) {  // O_i (+)= P_i V, the parts of P as they come
-              ok = ok && wait_for(&sh.p_ready[i][h], steps[i]);
-              if (!ok) break;
-              tc5::fence_after();
-#pragma unroll
-              for (int k16 = h * (kKeys / kParts / 16); k16 < (h + 1) * (kKeys / kParts / 16); ++k16)
-#pragma unroll
-                for (int e = kTerms - 1; e >= 0; --e)  // small terms first
-                  tc5::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + term_at(h, e) + (k16 & 1) * 8, vd + k16 * (2048 >> 4), kIdO,
-                              !fresh || k16 > 0 || e + 1 < kTerms);
+            tc5::commit(s_full + rs * 8);
+            if (!two || (k & 1)) {
+              if (++ks == C::STAGES) ks = 0, k_ph ^= 1;
             }
-            ++steps[i];
-            if (!ok) break;
-            if ((k >> 1) % kChain == kChain - 1 || k + 2 >= n) tc5::commit(smem_addr(&sh.o_full[i]));
-            if (nh == 1 || i == 1) tc5::commit(smem_addr(&sh.kv_empty[stage(y)]));
-            if (k + 2 < n) scores(k + 2);
+            if (++rs == kRegions) rs = 0;
+            s_half ^= 1;
+          };
+          ok = await(smem_addr(&sh.q_full), q_ph);
+          q_ph ^= 1;
+          // (a region is free: the products with the P that lay there were issued before)
+          for (int k = 0; k < min(n, kRegions); ++k) scores(k);
+          tc5::commit(empty + vs * 8);  // the first pair, which has no V
+          if (++vs == C::STAGES) vs = 0;
+          if (n <= kRegions) tc5::commit(smem_addr(&sh.q_empty));
+          ok = ok && await(p_ready + rp * 8, p_ph);
+          for (int k = 0; k < n && ok; ++k) {
+            if (two ? k == n - 2 : k == n - 1) {  // the last pair, which has no K
+              ok = await(full + ks * 8, k_ph);
+              if (++ks == C::STAGES) ks = 0, k_ph ^= 1;
+              if (!ok) break;
+            }
+            const bool fresh = (k >> 1) % kChain == 0;  // the half's sums have been read
+            const uint64_t vd = v_desc + vs * (2 * C::TILE >> 4);
+            const uint32_t d = tmem + kSums + half * 128, p = tmem + rp * kRegion;
+            tc5::fence_after();
+#pragma unroll
+            for (int z = 0; z < kKeys / 16; ++z)  // O (+)= P V
+#pragma unroll
+              for (int e = kTerms - 1; e >= 0; --e)  // small terms first
+                tc5::mma_ts(d, p + term_at(z, e), vd + z * (2048 >> 4), kIdO, !fresh || z > 0 || e + 1 < kTerms);
+            if (!two || (k & 1)) {
+              tc5::commit(empty + vs * 8);
+              if (++vs == C::STAGES) vs = 0;
+            }
+            // (who waits for these products otherwise waits for scores that were issued behind them)
+            if (k + kRegions >= n) tc5::commit(o_full + rp * 8);
+            half ^= 1;
+            if (++rp == kRegions) rp = 0, p_ph ^= 1;
+            // P of the next step mostly lies there already; if not, the scores go first
+            const bool there = k + 1 < n && mbar_test_wait(p_ready + rp * 8, p_ph);
+            if (k + kRegions < n) scores(k + kRegions);
+            if (k + kRegions + 1 == n) tc5::commit(smem_addr(&sh.q_empty));
+            if (k + 1 < n && !there) ok = ok && await(p_ready + rp * 8, p_ph);
           }
-          x += w.j1 - w.j0;
         }
         // the products in flight end before tensor memory is freed, whether or
         // not a softmax warp still waits for them
@@ -459,52 +499,85 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
     const int i = warp >> 2;
     const int r = tid & 127;
     const uint32_t lanes = uint32_t(warp & 3) << 21;  // 32 * (warp % 4) in the lane field
-    const uint32_t s_tm = tmem + i * 128 + lanes, o_tm = tmem + 256 + i * 128 + lanes;
-    const uint32_t p_bar = smem_addr(&sh.p_ready[i][0]);
+    const uint32_t o_tm = tmem + kSums + i * 128 + lanes;
     const float c = a.own.scale_log2;
-    int steps = 0, sums = 0;
+    int done = 0;            // steps of the pieces before
+    uint32_t o_ph = 0;       // bit r: parity of the region's next commit of sums
     bool ok = true;
     for (Walk w(sh, n_tiles, H_kv, from, to); w.more() && ok; w.next(sh, H_kv)) {
-      const int nh = halves(w.tile), every = nh == 2 ? 1 : 2;
+      const bool two = halves(w.tile) == 2;
+      const int n = (w.j1 - w.j0) << two;
       float m = -INFINITY, l = 0.f;
       uint64_t o[D / 2];
 #pragma unroll
       for (int x = 0; x < D / 2; ++x) o[x] = 0;
-      int k = 0;  // blocks of this half
-      for (int j = w.j0 + (nh == 2 ? 0 : i); j < w.j1; j += every, ++k, ++steps) {
-        ok = __all_sync(kFull, wait_for(&sh.s_full[i], steps));
+      // the products with V of the last few blocks, from tensor memory (the tensor cores truncate
+      // where they add; here it is fp32)
+      auto add_sums = [&] {
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          uint32_t v[16];
+          tc5::ld16(o_tm + 16 * x, v);
+          tc5::wait_ld();
+          pin(v);
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            o[8 * x + y] = add2(o[8 * x + y], pair(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])));
+        }
+      };
+      // The products of step k are complete once the scores of step k + 3 are, which were issued
+      // behind them, or their own commit has arrived, where there are no such scores.
+      auto summed = [&](int k) {
+        const uint32_t step = done + k, reg = step % kRegions;
+        if (k + kRegions < n) return __all_sync(kFull, wait_for(&sh.s_full[reg], step / kRegions + 1));
+        return __all_sync(kFull, wait_for(&sh.o_full[reg], o_ph >> reg & 1));
+      };
+      const int k0 = (i - done) & 1;
+      int chain = 0;  // blocks whose products are in tensor memory
+      for (int k = k0; k < n; k += 2) {
+        const int j = w.j0 + (k >> two), lim = w.tile.n - j * kKeys;
+        const uint32_t step = done + k, reg = step % kRegions, s_tm = tmem + reg * kRegion + lanes;
+        ok = __all_sync(kFull, wait_for(&sh.s_full[reg], step / kRegions));
         if (!ok) break;
         tc5::fence_after();
-        // (32 scores at a time, the first ones again for their exponentials: registers are short)
-        const int lim = w.tile.n - j * kKeys;
+        // (32 scores and 16, these again for their exponentials: registers are short)
         uint32_t s[32];
-        auto load = [&](int h) {
-          tc5::ld32(s_tm + 32 * h, s);
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        {
+          uint32_t t[16];
+          tc5::ld16(s_tm + 32, t);
+          tc5::ld32(s_tm, s);
           tc5::wait_ld();
+          pin(t);
           pin(s);
           if (lim < kKeys) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) s[x] = 32 * h + x < lim ? s[x] : 0xff800000u;
+            for (int x = 0; x < 32; ++x) s[x] = x < lim ? s[x] : 0xff800000u;
+#pragma unroll
+            for (int x = 0; x < 16; ++x) t[x] = 32 + x < lim ? t[x] : 0xff800000u;
           }
-        };
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 1; h >= 0; --h) {
-          load(h);
-#pragma unroll
-          for (int x = 0; x < 32; x += 2)
-            mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+          for (int x = 0; x < 16; x += 2)
+            mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(t[x]), __uint_as_float(t[x + 1]));
         }
+#pragma unroll
+        for (int x = 0; x < 32; x += 2)
+          mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
         const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
-        const bool grow = (top - m) * c > kGrow;
-        if (__any_sync(kFull, grow)) {
+        const bool grow = (top - m) * c > kGrow, any = __any_sync(kFull, grow);
+        if (chain == kChain || (any && chain > 0)) {
+          ok = summed(k - 2);
+          if (!ok) break;
+          tc5::fence_after();
+        }
+        if (chain == kChain) add_sums(), chain = 0;
+        if (any) {
           const float f = grow ? ex2((m - top) * c) : 1.f;
           if (grow) m = top;
           l *= f;
 #pragma unroll
           for (int x = 0; x < D / 2; ++x) o[x] = mul2(o[x], pair(f, f));
-          if (k % kChain != 0) {
-            // (the products of the block before are complete: they were issued before these scores)
+          if (chain > 0) {
 #pragma unroll 1
             for (int x = 0; x < D / 16; ++x) {
               uint32_t v[16];
@@ -520,42 +593,39 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
         const float mc = m == -INFINITY ? 0.f : -m * c;
         const uint64_t cc = pair(c, c), mm = pair(mc, mc);
         uint64_t sum[4] = {0, 0, 0, 0};
+        hand_over(smem_addr(&sh.p_ready[reg]), [&] {
 #pragma unroll
-        for (int h = 0; h < kParts; ++h) {
-          if (h > 0) load(h);
-          hand_over(p_bar + 8 * h, [&] {
+          for (int z = 0; z < kKeys / 16; ++z) {
+            if (z == 2) {
+              uint32_t t[16];
+              tc5::ld16(s_tm + 32, t);
+              tc5::wait_ld();
+              pin(t);
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              uint32_t p[kTerms][8];
-              exp_terms(s + z * 16, cc, mm, sum, p);
-#pragma unroll
-              for (int e = 0; e < kTerms; ++e) tc5::st8(s_tm + term_at(h, e) + z * 8, p[e]);
+              for (int x = 0; x < 16; ++x) s[x] = 32 + x < lim ? t[x] : 0xff800000u;
             }
-          });
-        }
+            uint32_t p[kTerms][8];
+            exp_terms(s + (z & 1) * 16, cc, mm, sum, p);
+#pragma unroll
+            for (int e = 0; e < kTerms; ++e) tc5::st8(s_tm + term_at(z, e), p[e]);
+          }
+        });
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += lo(sum[0]) + hi(sum[0]);
-        // the products with V of a few blocks, added here in fp32 (the tensor cores truncate
-        // where they add)
-        if (k % kChain != kChain - 1 && j + every < w.j1) continue;
-        ok = __all_sync(kFull, wait_for(&sh.o_full[i], sums++));
-        if (!ok) break;
+        ++chain;
+      }
+      if (ok && chain > 0) {
+        ok = summed(n - 1 - ((n - 1 - k0) & 1));
         tc5::fence_after();
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          uint32_t v[32];
-          tc5::ld32(o_tm + 32 * x, v);
-          tc5::wait_ld();
-          pin(v);
-#pragma unroll
-          for (int y = 0; y < 16; ++y)
-            o[16 * x + y] = add2(o[16 * x + y], pair(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])));
-        }
+        if (ok) add_sums();
       }
       if (!ok) break;
+      // the commits of this piece's last steps
+      for (int k = max(0, n - kRegions); k < n; ++k) o_ph ^= 1u << (done + k) % kRegions;
+      done += n;
       // the piece's state (rows side by side, so that the lanes' stores are)
       float* const st = a.states + int64_t(share + w.t * H_kv + w.g) * (kTileRows * (D + 2)) + i * kRows + r;
-      if (r < a.tok * G && (nh == 2 ? i : 0) * a.tok + r / G < w.tile.seqs) {
+      if (r < a.tok * G && (two ? i : 0) * a.tok + r / G < w.tile.seqs) {
 #pragma unroll
         for (int x = 0; x < D / 2; ++x) st[2 * x * kTileRows] = lo(o[x]), st[(2 * x + 1) * kTileRows] = hi(o[x]);
         st[D * kTileRows] = m, st[(D + 1) * kTileRows] = l;
@@ -659,7 +729,6 @@ cudaError_t launch_shared(const SharedArgs& a, bool own_tma, int grid, cudaStrea
   static std::atomic<uint64_t> allowed{0};  // the devices on which the kernel may use its shared memory
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(shared_attn_kernel<D, TMA>), int(SCfg<D>::SMEM), allowed);
   if (e != cudaSuccess) return e;
-  if ((e = launch_pdl(shared_plan_kernel, dim3(1), kPlan, 0, st, a)) != cudaSuccess) return e;
   if ((e = launch_pdl(shared_attn_kernel<D, TMA>, dim3(grid), kSharedThreads, SCfg<D>::SMEM, st, a)) != cudaSuccess) return e;
   if ((e = launch_paged_pieces(a.own, D, own_tma, grid, st)) != cudaSuccess) return e;
   const int units = a.own.geo.B * a.own.geo.H_kv, most = 4 * grid, y = a.own.G * (D / 32);

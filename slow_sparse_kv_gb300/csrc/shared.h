@@ -16,7 +16,7 @@ struct SharedTile {
   int32_t n;         // positions that they share
 };
 
-// What the planning kernel leaves for the others.
+// What the first kernel leaves for the others.
 struct SharedPlan {
   int32_t n_tiles;
   int32_t alone;    // != 0: some sequence shares nothing
@@ -29,7 +29,7 @@ struct SharedArgs {
   // 3-D maps: [sequence][head][d] of q, boxes of 64 elements of d, G heads and 128 / G sequences;
   // of the pool's rows (64 elements of d, row, 64-element block of d), boxes of `box` rows
   CUtensorMap tmq, tmk, tmv;
-  int32_t box;        // a power of two that divides the page size and 64, 8 at least; 0: no maps of k and v
+  int32_t box;        // 8, 16, 24 or 48, which divides the page size; 0: no maps of k and v
   int32_t pool_rows;  // rows of the maps: what lies behind reads as zero
   int32_t tok;        // sequences of 128 query rows: 128 / G
   int32_t max_tiles;  // that the plan may have
