@@ -40,14 +40,15 @@ struct Cut {
     total = total_;
     const long long most = (total + least - 1) / least;
     shares = most < grid ? int(most) : grid;
-    per = shares > 0 ? total / shares : 0;
+    // (a 64-bit division takes ~10 times as long)
+    per = shares <= 0 ? 0 : total < (1LL << 31) ? (long long)(uint32_t(total) / uint32_t(shares)) : total / shares;
     extra = shares > 0 ? int(total - per * shares) : 0;
     wide = extra * (per + 1);
   }
   __device__ __forceinline__ long long start(int share) const { return share * per + min(share, extra); }
   // the share that holds tile x
   __device__ __forceinline__ int holder(long long x) const {
-    if (total < (1LL << 31))  // (a 64-bit division takes ~10 times as long)
+    if (total < (1LL << 31))
       return x < wide ? int(uint32_t(x) / uint32_t(per + 1)) : extra + int(uint32_t(x - wide) / uint32_t(per));
     return int(x < wide ? x / (per + 1) : extra + (x - wide) / per);
   }

@@ -34,7 +34,7 @@
 namespace sfi {
 namespace {
 
-constexpr int kSharedThreads = 384;  // 2 softmax warpgroups; two loading warps, an MMA warp, one that idles
+constexpr int kSharedThreads = 384;  // 2 softmax warpgroups; two loading warps, an MMA warp, one for the plan
 constexpr int kRows = 128;           // query rows of a half tile
 constexpr int kKeys = 48;            // keys of a block
 // Tensor memory: three regions of a block's scores and, over and behind them, its P, which the
@@ -46,7 +46,7 @@ constexpr int kTerms = 3;            // bf16 terms of P
 constexpr int kChain = 4;            // blocks of a half whose products with V are added in tensor memory
 constexpr float kGrow = 8.0f;        // growth of the maximum (log2) that moves m
 template <int D>
-constexpr int kJoinBlocks = kTileRows / 32 * (D / 32);  // CTAs' worth of a tile and KV head in the join
+constexpr int kJoinBlocks = kTileRows / 32 * (D / 64);  // CTAs' worth of a tile and KV head in the join
 constexpr int kOwnTile = 16;         // positions of a tile of paged_attn.cu's kernel in bf16
 
 template <int D>
@@ -88,12 +88,28 @@ struct SharedMem {
   bool bad[kMaxBatch];
 };
 
-// Which sequences share what, as tiles; every CTA makes the plan for itself, and the first one
-// leaves it for the kernels behind.  Offsets that are out of order leave all sequences by themselves;
-// so does, for its group, a number of pages that is out of range or more than a member holds:
-// the result does not depend on what is shared, only the time does.  (Loops are not unrolled:
-// this runs once, and its instructions take longer to come than to run.)
-__device__ __forceinline__ void make_plan(const SharedArgs& a, SharedMem& sh, bool first) {
+// The group of sequence b: the last one that begins at or before it, if it holds it; -1: none.
+__device__ __forceinline__ int group_of(const SharedMem& sh, int n, int b) {
+  int lo = 0, hi = n;  // (as many groups begin at or before b as lie below `lo`)
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (sh.cu[mid] <= b) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo > 0 && b < sh.cu[lo] ? lo - 1 : -1;
+}
+
+// Pages that group i shares (one sequence alone would gain nothing).
+__device__ __forceinline__ int shares_of(const SharedMem& sh, int i) {
+  return !sh.bad[i] && sh.cu[i + 1] - sh.cu[i] > 1 ? sh.pages[i] : 0;
+}
+
+// Which sequences share what, as tiles, made by every CTA for itself; returns the number of groups,
+// 0 if their offsets are out of order: then all sequences are by themselves.  So are those of a
+// group whose number of pages is out of range or more than a member holds: the result does not
+// depend on what is shared, only the time does.  (Loops are not unrolled: this runs once, and its
+// instructions take longer to come than to run.)
+__device__ __forceinline__ int make_plan(const SharedArgs& a, SharedMem& sh, bool first) {
   const PagedGeo& geo = a.own.geo;
   const int tid = threadIdx.x, lane = tid & 31, n = a.n_groups, B = geo.B, cap = geo.max_pages * geo.P;
   const int len0 = tid < B ? geo.len[tid] : 0;
@@ -110,21 +126,11 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, SharedMem& sh, bo
   bool wrong = false;
 #pragma unroll 1
   for (int i = tid; i < n; i += kSharedThreads) wrong |= sh.cu[i] < 0 || sh.cu[i] > sh.cu[i + 1] || sh.cu[i + 1] > B;
-  const bool none = __syncthreads_or(wrong);
-  if (none && first && tid == 0) set_status(geo.status, SFI_DEV_LEN_OVER_CAP);
-  // the group of sequence b: the last one that begins at or before it, if it holds it
-  auto group_of = [&](int b) {
-    int lo = 0, hi = none ? 0 : n;  // (as many groups begin at or before b as lie below `lo`)
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (sh.cu[mid] <= b) lo = mid + 1;
-      else hi = mid;
-    }
-    return lo > 0 && b < sh.cu[lo] ? lo - 1 : -1;
-  };
+  const int groups = __syncthreads_or(wrong) ? 0 : n;
+  if (groups < n && first && tid == 0) set_status(geo.status, SFI_DEV_LEN_OVER_CAP);
 #pragma unroll 1
   for (int b = tid; b < B; b += kSharedThreads) {
-    const int g = group_of(b), len = b == tid ? len0 : geo.len[b];
+    const int g = group_of(sh, groups, b), len = b == tid ? len0 : geo.len[b];
     if (g < 0 || sh.pages[g] <= 0) continue;
     if (len < 0 || len > cap || len < (long long)sh.pages[g] * geo.P) {
       if (first) set_status(geo.status, SFI_DEV_LEN_OVER_CAP);
@@ -132,14 +138,12 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, SharedMem& sh, bo
     }
   }
   __syncthreads();
-  // pages that group i shares (one sequence alone would gain nothing)
-  auto shares = [&](int i) { return !none && !sh.bad[i] && sh.cu[i + 1] - sh.cu[i] > 1 ? sh.pages[i] : 0; };
   if (tid < 32) {
     int t0 = 0;  // tiles and blocks of the groups before
     long long x0 = 0;
 #pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + lane, pages = i < n ? shares(i) : 0;
+    for (int i0 = 0; i0 < groups; i0 += 32) {
+      const int i = i0 + lane, pages = i < groups ? shares_of(sh, i) : 0;
       const int tiles = pages > 0 ? (sh.cu[i + 1] - sh.cu[i] + 2 * a.tok - 1) / (2 * a.tok) : 0;
       const long long blocks = (long long)((pages * geo.P + kKeys - 1) / kKeys) * geo.H_kv;
       int t = tiles;
@@ -164,21 +168,38 @@ __device__ __forceinline__ void make_plan(const SharedArgs& a, SharedMem& sh, bo
     if (lane == 0) sh.n_tiles = t0, sh.total = sh.start[t0] = x0;
   }
   __syncthreads();
-  if (!first) return;
-  bool alone = false;
+  return groups;
+}
+
+// Leaves the plan for the kernels behind (one warp of the first CTA, beside the others' work).
+__device__ __forceinline__ void publish_plan(const SharedArgs& a, const SharedMem& sh, int groups) {
+  const PagedGeo& geo = a.own.geo;
+  const int lane = threadIdx.x & 31, cap = geo.max_pages * geo.P;
 #pragma unroll 1
-  for (int b = tid; b < B; b += kSharedThreads) {
-    const int g = group_of(b), skip = g < 0 ? 0 : shares(g);
-    a.skip[b] = skip;
-    alone |= skip == 0;
-  }
-  alone = __syncthreads_or(alone);
-#pragma unroll 1
-  for (int i = tid; i <= sh.n_tiles; i += kSharedThreads) {
+  for (int i = lane; i <= sh.n_tiles; i += 32) {
     a.plan->start[i] = sh.start[i];
     if (i < sh.n_tiles) a.plan->tile[i] = sh.tile[i];
   }
-  if (tid == 0) a.plan->n_tiles = sh.n_tiles, a.plan->total = sh.total, a.plan->alone = alone;
+  bool alone = false;
+  long long before = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < geo.B; b0 += 32) {
+    const int b = b0 + lane, g = b < geo.B ? group_of(sh, groups, b) : -1, skip = g < 0 ? 0 : shares_of(sh, g);
+    const int len = b < geo.B ? min(max(geo.len[b], 0), cap) : 0;
+    if (b < geo.B) a.skip[b] = skip;
+    alone |= b < geo.B && skip == 0;
+    const int tiles = b < geo.B ? (len - skip * geo.P + kOwnTile - 1) / kOwnTile : 0;
+    long long x = tiles;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x1 = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += x1;
+    }
+    if (b < geo.B) a.plan->own[b + 1] = before + x;
+    before += __shfl_sync(kFull, x, 31);
+  }
+  alone = __any_sync(kFull, alone);
+  if (lane == 0) a.plan->own[0] = 0, a.plan->n_tiles = sh.n_tiles, a.plan->total = sh.total, a.plan->alone = alone;
 }
 
 // The pieces of a CTA's share of the line: blocks [j0, j1) of KV head g of tile t.
@@ -279,7 +300,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
   }
   pdl_launch();
   pdl_wait();
-  make_plan(a, sh, blockIdx.x == 0);
+  const int groups = make_plan(a, sh, blockIdx.x == 0);
   const int n_tiles = sh.n_tiles;
   tc5::fence_after();
   const uint32_t tmem = sh.tmem;
@@ -492,6 +513,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
         mbar_wait(smem_addr(&sh.drained), 0);
       }
       __syncwarp();
+    } else if (warp == 11 && blockIdx.x == 0) {
+      publish_plan(a, sh, groups);
     }
   } else {
     // ---- softmax, sums and states of half i: one thread per row
@@ -641,87 +664,160 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
 }
 
 // ---- the join
-// The first `tile_ctas` CTAs take 32 rows of a tile and 32 columns each, a lane a row, a warp 4
-// columns: the states of the shared part in the line's order, then those of the
-// sequence's own positions.  The others join the pieces of sequences that share nothing.
+// Items of 32 rows of a tile and 64 columns: first the states of the shared part in the line's
+// order, a lane a row and a warp 8 columns, as these states lie; then, through shared memory,
+// those of the sequences' own positions, a lane two columns and a warp 4 rows, as those do
+// (with a lane a row there too, each read touched 32 lines: 25 us where it is 10 now).  Then
+// the pieces of sequences that share nothing.  Bound by latency, a few dependent reads from L2, so
+// nothing is computed again that the first kernel could leave.
+struct State {
+  float m = -INFINITY, l = 0.f;
+  // Takes in N states; returns the factors of what it was and of theirs.
+  template <int N>
+  __device__ __forceinline__ float take(const float (&mv)[N], const float (&lv)[N], float (&f)[N], float c) {
+    float top = m;
+#pragma unroll
+    for (int w = 0; w < N; ++w) top = fmaxf(top, mv[w]);
+    const float was = m == -INFINITY && l == 0.f ? 0.f : ex2((m - top) * c);
+    l = was == 0.f ? 0.f : l * was;
+#pragma unroll
+    for (int w = 0; w < N; ++w) {
+      // (one that saw only scores of -infinity, or nothing, adds nothing)
+      f[w] = mv[w] == -INFINITY && lv[w] == 0.f ? 0.f : ex2((mv[w] - top) * c);
+      l = f[w] == 0.f ? l : fmaf(f[w], lv[w], l);
+    }
+    m = top;
+    return was;
+  }
+};
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) shared_join_kernel(const __grid_constant__ SharedArgs a, int grid, int tile_ctas, int ny) {
-  constexpr int PER = 4, AHEAD = 8;  // columns of a thread; states read at a time
+__global__ void __launch_bounds__(kThreads) shared_join_kernel(const __grid_constant__ SharedArgs a, int grid, int ny) {
+  constexpr int PER = 8, AHEAD = 4;  // columns of a thread; states read at a time
+  constexpr int ROWS = 32 / kWarps;  // of a warp, of the own positions
   __shared__ Line ln;
+  __shared__ float o_sh[32][66], m_sh[32], l_sh[32];
   const PagedGeo& geo = a.own.geo;
   const int H_kv = geo.H_kv, G = a.own.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float c = a.own.scale_log2;
   pdl_launch();
   pdl_wait();
-  const int n_tiles = a.plan->n_tiles;
-  const long long total = a.plan->total, items = (long long)n_tiles * H_kv * kJoinBlocks<D>;
-  if (int(blockIdx.x) >= tile_ctas ? !a.plan->alone : blockIdx.x >= items) return;
-  scan_lengths<kOwnTile>(geo, ln, false);
-  const Cut own(ln.pre[geo.B] * H_kv, grid * kPagedWarps, 1);
-  if (int(blockIdx.x) >= tile_ctas) {
-    const int x = blockIdx.x - tile_ctas, nx = (gridDim.x - tile_ctas) / ny;
-    join_units<kOwnTile, D>(a.own, ln, own, true, x % nx, nx, x / nx, ny);
-    return;
-  }
-  const Cut shared(total, grid, 1);
-  for (long long y = blockIdx.x; y < items; y += tile_ctas) {
-    const int unit = int(y / kJoinBlocks<D>), t = unit / H_kv, g = unit - t * H_kv, at = int(y % (kTileRows / 32)) * 32 + lane;
-    const int d = int(y % kJoinBlocks<D>) / (kTileRows / 32) * 32 + warp * PER;
+  const int n_tiles = a.plan->n_tiles, alone = a.plan->alone;
+  const Cut shared(a.plan->total, grid, 1), own(a.plan->own[geo.B] * H_kv, grid * kPagedWarps, 1);
+  // (32-row blocks that all tiles have first: they are spread over the SMs)
+  const int columns = n_tiles * H_kv * (D / 64), items = columns * (kTileRows / 32);
+  for (int y = blockIdx.x; y < items; y += gridDim.x) {
+    const int block = y / columns, unit = (y - block * columns) / (D / 64), t = unit / H_kv, g = unit - t * H_kv;
+    const int at = block * 32 + lane, d0 = y % (D / 64) * 64;
     const SharedTile tile = a.plan->tile[t];
     const long long start = a.plan->start[t];
-    const int i = at / kRows, r = at % kRows, tt = r / G, seq = i * a.tok + tt;
-    if (tt >= a.tok || seq >= tile.seqs) continue;
-    float m = -INFINITY, l = 0.f, o[PER];
-#pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = 0.f;
-    // states from `p` on, `step` floats apart (odd ones another `odd`); columns `col` floats apart
-    auto add = [&](const float* p, int64_t step, int odd, int pieces, int64_t col) {
-      for (int w0 = 0; w0 < pieces; w0 += AHEAD) {
-        float mv[AHEAD], lv[AHEAD], v[AHEAD][PER], top = m;
-#pragma unroll
-        for (int w = 0; w < AHEAD; ++w) {
-          const bool in = w0 + w < pieces;
-          const float* const s = odd ? p + ((w0 + w) >> 1) * step + (w & 1) * odd : p + (w0 + w) * step;
-          mv[w] = in ? __ldcg(s + D * col) : -INFINITY;
-          lv[w] = in ? __ldcg(s + (D + 1) * col) : 0.f;
-#pragma unroll
-          for (int e = 0; e < PER; ++e) v[w][e] = in ? __ldcg(s + (d + e) * col) : 0.f;
-        }
-#pragma unroll
-        for (int w = 0; w < AHEAD; ++w) top = fmaxf(top, mv[w]);
-        const bool none = m == -INFINITY && l == 0.f;
-        const float f = none ? 0.f : ex2((m - top) * c);
-        l = none ? 0.f : l * f;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) o[e] = none ? 0.f : o[e] * f;
-#pragma unroll
-        for (int w = 0; w < AHEAD; ++w) {
-          if (mv[w] == -INFINITY && lv[w] == 0.f) continue;  // saw only scores of -infinity, or nothing
-          const float fw = ex2((mv[w] - top) * c);
-          l = fmaf(fw, lv[w], l);
-#pragma unroll
-          for (int e = 0; e < PER; ++e) o[e] = fmaf(fw, v[w][e], o[e]);
-        }
-        m = top;
-      }
+    const int i = at / kRows;
+    // the row at place x of the block: its sequence of the tile, -1 for none, and head of the group
+    auto seq_of = [&](int x, int& hh) {
+      const int r = (block * 32 + x) % kRows, tt = r / G, seq = i * a.tok + tt;
+      hh = r - tt * G;
+      return tt < a.tok && seq < tile.seqs ? seq : -1;
     };
-    const int nb = (tile.n + kKeys - 1) / kKeys;
-    const long long begin = start + (long long)g * nb;
-    const int first = shared.holder(begin), pieces = shared.holder(begin + nb - 1) - first + 1;
-    // (a tile of one half has two states of each row in a piece)
-    const bool both = tile.seqs <= a.tok;
-    add(a.states + int64_t(first + unit) * (kTileRows * (D + 2)) + at, kTileRows * (D + 2), both ? kRows : 0, both ? 2 * pieces : pieces, kTileRows);
-    const int b = tile.b0 + seq, hh = r - tt * G;
-    const long long nt = ln.pre[b + 1] - ln.pre[b], b0 = ln.pre[b] * H_kv + g * nt;
-    if (nt > 0) {
-      const int f2 = own.holder(b0), n2 = own.holder(b0 + nt - 1) - f2 + 1;
-      add(a.own.partials + (f2 + int64_t(b) * H_kv + g) * (int64_t(G) * (D + 2)) + hh * (D + 2), int64_t(G) * (D + 2), 0, n2, 1);
+    int hh;
+    const bool valid = seq_of(lane, hh) >= 0;
+    if (!__syncthreads_or(valid)) continue;  // (what an item before left in shared memory has been read)
+    if (valid) {
+      const int nb = (tile.n + kKeys - 1) / kKeys;
+      const long long begin = start + (long long)g * nb;
+      const int first = shared.holder(begin), pieces = shared.holder(begin + nb - 1) - first + 1;
+      // (a tile of one half has two states of each row in a piece)
+      const bool both = tile.seqs <= a.tok;
+      const int n = both ? 2 * pieces : pieces;
+      constexpr int STEP = kTileRows * (D + 2);
+      const float* p = a.states + int64_t(first + unit) * STEP + at;
+      State st;
+      float o[PER];
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o[e] = 0.f;
+      for (int w0 = 0; w0 < n; w0 += AHEAD) {
+        float mv[AHEAD], lv[AHEAD], f[AHEAD], v[AHEAD][PER];
+#pragma unroll
+        for (int w = 0; w < AHEAD; ++w) {
+          const float* const q = p + (both ? (w >> 1) * STEP + (w & 1) * kRows : w * STEP);
+          const bool in = w0 + w < n;
+          mv[w] = in ? __ldcg(q + D * kTileRows) : -INFINITY;
+          lv[w] = in ? __ldcg(q + (D + 1) * kTileRows) : 0.f;
+#pragma unroll
+          for (int e = 0; e < PER; ++e) v[w][e] = in ? __ldcg(q + (d0 + warp * PER + e) * kTileRows) : 0.f;
+        }
+        p += (both ? AHEAD / 2 : AHEAD) * STEP;
+        const float was = st.take(mv, lv, f, c);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          o[e] = was == 0.f ? 0.f : o[e] * was;
+#pragma unroll
+          for (int w = 0; w < AHEAD; ++w) o[e] = f[w] == 0.f ? o[e] : fmaf(f[w], v[w][e], o[e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o_sh[lane][warp * PER + e] = o[e];
+      if (warp == 0) m_sh[lane] = st.m, l_sh[lane] = st.l;
     }
-    const int64_t row = int64_t(b) * a.own.H_q + g * G + hh;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<float4*>(a.own.out + row * D + d) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-    if (d == 0 && a.own.lse) a.own.lse[row] = (m * c + log2f(l)) * 0.6931471805599453f;
+    __syncthreads();
+    int seq[ROWS], h[ROWS], n[ROWS], most = 0;
+    const float* p[ROWS];
+    State st[ROWS];
+    float2 o[ROWS];
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) {
+      const int x = warp * ROWS + q;
+      seq[q] = seq_of(x, h[q]);
+      n[q] = 0;
+      p[q] = nullptr;
+      if (seq[q] < 0) continue;
+      const int b = tile.b0 + seq[q];
+      const long long own0 = a.plan->own[b], nt = a.plan->own[b + 1] - own0, b0 = own0 * H_kv + g * nt;
+      if (nt > 0) {
+        const int first = own.holder(b0);
+        n[q] = own.holder(b0 + nt - 1) - first + 1;
+        p[q] = a.own.partials + ((first + int64_t(b) * H_kv + g) * G + h[q]) * (D + 2);
+      }
+      most = max(most, n[q]);
+      st[q].m = m_sh[x], st[q].l = l_sh[x];
+      o[q] = make_float2(o_sh[x][2 * lane], o_sh[x][2 * lane + 1]);
+    }
+    constexpr int TWO = 2;  // pieces of each row at a time
+    for (int w0 = 0; w0 < most; w0 += TWO) {
+      float mv[ROWS][TWO], lv[ROWS][TWO];
+      float2 v[ROWS][TWO];
+#pragma unroll
+      for (int q = 0; q < ROWS; ++q)
+#pragma unroll
+        for (int w = 0; w < TWO; ++w) {
+          const bool in = w0 + w < n[q];
+          const float* const z = p[q] + (w0 + w) * int64_t(G) * (D + 2);
+          const float2 ml = in ? __ldcg(reinterpret_cast<const float2*>(z + D)) : make_float2(-INFINITY, 0.f);
+          mv[q][w] = ml.x, lv[q][w] = ml.y;
+          v[q][w] = in ? __ldcg(reinterpret_cast<const float2*>(z + d0) + lane) : make_float2(0.f, 0.f);
+        }
+#pragma unroll
+      for (int q = 0; q < ROWS; ++q) {
+        float f[TWO];
+        const float was = st[q].take(mv[q], lv[q], f, c);
+        o[q].x = was == 0.f ? 0.f : o[q].x * was, o[q].y = was == 0.f ? 0.f : o[q].y * was;
+#pragma unroll
+        for (int w = 0; w < TWO; ++w)
+          if (f[w] != 0.f) o[q].x = fmaf(f[w], v[q][w].x, o[q].x), o[q].y = fmaf(f[w], v[q][w].y, o[q].y);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) {
+      if (seq[q] < 0) continue;
+      const int64_t row = int64_t(tile.b0 + seq[q]) * a.own.H_q + g * G + h[q];
+      const float inv = st[q].l == 0.f ? 0.f : 1.f / st[q].l;
+      reinterpret_cast<float2*>(a.own.out + row * D + d0)[lane] = make_float2(o[q].x * inv, o[q].y * inv);
+      if (d0 == 0 && lane == 0 && a.own.lse) a.own.lse[row] = (st[q].m * c + log2f(st[q].l)) * 0.6931471805599453f;
+    }
   }
+  if (!alone) return;
+  scan_lengths<kOwnTile>(geo, ln, false);
+  const int nx = gridDim.x / ny;
+  if (int(blockIdx.x) < nx * ny) join_units<kOwnTile, D>(a.own, ln, own, true, blockIdx.x % nx, nx, blockIdx.x / nx, ny);
 }
 
 template <int D, bool TMA>
@@ -731,11 +827,12 @@ cudaError_t launch_shared(const SharedArgs& a, bool own_tma, int grid, cudaStrea
   if (e != cudaSuccess) return e;
   if ((e = launch_pdl(shared_attn_kernel<D, TMA>, dim3(grid), kSharedThreads, SCfg<D>::SMEM, st, a)) != cudaSuccess) return e;
   if ((e = launch_paged_pieces(a.own, D, own_tma, grid, st)) != cudaSuccess) return e;
-  const int units = a.own.geo.B * a.own.geo.H_kv, most = 4 * grid, y = a.own.G * (D / 32);
-  const int nx = units < most ? units : most, ny = units >= most ? 1 : most / units < y ? most / units : y;
-  const long long blocks = (long long)a.max_tiles * a.own.geo.H_kv * kJoinBlocks<D>;
-  const int tile_ctas = int(blocks < 2 * most ? blocks : 2 * most);
-  return launch_pdl(shared_join_kernel<D>, dim3(tile_ctas + nx * ny), kThreads, 0, st, a, grid, tile_ctas, ny);
+  // CTAs for the items that there may be, and for 32 outputs of a unit each, up to four to an SM
+  const long long most = 4LL * grid, units = (long long)a.own.geo.B * a.own.geo.H_kv, y = a.own.G * (D / 32);
+  const long long items = (long long)a.max_tiles * a.own.geo.H_kv * kJoinBlocks<D>, pieces = units * y;
+  const int ctas = int(items < most && pieces < most ? (items < pieces ? pieces : items) : most);
+  const int ny = int(units >= ctas ? 1 : ctas / units < y ? ctas / units : y);
+  return launch_pdl(shared_join_kernel<D>, dim3(ctas), kThreads, 0, st, a, grid, ny);
 }
 
 }  // namespace

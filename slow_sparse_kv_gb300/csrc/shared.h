@@ -21,6 +21,7 @@ struct SharedPlan {
   int32_t n_tiles;
   int32_t alone;    // != 0: some sequence shares nothing
   long long total;  // key blocks of all KV heads in all tiles
+  long long own[kMaxBatch + 1];  // tiles of a KV head in the own positions of the sequences before each
   long long start[kMaxTiles + 1];  // key blocks of all KV heads in the tiles before each
   SharedTile tile[kMaxTiles];
 };
