@@ -45,8 +45,8 @@ constexpr int kRegions = 3, kRegion = 80, kSums = 256;
 constexpr int kTerms = 3;            // bf16 terms of P
 constexpr int kChain = 4;            // blocks of a half whose products with V are added in tensor memory
 constexpr float kGrow = 8.0f;        // growth of the maximum (log2) that moves m
-template <int D>
-constexpr int kJoinBlocks = kTileRows / 32 * (D / 64);  // CTAs' worth of a tile and KV head in the join
+constexpr int kJoinCols = 16;        // columns of an item of the join
+constexpr int kJoinCtas = 2;         // its CTAs on an SM
 constexpr int kOwnTile = 16;         // positions of a tile of paged_attn.cu's kernel in bf16
 
 template <int D>
@@ -664,12 +664,14 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
 }
 
 // ---- the join
-// Items of 32 rows of a tile and 64 columns: first the states of the shared part in the line's
-// order, a lane a row and a warp 8 columns, as these states lie; then, through shared memory,
-// those of the sequences' own positions, a lane two columns and a warp 4 rows, as those do
-// (with a lane a row there too, each read touched 32 lines: 25 us where it is 10 now).  Then
-// the pieces of sequences that share nothing.  Bound by latency, a few dependent reads from L2, so
-// nothing is computed again that the first kernel could leave.
+// Items of 32 rows of a tile and 16 columns.  First the states of the shared part, a lane a row,
+// as these states lie, and the pieces dealt over the warps; then, through shared memory, the
+// warps' states and those of the sequences' own positions, 8 lanes a row, as those lie.  Then
+// the pieces of sequences that share nothing.
+// Bound by latency: a few dependent reads from L2, about 1000 clocks each, so reads that do
+// not depend on one another are issued together, and nothing is computed again that the first
+// kernel could leave.  (All pieces by each warp, 8 columns of 64 each, and a lane a row for the own
+// positions too, where each read touches 32 lines: 25 us for 256 rows of 20 pieces.)
 struct State {
   float m = -INFINITY, l = 0.f;
   // Takes in N states; returns the factors of what it was and of theirs.
@@ -692,129 +694,119 @@ struct State {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) shared_join_kernel(const __grid_constant__ SharedArgs a, int grid, int ny) {
-  constexpr int PER = 8, AHEAD = 4;  // columns of a thread; states read at a time
-  constexpr int ROWS = 32 / kWarps;  // of a warp, of the own positions
+__global__ void __launch_bounds__(kThreads, kJoinCtas) shared_join_kernel(const __grid_constant__ SharedArgs a, int grid, int ny) {
+  constexpr int AHEAD = 3, OWN = 4;  // states that a thread reads at a time
+  constexpr int STEP = kTileRows * (D + 2);
   __shared__ Line ln;
-  __shared__ float o_sh[32][66], m_sh[32], l_sh[32];
+  __shared__ float o_sh[kWarps][kJoinCols][33], ml_sh[kWarps][2][32];
   const PagedGeo& geo = a.own.geo;
-  const int H_kv = geo.H_kv, G = a.own.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int H_kv = geo.H_kv, G = a.own.G, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float c = a.own.scale_log2;
   pdl_launch();
   pdl_wait();
   const int n_tiles = a.plan->n_tiles, alone = a.plan->alone;
   const Cut shared(a.plan->total, grid, 1), own(a.plan->own[geo.B] * H_kv, grid * kPagedWarps, 1);
   // (32-row blocks that all tiles have first: they are spread over the SMs)
-  const int columns = n_tiles * H_kv * (D / 64), items = columns * (kTileRows / 32);
+  const int columns = n_tiles * H_kv * (D / kJoinCols), items = columns * (kTileRows / 32);
   for (int y = blockIdx.x; y < items; y += gridDim.x) {
-    const int block = y / columns, unit = (y - block * columns) / (D / 64), t = unit / H_kv, g = unit - t * H_kv;
-    const int at = block * 32 + lane, d0 = y % (D / 64) * 64;
+    const int block = y / columns, in = y - block * columns, unit = in / (D / kJoinCols), t = unit / H_kv, g = unit - t * H_kv;
+    const int d0 = in % (D / kJoinCols) * kJoinCols;
     const SharedTile tile = a.plan->tile[t];
     const long long start = a.plan->start[t];
-    const int i = at / kRows;
+    const int half = block * 32 / kRows;
     // the row at place x of the block: its sequence of the tile, -1 for none, and head of the group
-    auto seq_of = [&](int x, int& hh) {
-      const int r = (block * 32 + x) % kRows, tt = r / G, seq = i * a.tok + tt;
-      hh = r - tt * G;
+    auto seq_of = [&](int x, int& head) {
+      const int r = (block * 32 + x) % kRows, tt = r / G, seq = half * a.tok + tt;
+      head = r - tt * G;
       return tt < a.tok && seq < tile.seqs ? seq : -1;
     };
-    int hh;
-    const bool valid = seq_of(lane, hh) >= 0;
-    if (!__syncthreads_or(valid)) continue;  // (what an item before left in shared memory has been read)
-    if (valid) {
+    int head;
+    const bool valid = seq_of(lane, head) >= 0;
+    if (!__syncthreads_or(valid)) continue;  // (and what an item before left in shared memory has been read)
+    // whose row this thread writes, and where its own positions lie in their line
+    const int seq = seq_of(tid >> 3, head), b = tile.b0 + max(seq, 0);
+    const long long own0 = a.plan->own[b], own1 = a.plan->own[b + 1];
+    {
       const int nb = (tile.n + kKeys - 1) / kKeys;
       const long long begin = start + (long long)g * nb;
       const int first = shared.holder(begin), pieces = shared.holder(begin + nb - 1) - first + 1;
       // (a tile of one half has two states of each row in a piece)
       const bool both = tile.seqs <= a.tok;
-      const int n = both ? 2 * pieces : pieces;
-      constexpr int STEP = kTileRows * (D + 2);
-      const float* p = a.states + int64_t(first + unit) * STEP + at;
+      const int n = valid ? both ? 2 * pieces : pieces : 0;
+      const float* const p = a.states + int64_t(first + unit) * STEP + block * 32 + lane;
       State st;
-      float o[PER];
+      float o[kJoinCols];
 #pragma unroll
-      for (int e = 0; e < PER; ++e) o[e] = 0.f;
-      for (int w0 = 0; w0 < n; w0 += AHEAD) {
-        float mv[AHEAD], lv[AHEAD], f[AHEAD], v[AHEAD][PER];
+      for (int e = 0; e < kJoinCols; ++e) o[e] = 0.f;
+#pragma unroll 1
+      for (int w0 = warp; w0 < n; w0 += AHEAD * kWarps) {
+        float mv[AHEAD], lv[AHEAD], f[AHEAD], v[AHEAD][kJoinCols];
 #pragma unroll
-        for (int w = 0; w < AHEAD; ++w) {
-          const float* const q = p + (both ? (w >> 1) * STEP + (w & 1) * kRows : w * STEP);
-          const bool in = w0 + w < n;
-          mv[w] = in ? __ldcg(q + D * kTileRows) : -INFINITY;
-          lv[w] = in ? __ldcg(q + (D + 1) * kTileRows) : 0.f;
+        for (int k = 0; k < AHEAD; ++k) {
+          const int w = w0 + k * kWarps;
+          const float* const q = p + (both ? int64_t(w >> 1) * STEP + (w & 1) * kRows : int64_t(w) * STEP);
+          const bool there = w < n;
+          mv[k] = there ? __ldcg(q + D * kTileRows) : -INFINITY;
+          lv[k] = there ? __ldcg(q + (D + 1) * kTileRows) : 0.f;
 #pragma unroll
-          for (int e = 0; e < PER; ++e) v[w][e] = in ? __ldcg(q + (d0 + warp * PER + e) * kTileRows) : 0.f;
+          for (int e = 0; e < kJoinCols; ++e) v[k][e] = there ? __ldcg(q + (d0 + e) * kTileRows) : 0.f;
         }
-        p += (both ? AHEAD / 2 : AHEAD) * STEP;
         const float was = st.take(mv, lv, f, c);
 #pragma unroll
-        for (int e = 0; e < PER; ++e) {
+        for (int e = 0; e < kJoinCols; ++e) {
           o[e] = was == 0.f ? 0.f : o[e] * was;
 #pragma unroll
-          for (int w = 0; w < AHEAD; ++w) o[e] = f[w] == 0.f ? o[e] : fmaf(f[w], v[w][e], o[e]);
+          for (int k = 0; k < AHEAD; ++k) o[e] = f[k] == 0.f ? o[e] : fmaf(f[k], v[k][e], o[e]);
         }
       }
 #pragma unroll
-      for (int e = 0; e < PER; ++e) o_sh[lane][warp * PER + e] = o[e];
-      if (warp == 0) m_sh[lane] = st.m, l_sh[lane] = st.l;
+      for (int e = 0; e < kJoinCols; ++e) o_sh[warp][e][lane] = o[e];
+      ml_sh[warp][0][lane] = st.m, ml_sh[warp][1][lane] = st.l;
     }
     __syncthreads();
-    int seq[ROWS], h[ROWS], n[ROWS], most = 0;
-    const float* p[ROWS];
-    State st[ROWS];
-    float2 o[ROWS];
+    if (seq < 0) continue;
+    const int row = tid >> 3, col = 2 * (tid & 7);
+    State st;
+    float2 o = make_float2(0.f, 0.f);
+    {
+      float mv[kWarps], lv[kWarps], f[kWarps];
 #pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-      const int x = warp * ROWS + q;
-      seq[q] = seq_of(x, h[q]);
-      n[q] = 0;
-      p[q] = nullptr;
-      if (seq[q] < 0) continue;
-      const int b = tile.b0 + seq[q];
-      const long long own0 = a.plan->own[b], nt = a.plan->own[b + 1] - own0, b0 = own0 * H_kv + g * nt;
-      if (nt > 0) {
-        const int first = own.holder(b0);
-        n[q] = own.holder(b0 + nt - 1) - first + 1;
-        p[q] = a.own.partials + ((first + int64_t(b) * H_kv + g) * G + h[q]) * (D + 2);
-      }
-      most = max(most, n[q]);
-      st[q].m = m_sh[x], st[q].l = l_sh[x];
-      o[q] = make_float2(o_sh[x][2 * lane], o_sh[x][2 * lane + 1]);
+      for (int w = 0; w < kWarps; ++w) mv[w] = ml_sh[w][0][row], lv[w] = ml_sh[w][1][row];
+      st.take(mv, lv, f, c);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        if (f[w] != 0.f) o.x = fmaf(f[w], o_sh[w][col][row], o.x), o.y = fmaf(f[w], o_sh[w][col + 1][row], o.y);
     }
-    constexpr int TWO = 2;  // pieces of each row at a time
-    for (int w0 = 0; w0 < most; w0 += TWO) {
-      float mv[ROWS][TWO], lv[ROWS][TWO];
-      float2 v[ROWS][TWO];
+    const long long nt = own1 - own0, o0 = own0 * H_kv + g * nt;
+    if (nt > 0) {
+      const int first = own.holder(o0), n = own.holder(o0 + nt - 1) - first + 1;
+      const float* p = a.own.partials + ((first + int64_t(b) * H_kv + g) * G + head) * (D + 2);
+      const int64_t step = int64_t(G) * (D + 2);
+#pragma unroll 1
+      for (int w0 = 0; w0 < n; w0 += OWN, p += OWN * step) {
+        float mv[OWN], lv[OWN], f[OWN];
+        float2 v[OWN];
 #pragma unroll
-      for (int q = 0; q < ROWS; ++q)
-#pragma unroll
-        for (int w = 0; w < TWO; ++w) {
-          const bool in = w0 + w < n[q];
-          const float* const z = p[q] + (w0 + w) * int64_t(G) * (D + 2);
-          const float2 ml = in ? __ldcg(reinterpret_cast<const float2*>(z + D)) : make_float2(-INFINITY, 0.f);
-          mv[q][w] = ml.x, lv[q][w] = ml.y;
-          v[q][w] = in ? __ldcg(reinterpret_cast<const float2*>(z + d0) + lane) : make_float2(0.f, 0.f);
+        for (int k = 0; k < OWN; ++k) {
+          const bool there = w0 + k < n;
+          const float2 ml = there ? __ldcg(reinterpret_cast<const float2*>(p + k * step + D)) : make_float2(-INFINITY, 0.f);
+          mv[k] = ml.x, lv[k] = ml.y;
+          v[k] = there ? __ldcg(reinterpret_cast<const float2*>(p + k * step + d0 + col)) : make_float2(0.f, 0.f);
         }
+        const float was = st.take(mv, lv, f, c);
+        o.x = was == 0.f ? 0.f : o.x * was, o.y = was == 0.f ? 0.f : o.y * was;
 #pragma unroll
-      for (int q = 0; q < ROWS; ++q) {
-        float f[TWO];
-        const float was = st[q].take(mv[q], lv[q], f, c);
-        o[q].x = was == 0.f ? 0.f : o[q].x * was, o[q].y = was == 0.f ? 0.f : o[q].y * was;
-#pragma unroll
-        for (int w = 0; w < TWO; ++w)
-          if (f[w] != 0.f) o[q].x = fmaf(f[w], v[q][w].x, o[q].x), o[q].y = fmaf(f[w], v[q][w].y, o[q].y);
+        for (int k = 0; k < OWN; ++k)
+          if (f[k] != 0.f) o.x = fmaf(f[k], v[k].x, o.x), o.y = fmaf(f[k], v[k].y, o.y);
       }
     }
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-      if (seq[q] < 0) continue;
-      const int64_t row = int64_t(tile.b0 + seq[q]) * a.own.H_q + g * G + h[q];
-      const float inv = st[q].l == 0.f ? 0.f : 1.f / st[q].l;
-      reinterpret_cast<float2*>(a.own.out + row * D + d0)[lane] = make_float2(o[q].x * inv, o[q].y * inv);
-      if (d0 == 0 && lane == 0 && a.own.lse) a.own.lse[row] = (st[q].m * c + log2f(st[q].l)) * 0.6931471805599453f;
-    }
+    const int64_t to = int64_t(b) * a.own.H_q + g * G + head;
+    const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
+    *reinterpret_cast<float2*>(a.own.out + to * D + d0 + col) = make_float2(o.x * inv, o.y * inv);
+    if (d0 + col == 0 && a.own.lse) a.own.lse[to] = (st.m * c + log2f(st.l)) * 0.6931471805599453f;
   }
   if (!alone) return;
+  __syncthreads();
   scan_lengths<kOwnTile>(geo, ln, false);
   const int nx = gridDim.x / ny;
   if (int(blockIdx.x) < nx * ny) join_units<kOwnTile, D>(a.own, ln, own, true, blockIdx.x % nx, nx, blockIdx.x / nx, ny);
@@ -827,9 +819,10 @@ cudaError_t launch_shared(const SharedArgs& a, bool own_tma, int grid, cudaStrea
   if (e != cudaSuccess) return e;
   if ((e = launch_pdl(shared_attn_kernel<D, TMA>, dim3(grid), kSharedThreads, SCfg<D>::SMEM, st, a)) != cudaSuccess) return e;
   if ((e = launch_paged_pieces(a.own, D, own_tma, grid, st)) != cudaSuccess) return e;
-  // CTAs for the items that there may be, and for 32 outputs of a unit each, up to four to an SM
-  const long long most = 4LL * grid, units = (long long)a.own.geo.B * a.own.geo.H_kv, y = a.own.G * (D / 32);
-  const long long items = (long long)a.max_tiles * a.own.geo.H_kv * kJoinBlocks<D>, pieces = units * y;
+  // CTAs for the items that there may be, or for 32 outputs of a unit each, while all of them
+  // find room at once
+  const long long most = (long long)kJoinCtas * grid, units = (long long)a.own.geo.B * a.own.geo.H_kv, y = a.own.G * (D / 32);
+  const long long items = (long long)a.max_tiles * a.own.geo.H_kv * (kTileRows / 32 * (D / kJoinCols)), pieces = units * y;
   const int ctas = int(items < most && pieces < most ? (items < pieces ? pieces : items) : most);
   const int ny = int(units >= ctas ? 1 : ctas / units < y ? ctas / units : y);
   return launch_pdl(shared_join_kernel<D>, dim3(ctas), kThreads, 0, st, a, grid, ny);
