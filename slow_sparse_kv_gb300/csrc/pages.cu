@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "paged.h"
 #include "pdl.cuh"
 
@@ -446,17 +447,48 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, int b, int m, in
   }
 }
 
-// The largest magnitude of a row's elements, 8 in each of LPH lanes, as its bits (those of
-// an infinity or a NaN are larger than any number's).
-template <int LPH>
-__device__ __forceinline__ uint32_t row_top(const float (&x)[8]) {
-  uint32_t top = 0;
+// 8 elements of a row as they lie in memory.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  float4 v[2];
+  __device__ __forceinline__ void load(const float* p) {
+    v[0] = __ldcs(reinterpret_cast<const float4*>(p)), v[1] = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void clear() { v[0] = v[1] = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = v[0].x, x[1] = v[0].y, x[2] = v[0].z, x[3] = v[0].w, x[4] = v[1].x, x[5] = v[1].y, x[6] = v[1].z, x[7] = v[1].w;
+  }
+  // The largest magnitude over the row's LPH lanes, as its bits (those of an infinity or a NaN are
+  // larger than any number's).
+  template <int LPH>
+  __device__ __forceinline__ uint32_t top() const {
+    float x[8];
+    get(x);
+    uint32_t t = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+    for (int e = 0; e < 8; ++e) t = max(t, __float_as_uint(x[e]) & 0x7fffffffu);
 #pragma unroll
-  for (int w = 1; w < LPH; w <<= 1) top = max(top, __shfl_xor_sync(kFull, top, w));
-  return top;
-}
+    for (int w = 1; w < LPH; w <<= 1) t = max(t, __shfl_xor_sync(kFull, t, w));
+    return t;
+  }
+};
+template <>
+struct Eight<bf16_t> {
+  uint4 v;
+  __device__ __forceinline__ void load(const bf16_t* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&x)[8]) const { Unpack<bf16_t>::run(v, x); }
+  // (two at a time: magnitudes compare as 16-bit numbers)
+  template <int LPH>
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t t = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+#pragma unroll
+    for (int w = 1; w < LPH; w <<= 1) t = __vmaxu2(t, __shfl_xor_sync(kFull, t, w));
+    return max(t & 0xffff0000u, t << 16);
+  }
+};
 
 // Codes of 8 elements of a row whose largest magnitude is `top` (bits), and the row's scale.
 //
@@ -464,10 +496,14 @@ __device__ __forceinline__ uint32_t row_top(const float (&x)[8]) {
 // only next to a tie; e = x - n s is exact in fp32 (a multiple of the smaller of both
 // last places, below s in magnitude), so comparing it with s / 2 decides: half of the maximum
 // is such a tie in every row (63.5), and the rounded quotient would put it on either side.
-// (Rows below 2^-60 are scaled up by 2^80 with their scale, so that nothing underflows.)
+// rint by an addition of 1.5 * 2^23, whose last byte is then the code.
 // e4m3: the scale is a power of two, so x / s is exact and the conversion rounds once.
+// Rows whose maximum lies outside [2^-60, 2^100] take a longer way: there 1 / s or e could leave
+// fp32's normal numbers.
 template <bool E4M3>
-__device__ __forceinline__ uint2 quantise(float (&x)[8], uint32_t top, float* scale) {
+__device__ __noinline__ uint2 quantise_far(float x0, float x1, float x2, float x3, float x4, float x5, float x6, float x7,
+                                           uint32_t top, float* scale) {
+  const float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7};
   if (top >= 0x7f800000u) {
     *scale = __uint_as_float(0x7fc00000u);
     return make_uint2(0, 0);
@@ -475,8 +511,7 @@ __device__ __forceinline__ uint2 quantise(float (&x)[8], uint32_t top, float* sc
   const float amax = __uint_as_float(top);
   uint32_t w[2] = {0, 0};
   if constexpr (E4M3) {
-    // amax = m 2^e, 1 <= m < 2, and 448 = 1.75 * 2^8 (subnormal maxima are scaled up for this)
-    const bool tiny = amax < 0x1p-126f;
+    const bool tiny = amax < 0x1p-126f;  // (scaled up to read its exponent)
     const uint32_t bits = tiny ? __float_as_uint(amax * 0x1p64f) : top;
     const int k = int(bits >> 23) - 127 - (tiny ? 64 : 0) - 8 + ((bits & 0x7fffffu) > 0x600000u);
     const float s = amax == 0.f || k < -149 ? 0.f : k < -126 ? __uint_as_float(1u << (k + 149)) : __uint_as_float(uint32_t(k + 127) << 23);
@@ -484,7 +519,6 @@ __device__ __forceinline__ uint2 quantise(float (&x)[8], uint32_t top, float* sc
     if (s == 0.f) return make_uint2(0, 0);
     const int k0 = -k / 2, k1 = -k - k0;  // (1 / s may be beyond fp32)
     const float f0 = __uint_as_float(uint32_t(k0 + 127) << 23), f1 = __uint_as_float(uint32_t(k1 + 127) << 23);
-#pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint16_t c;
       asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(x[2 * i + 1] * f0 * f1), "f"(x[2 * i] * f0 * f1));
@@ -494,33 +528,65 @@ __device__ __forceinline__ uint2 quantise(float (&x)[8], uint32_t top, float* sc
     float s = amax / 127.f;
     *scale = s;
     if (s == 0.f) return make_uint2(0, 0);
-    const float up = amax < 0x1p-60f ? 0x1p80f : 1.f;
+    const float up = amax < 0x1p-60f ? 0x1p80f : 1.f;  // both sides of the quotient, so that nothing underflows
     s *= up;
     const float inv = 1.f / s, half = 0.5f * s;
-#pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float y = x[i] * up;
       float n = rintf(y * inv);
       const float e = fmaf(-n, s, y);
-      const int odd = int(n) & 1;
-      if (fabsf(e) > half || (fabsf(e) == half && odd)) n += copysignf(1.f, e);
-      n = fminf(fmaxf(n, -127.f), 127.f);
+      if (fabsf(e) > half || (fabsf(e) == half && (int(n) & 1))) n += copysignf(1.f, e);
+      n = fminf(fmaxf(n, -127.f), 127.f);  // (a subnormal scale may be much too small)
       w[i / 4] |= (uint32_t(int(n)) & 0xffu) << (i % 4 * 8);
     }
   }
   return make_uint2(w[0], w[1]);
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<bf16_t>(const bf16_t* p, float (&x)[8]) {
-  Unpack<bf16_t>::run(__ldcs(reinterpret_cast<const uint4*>(p)), x);
+template <bool E4M3>
+__device__ __forceinline__ uint2 quantise(const float (&x)[8], uint32_t top, float* scale) {
+  if (top < 0x21800000u || top > 0x71800000u)  // 2^-60, 2^100
+    return quantise_far<E4M3>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], top, scale);
+  uint32_t w[2];
+  if constexpr (E4M3) {
+    // amax = m 2^e, 1 <= m < 2, and 448 = 1.75 * 2^8: s = 2^k, k = e - 8, or e - 7 where m > 1.75
+    const uint32_t k = (top + 0x1fffffu) >> 23;  // e + 127, + 1
+    *scale = __uint_as_float((k - 8) << 23);
+    const float f = __uint_as_float((254 + 8 - k) << 23);
+    const uint64_t ff = pair(f, f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t p = mul2(pair(x[4 * i], x[4 * i + 1]), ff), q = mul2(pair(x[4 * i + 2], x[4 * i + 3]), ff);
+      asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+          "mov.b32 %0, {l, h};\n\t}"
+          : "=r"(w[i])
+          : "f"(lo(p)), "f"(hi(p)), "f"(lo(q)), "f"(hi(q)));
+    }
+  } else {
+    constexpr float BIG = 12582912.f;
+    const float s = __uint_as_float(top) / 127.f, inv = 1.f / s, half = 0.5f * s;
+    *scale = s;
+    float t[8], worst = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t p = pair(x[2 * i], x[2 * i + 1]), z = fma2(p, pair(inv, inv), pair(BIG, BIG));
+      const uint64_t n = add2(z, pair(-BIG, -BIG)), e = fma2(n, pair(-s, -s), p);
+      t[2 * i] = lo(z), t[2 * i + 1] = hi(z);
+      worst = fmaxf(worst, fmaxf(fabsf(lo(e)), fabsf(hi(e))));
+    }
+    if (worst >= half) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float n = t[i] - BIG, e = fmaf(-n, s, x[i]);
+        if (fabsf(e) > half || (fabsf(e) == half && (__float_as_uint(t[i]) & 1))) t[i] += copysignf(1.f, e);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      w[i] = __byte_perm(__byte_perm(__float_as_uint(t[4 * i]), __float_as_uint(t[4 * i + 1]), 0x0040),
+                         __byte_perm(__float_as_uint(t[4 * i + 2]), __float_as_uint(t[4 * i + 3]), 0x0040), 0x5410);
+  }
+  return make_uint2(w[0], w[1]);
 }
 
 // A token's rows into an 8-bit pool: d / 8 lanes a head, K and V of `AHEAD` heads read at once.
@@ -529,7 +595,7 @@ struct Quant : QuantArgs {};
 
 template <typename T, bool E4M3, int D>
 __device__ __forceinline__ void append_row(const Quant<T, E4M3, D>& a, int b, int m, int back, int t, int cap, int lane) {
-  constexpr int LPH = D / 8, HPW = 32 / LPH, AHEAD = sizeof(T) == 4 ? 1 : 2;
+  constexpr int LPH = D / 8, HPW = 32 / LPH, AHEAD = 2;
   const PagedGeo& g = a.geo;
   const int n = g.len[b];
   const uint32_t refused = g.refused[b >> 5] >> (b & 31) & 1;
@@ -546,26 +612,23 @@ __device__ __forceinline__ void append_row(const Quant<T, E4M3, D>& a, int b, in
   uint8_t* const dst[2] = {a.k + at, a.v + at};
   const int in = pos % g.P, u = lane % LPH;
   for (int h0 = lane / LPH; h0 - lane / LPH < g.H_kv; h0 += AHEAD * HPW) {
-    float x[AHEAD][2][8];
+    Eight<T> r[AHEAD][2];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int h = h0 + i * HPW;
-        if (h < g.H_kv) {
-          load8<T>(src[y] + h * D + u * 8, x[i][y]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[i][y][e] = 0.f;
-        }
+        if (h < g.H_kv) r[i][y].load(src[y] + h * D + u * 8);
+        else r[i][y].clear();
       }
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const uint32_t top = row_top<LPH>(x[i][y]);
-        float scale;
-        const uint2 codes = quantise<E4M3>(x[i][y], top, &scale);
+        const uint32_t top = r[i][y].template top<LPH>();
+        float x[8], scale;
+        r[i][y].get(x);
+        const uint2 codes = quantise<E4M3>(x, top, &scale);
         const int h = h0 + i * HPW;
         if (h >= g.H_kv) continue;
         const int64_t row = int64_t(h) * g.P + in;

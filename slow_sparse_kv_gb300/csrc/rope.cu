@@ -14,10 +14,13 @@
 // A lane holds 4 + 4 elements of a head, both sides of its four pairs, so that nothing is
 // exchanged but the sum of squares (d / 8 lanes a head), and reads and writes the same
 // places, so that a call may work in place.  A row's warp computes its four angles once
-// for all heads.  Bound by HBM: every row is read and written once.
+// for all heads, and once for its query and its key heads the products of weight and cosine
+// or sine, so that a head costs a rotation and a factor: with the weights read and applied head by
+// head the instructions took longer than HBM, 67 us for 16384 rows of 32 + 8 heads of 128.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "pdl.cuh"
 #include "rope.h"
 
@@ -25,7 +28,7 @@ namespace sfi {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;  // heads that a lane reads ahead
+constexpr int kAhead = 4;  // steps that a lane reads ahead
 
 // Four elements as they lie in memory.
 template <typename T>
@@ -46,7 +49,26 @@ struct Quad<bf16_t> {
   __device__ __forceinline__ void set(const float (&x)[4]) { v = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])); }
 };
 
-template <typename T, int D, bool NEXT>
+// A lane's two quads as the first and the second elements of its four pairs, two pairs to a
+// register, and back.
+template <bool NEXT>
+__device__ __forceinline__ void to_pairs(const float (&x)[4], const float (&y)[4], uint64_t (&u)[2], uint64_t (&v)[2]) {
+  u[0] = NEXT ? pair(x[0], x[2]) : pair(x[0], x[1]), u[1] = NEXT ? pair(y[0], y[2]) : pair(x[2], x[3]);
+  v[0] = NEXT ? pair(x[1], x[3]) : pair(y[0], y[1]), v[1] = NEXT ? pair(y[1], y[3]) : pair(y[2], y[3]);
+}
+template <bool NEXT>
+__device__ __forceinline__ void from_pairs(const uint64_t (&u)[2], const uint64_t (&v)[2], float (&x)[4], float (&y)[4]) {
+  if (NEXT) {
+    x[0] = lo(u[0]), x[2] = hi(u[0]), y[0] = lo(u[1]), y[2] = hi(u[1]);
+    x[1] = lo(v[0]), x[3] = hi(v[0]), y[1] = lo(v[1]), y[3] = hi(v[1]);
+  } else {
+    x[0] = lo(u[0]), x[1] = hi(u[0]), x[2] = lo(u[1]), x[3] = hi(u[1]);
+    y[0] = lo(v[0]), y[1] = hi(v[0]), y[2] = lo(v[1]), y[3] = hi(v[1]);
+  }
+}
+
+// FULL: all d dimensions are rotated.
+template <typename T, int D, bool NEXT, bool FULL>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LPH = D / 8;        // lanes of a head
   constexpr int HPW = 32 / LPH;     // heads of a warp at a time
@@ -61,8 +83,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   // (several parts only where there are few items)
   const int row = a.parts == 1 ? int(item) : int(uint32_t(item) / uint32_t(a.parts)), part = a.parts == 1 ? 0 : int(item) - row * a.parts;
   // the lane's elements: at and at + 4 .., or both sides of pairs that lie rot / 2 apart
-  const bool turns = u < a.rot / 8;
-  const int at0 = turns && !NEXT ? 4 * u : 8 * u, at1 = turns && !NEXT ? a.rot / 2 + 4 * u : 8 * u + 4;
+  const bool turns = FULL || u < a.rot / 8;
+  const int at0 = turns && !NEXT ? 4 * u : 8 * u, at1 = turns && !NEXT ? (FULL ? D / 2 : a.rot / 2) + 4 * u : 8 * u + 4;
   float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
   if (turns) {
     const int64_t pos = int64_t(a.pos[row]) + a.pos_offset;
@@ -72,94 +94,105 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       sincospif(float(turn) * 0x1p-31f, &s[e], &c[e]);
     }
   }
-  const int heads = a.H_q + a.H_kv;
-  const int steps = (heads + HPW - 1) / HPW, from = steps * part / a.parts, to = steps * (part + 1) / a.parts;
-  const T* const q = static_cast<const T*>(a.q) + int64_t(row) * a.q_stride;
-  const T* const k = static_cast<const T*>(a.k) + int64_t(row) * a.k_stride;
-  T* const qo = static_cast<T*>(a.q_out) + int64_t(row) * a.q_out_stride;
-  T* const ko = static_cast<T*>(a.k_out) + int64_t(row) * a.k_out_stride;
-  for (int i0 = from; i0 < to; i0 += kAhead) {
-    Quad<T> x0[kAhead], x1[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int h = (i0 + j) * HPW + lane / LPH;
-      if (i0 + j >= to || h >= heads) continue;
-      const T* const x = h < a.H_q ? q + h * D : k + (h - a.H_q) * D;
-      x0[j] = *reinterpret_cast<const Quad<T>*>(x + at0);
-      x1[j] = *reinterpret_cast<const Quad<T>*>(x + at1);
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int h = (i0 + j) * HPW + lane / LPH;
-      if (i0 + j >= to) break;
-      const bool there = h < heads, is_q = h < a.H_q;
-      float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-      if (there) x0[j].get(x), x1[j].get(y);
-      if (a.norm) {
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum = fmaf(x[e], x[e], fmaf(y[e], y[e], sum));
-#pragma unroll
-        for (int w = 1; w < LPH; w <<= 1) sum += __shfl_xor_sync(kFull, sum, w);
-        const float r = rsqrtf(sum * (1.f / D) + a.eps);
-        const T* const w = static_cast<const T*>(is_q ? a.wq : a.wk);
-        float w0[4] = {1.f, 1.f, 1.f, 1.f}, w1[4] = {1.f, 1.f, 1.f, 1.f};
-        if (w) {
-          reinterpret_cast<const Quad<T>*>(w + at0)->get(w0);
-          reinterpret_cast<const Quad<T>*>(w + at1)->get(w1);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] *= r * w0[e], y[e] *= r * w1[e];
+  // steps of HPW heads: those of q, then those of k
+  const int q_steps = (a.H_q + HPW - 1) / HPW, steps = q_steps + (a.H_kv + HPW - 1) / HPW;
+  const int from = steps * part / a.parts, to = steps * (part + 1) / a.parts;
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int begin = max(from - (which ? q_steps : 0), 0), end = min(to, which ? steps : q_steps) - (which ? q_steps : 0);
+    if (begin >= end) continue;
+    const int heads = which ? a.H_kv : a.H_q;
+    const T* const src = static_cast<const T*>(which ? a.k : a.q) + int64_t(row) * (which ? a.k_stride : a.q_stride);
+    T* const dst = static_cast<T*>(which ? a.k_out : a.q_out) + int64_t(row) * (which ? a.k_out_stride : a.q_out_stride);
+    // first = x wc - y ws', second = x ws + y wc' for a pair (x, y) of weights (w, w')
+    uint64_t wc[2], ws[2], vc[2], vs[2];
+    {
+      float w0[4] = {1.f, 1.f, 1.f, 1.f}, w1[4] = {1.f, 1.f, 1.f, 1.f};
+      const T* const w = static_cast<const T*>(which ? a.wk : a.wq);
+      if (w) {
+        reinterpret_cast<const Quad<T>*>(w + at0)->get(w0);
+        reinterpret_cast<const Quad<T>*>(w + at1)->get(w1);
       }
-      float p[4], o[4];
-      if (NEXT) {
+      uint64_t wu[2], wv[2];
+      to_pairs<NEXT>(w0, w1, wu, wv);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint64_t ce = pair(c[2 * e], c[2 * e + 1]), se = pair(s[2 * e], s[2 * e + 1]);
+        wc[e] = mul2(wu[e], ce), ws[e] = mul2(wu[e], se);
+        vc[e] = mul2(wv[e], ce), vs[e] = mul2(wv[e], pair(-s[2 * e], -s[2 * e + 1]));
+      }
+    }
+    const int head0 = lane / LPH;
+#pragma unroll 1
+    for (int i0 = begin; i0 < end; i0 += kAhead) {
+      Quad<T> x0[kAhead], x1[kAhead];
+      const int first = i0 * HPW + head0, n = min(end - i0, kAhead);
+      const T* const x = src + first * D;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (j < n && first + j * HPW < heads) {
+          x0[j] = *reinterpret_cast<const Quad<T>*>(x + j * HPW * D + at0);
+          x1[j] = *reinterpret_cast<const Quad<T>*>(x + j * HPW * D + at1);
+        }
+      T* const y = dst + first * D;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (j >= n) break;
+        float p[4], o[4];
+        x0[j].get(p), x1[j].get(o);
+        uint64_t xu[2], xv[2], yu[2], yv[2];
+        to_pairs<NEXT>(p, o, xu, xv);
+        uint64_t rr = pair(1.f, 1.f);
+        if (a.norm) {
+          const uint64_t q = fma2(xu[0], xu[0], fma2(xu[1], xu[1], fma2(xv[0], xv[0], mul2(xv[1], xv[1]))));
+          float sum = lo(q) + hi(q);
+#pragma unroll
+          for (int w = 1; w < LPH; w <<= 1) sum += __shfl_xor_sync(kFull, sum, w);
+          const float r = rsqrtf(sum * (1.f / D) + a.eps);
+          rr = pair(r, r);
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          p[2 * e] = x[2 * e] * c[e] - x[2 * e + 1] * s[e];
-          p[2 * e + 1] = x[2 * e] * s[e] + x[2 * e + 1] * c[e];
-          o[2 * e] = y[2 * e] * c[2 + e] - y[2 * e + 1] * s[2 + e];
-          o[2 * e + 1] = y[2 * e] * s[2 + e] + y[2 * e + 1] * c[2 + e];
+          yu[e] = mul2(fma2(xu[e], wc[e], mul2(xv[e], vs[e])), rr);
+          yv[e] = mul2(fma2(xu[e], ws[e], mul2(xv[e], vc[e])), rr);
+          // (what is not rotated stays as it is, infinities among it)
+          if (!FULL && !turns) yu[e] = mul2(mul2(xu[e], wc[e]), rr), yv[e] = mul2(mul2(xv[e], vc[e]), rr);
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] = x[e] * c[e] - y[e] * s[e];
-          o[e] = x[e] * s[e] + y[e] * c[e];
-        }
+        if (first + j * HPW >= heads) continue;
+        from_pairs<NEXT>(yu, yv, p, o);
+        Quad<T> v0, v1;
+        v0.set(p), v1.set(o);
+        *reinterpret_cast<Quad<T>*>(y + j * HPW * D + at0) = v0;
+        *reinterpret_cast<Quad<T>*>(y + j * HPW * D + at1) = v1;
       }
-      // (what is not rotated stays as it is, infinities among it)
-      if (!turns) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = x[e], o[e] = y[e];
-      }
-      if (!there) continue;
-      T* const to_ = is_q ? qo + h * D : ko + (h - a.H_q) * D;
-      Quad<T> v0, v1;
-      v0.set(p), v1.set(o);
-      *reinterpret_cast<Quad<T>*>(to_ + at0) = v0;
-      *reinterpret_cast<Quad<T>*>(to_ + at1) = v1;
     }
   }
 }
 
-template <typename T, int D>
-cudaError_t launch_t(RopeArgs a, bool next, cudaStream_t st) {
+template <typename T, int D, bool NEXT>
+cudaError_t launch_t(RopeArgs a, cudaStream_t st) {
   // rows in abundance: a warp for each, which computes the angles once; few: their
   // heads over several warps
-  const int steps = (a.H_q + a.H_kv + 256 / D - 1) / (256 / D);
+  constexpr int HPW = 256 / D;
+  const int steps = (a.H_q + HPW - 1) / HPW + (a.H_kv + HPW - 1) / HPW;
   const long long want = 16LL * device_sm_count();
   a.parts = int(want / a.total < 1 ? 1 : want / a.total < steps ? want / a.total : steps);
   const long long items = (long long)a.total * a.parts;
   const dim3 grid(unsigned((items + kThreads / 32 - 1) / (kThreads / 32)));
-  return next ? launch_pdl(rope_kernel<T, D, true>, grid, kThreads, 0, st, a)
-              : launch_pdl(rope_kernel<T, D, false>, grid, kThreads, 0, st, a);
+  return a.rot == D ? launch_pdl(rope_kernel<T, D, NEXT, true>, grid, kThreads, 0, st, a)
+                    : launch_pdl(rope_kernel<T, D, NEXT, false>, grid, kThreads, 0, st, a);
+}
+
+template <typename T>
+cudaError_t launch_d(const RopeArgs& a, int D, bool next, cudaStream_t st) {
+  if (D == 64) return next ? launch_t<T, 64, true>(a, st) : launch_t<T, 64, false>(a, st);
+  return next ? launch_t<T, 128, true>(a, st) : launch_t<T, 128, false>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, int D, bool f32, bool next, cudaStream_t st) {
-  if (D == 64) return f32 ? launch_t<float, 64>(a, next, st) : launch_t<bf16_t, 64>(a, next, st);
-  return f32 ? launch_t<float, 128>(a, next, st) : launch_t<bf16_t, 128>(a, next, st);
+  return f32 ? launch_d<float>(a, D, next, st) : launch_d<bf16_t>(a, D, next, st);
 }
 
 }  // namespace sfi
