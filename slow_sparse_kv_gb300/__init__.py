@@ -341,6 +341,16 @@ def _want(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: 
     return t
 
 
+def _rows(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device) -> int:
+    """Refuse a tensor that is not rows of dense heads, as _want does; the rows' distance, 0 where
+    there is no second one."""
+    st = t.stride()
+    if (t.dtype is not dtype or t.shape != shape or t.device != device or len(st) != 3 or st[2] != 1 or st[1] != shape[2]
+            or (shape[0] > 1 and st[0] < shape[1] * shape[2])):
+        _want(name, t, shape, dtype, device, True)  # (which says what is wrong, if anything is)
+    return st[0] if shape[0] > 1 else 0
+
+
 def _device_of(name: str, t: torch.Tensor) -> torch.device:
     if not t.is_cuda:
         raise ValueError(f"{name}: libsfi takes device tensors")
@@ -603,13 +613,11 @@ def sfi_paged_append_q8(layout: PagedLayout, k_new, v_new, k, v, cu_new=None, ws
     _here(L.device, stream)
     new = (k_new.shape[0], L.n_kv_heads, L.head_dim)
     code = _rows_code("k_new", k_new)
-    _want("k_new", k_new, new, k_new.dtype, L.device, True)
-    _want("v_new", v_new, new, k_new.dtype, L.device, True)
+    ks, vs = (_rows(name, x, new, k_new.dtype, L.device) for name, x in (("k_new", k_new), ("v_new", v_new)))
     L._pool("k", k)
     L._pool("v", v)
     if cu_new is not None:
         _want("cu_new", cu_new, (L.B + 1,), torch.int32, L.device)
-    ks, vs = (t.stride(0) if new[0] > 1 else 0 for t in (k_new, v_new))
     _check("sfi_paged_append_q8", lib.sfi_paged_append_q8(
         ctypes.byref(L.c), code, new[0], _ptr(k_new), _ptr(v_new), ks, vs, _ptr(cu_new), _ptr(k),
         _ptr(v), *_ws(ws, L.device), _stream(stream)))
@@ -667,13 +675,14 @@ def sfi_qk_norm_rope(layout: RotaryLayout, q, k, q_out, k_out, q_weight=None, k_
             continue
         if x is None or y is None:
             raise ValueError(f"{name} and {name}_out must be given, with {heads} heads")
-        _want(name, x, (rows, heads, L.head_dim), L.dtype, device, True)
-        _want(f"{name}_out", y, (rows, heads, L.head_dim), L.dtype, device, True)
+        shape = (rows, heads, L.head_dim)
+        stride, out_stride = _rows(name, x, shape, L.dtype, device), _rows(name + "_out", y, shape, L.dtype, device)
         if w is not None:
-            _want(f"{name}_weight", w, (L.head_dim,), L.dtype, device)
-        if rows > 1:  # (a row stride only means something where there is a second row)
-            setattr(c, f"{name}_stride", x.stride(0))
-            setattr(c, f"{name}_out_stride", y.stride(0))
+            _want(name + "_weight", w, shape[2:], L.dtype, device)
+        if name == "q":
+            c.q_stride, c.q_out_stride = stride, out_stride
+        else:
+            c.k_stride, c.k_out_stride = stride, out_stride
     c.total = rows
     _check("sfi_qk_norm_rope", lib.sfi_qk_norm_rope(
         ctypes.byref(c), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(q_out), _ptr(k_out),
