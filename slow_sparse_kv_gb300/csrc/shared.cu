@@ -453,8 +453,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
           // both halves having the same rows.  The halves take the steps in turn, over all pieces.
           const bool two = halves(w.tile) == 2;
           const int n = (w.j1 - w.j0) << two;
-          auto scores = [&](int k) {  // S = Q K^T
-            if (!two || (k & 1) == 0) ok = ok && await(full + ks * 8, k_ph);
+          // Scores of the next step: whether it is the first of its block's steps, and the last.
+          auto scores = [&](bool begins, bool ends) {  // S = Q K^T
+            if (begins) ok = ok && await(full + ks * 8, k_ph);
             if (!ok) return;
             const uint64_t qd = q_desc + (two && s_half ? C::QTILE >> 4 : 0), kd = k_desc + ks * (2 * C::TILE >> 4);
             const uint32_t d = tmem + rs * kRegion;
@@ -463,48 +464,76 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
               tc5::mma_ss(d, qd + (((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4),
                           kd + (((kk / 4) * (kKeys * 128) + (kk % 4) * 32) >> 4), kIdS, kk > 0);
             tc5::commit(s_full + rs * 8);
-            if (!two || (k & 1)) {
-              if (++ks == C::STAGES) ks = 0, k_ph ^= 1;
+            if (ends) {
+              const bool wraps = ks + 1 == C::STAGES;
+              ks = wraps ? 0 : ks + 1;
+              k_ph ^= wraps;
             }
-            if (++rs == kRegions) rs = 0;
+            rs = rs + 1 == kRegions ? 0 : rs + 1;
             s_half ^= 1;
+          };
+          uint32_t chain = 0;  // steps since the sums were begun, of both halves
+          // Products with V of the next step, and whether it is the last of its block's.
+          auto products = [&](bool ends) {  // O (+)= P V
+            const uint64_t vd = v_desc + vs * (2 * C::TILE >> 4);
+            const uint32_t d = tmem + kSums + half * 128, p = tmem + rp * kRegion;
+            tc5::fence_after();
+#pragma unroll
+            for (int z = 0; z < kKeys / 16; ++z)
+#pragma unroll
+              for (int e = kTerms - 1; e >= 0; --e)  // small terms first
+                tc5::mma_ts(d, p + term_at(z, e), vd + z * (2048 >> 4), kIdO, chain > 1 || z > 0 || e + 1 < kTerms);
+            if (ends) {
+              tc5::commit(empty + vs * 8);
+              vs = vs + 1 == C::STAGES ? 0 : vs + 1;
+            }
+            chain = chain + 1 == 2 * kChain ? 0 : chain + 1;
+            half ^= 1;
+            const bool wraps = rp + 1 == kRegions;
+            rp = wraps ? 0 : rp + 1;
+            p_ph ^= wraps;
+          };
+          // A step with more behind it: P of the next one mostly lies there already; if not, the
+          // scores go first.
+          auto step = [&](bool ends, bool s_begins, bool s_ends) {
+            products(ends);
+            const bool there = mbar_test_wait(p_ready + rp * 8, p_ph);
+            scores(s_begins, s_ends);
+            if (!there) ok = ok && await(p_ready + rp * 8, p_ph);
           };
           ok = await(smem_addr(&sh.q_full), q_ph);
           q_ph ^= 1;
           // (a region is free: the products with the P that lay there were issued before)
-          for (int k = 0; k < min(n, kRegions); ++k) scores(k);
+          for (int k = 0; k < min(n, kRegions); ++k) scores(!two || (k & 1) == 0, !two || (k & 1));
           tc5::commit(empty + vs * 8);  // the first pair, which has no V
-          if (++vs == C::STAGES) vs = 0;
+          vs = vs + 1 == C::STAGES ? 0 : vs + 1;
           if (n <= kRegions) tc5::commit(smem_addr(&sh.q_empty));
           ok = ok && await(p_ready + rp * 8, p_ph);
-          for (int k = 0; k < n && ok; ++k) {
+          // (without a branch but for waits: one costs as much as an MMA)
+          int k = 0;
+          if (two) {
+            for (; k + kRegions + 1 < n && ok; k += 2) {
+              step(false, false, true);
+              step(true, true, false);
+            }
+          } else {
+            for (; k + kRegions < n && ok; ++k) step(true, true, true);
+          }
+          for (; k < n && ok; ++k) {
             if (two ? k == n - 2 : k == n - 1) {  // the last pair, which has no K
               ok = await(full + ks * 8, k_ph);
               if (++ks == C::STAGES) ks = 0, k_ph ^= 1;
               if (!ok) break;
             }
-            const bool fresh = (k >> 1) % kChain == 0;  // the half's sums have been read
-            const uint64_t vd = v_desc + vs * (2 * C::TILE >> 4);
-            const uint32_t d = tmem + kSums + half * 128, p = tmem + rp * kRegion;
-            tc5::fence_after();
-#pragma unroll
-            for (int z = 0; z < kKeys / 16; ++z)  // O (+)= P V
-#pragma unroll
-              for (int e = kTerms - 1; e >= 0; --e)  // small terms first
-                tc5::mma_ts(d, p + term_at(z, e), vd + z * (2048 >> 4), kIdO, !fresh || z > 0 || e + 1 < kTerms);
-            if (!two || (k & 1)) {
-              tc5::commit(empty + vs * 8);
-              if (++vs == C::STAGES) vs = 0;
-            }
+            const uint32_t region = rp;
+            products(!two || (k & 1));
+            if (k + kRegions < n) scores((k & 1) != 0, (k & 1) == 0);
             // (who waits for these products otherwise waits for scores that were issued behind them)
-            if (k + kRegions >= n) tc5::commit(o_full + rp * 8);
-            half ^= 1;
-            if (++rp == kRegions) rp = 0, p_ph ^= 1;
-            // P of the next step mostly lies there already; if not, the scores go first
-            const bool there = k + 1 < n && mbar_test_wait(p_ready + rp * 8, p_ph);
-            if (k + kRegions < n) scores(k + kRegions);
-            if (k + kRegions + 1 == n) tc5::commit(smem_addr(&sh.q_empty));
-            if (k + 1 < n && !there) ok = ok && await(p_ready + rp * 8, p_ph);
+            else tc5::commit(o_full + region * 8);
+            if (k + kRegions + 1 == n || (k + kRegions == n && !two)) {
+              if (n > kRegions) tc5::commit(smem_addr(&sh.q_empty));
+            }
+            if (k + 1 < n) ok = ok && await(p_ready + rp * 8, p_ph);
           }
         }
         // the products in flight end before tensor memory is freed, whether or
