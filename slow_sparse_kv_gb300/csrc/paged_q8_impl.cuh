@@ -137,22 +137,25 @@ __device__ __forceinline__ void copy_q8(const PagedAttnArgs& a, SharedQ8& sh, lo
     const long long x = x0 + kProducers * lane;
     const bool mine = x < to;
     Unit u{0, 0, 0, 0};
-    int t = 0, n = 0, page[2] = {0, 0}, boxes = 0;
+    int t = 0, n = 0, page[2] = {0, 0}, row[2] = {0, 0}, boxes = 0;
+    int64_t at[2] = {0, 0};  // bytes to the boxes' scales
     if (mine) {
       u = unit_at(x, sh.ln, geo.B, H_kv);
       t = int(x - u.begin);
       n = min(geo.len[u.b], cap);
     }
     if (TMA) {
-      const int32_t* const row = geo.table + int64_t(u.b) * geo.max_pages;
+      const int32_t* const urow = geo.table + int64_t(u.b) * geo.max_pages;
       bool bad = false;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int pos = t * kTile + i * a.box;
         if (!mine || pos >= n || i * a.box >= kTile) continue;
-        page[i] = row[pos / P];
+        page[i] = urow[pos / P];
+        row[i] = u.g * P + pos % P;
         if (page[i] < 0 || page[i] >= geo.n_pages) bad = true, page[i] = 0;
         boxes = i + 1;
+        at[i] = page[i] * geo.page_stride + a.scale_at + row[i] * 4LL;
       }
       if (bad) set_status(geo.status, SFI_DEV_BAD_INDEX);
     }
@@ -183,12 +186,10 @@ __device__ __forceinline__ void copy_q8(const PagedAttnArgs& a, SharedQ8& sh, lo
 #pragma unroll
           for (int y2 = 0; y2 < 2; ++y2) {
             if (y2 >= boxes) break;
-            const int row = u.g * P + (t * kTile + y2 * a.box) % P;  // of its page
-            const int64_t at = page[y2] * geo.page_stride + a.scale_at + row * 4LL;
-            tma_load_3d(dst + y2 * a.box * D, &a.tmk, 0, row, page[y2], bar);
-            bulk_load(sdst + y2 * a.box * 4, kp + at, a.box * 4, bar);
-            tma_load_3d(dst + C::HALF + y2 * a.box * D, &a.tmv, 0, row, page[y2], bar);
-            bulk_load(sdst + kTile * 4 + y2 * a.box * 4, vp + at, a.box * 4, bar);
+            tma_load_3d(dst + y2 * a.box * D, &a.tmk, 0, row[y2], page[y2], bar);
+            bulk_load(sdst + y2 * a.box * 4, kp + at[y2], a.box * 4, bar);
+            tma_load_3d(dst + C::HALF + y2 * a.box * D, &a.tmv, 0, row[y2], page[y2], bar);
+            bulk_load(sdst + kTile * 4 + y2 * a.box * 4, vp + at[y2], a.box * 4, bar);
           }
         }
       } else {
