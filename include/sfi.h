@@ -491,8 +491,8 @@ sfi_status sfi_paged_attn(const sfi_paged_layout* layout, const void* q, const v
  *    anything; a number of pages outside [0, max_pages], or more than one of the group's
  *    sequences holds, sets it too, and that group shares nothing: each then reads its own
  *    row of the table, and the result is the same.
- *  - Probabilities of the shared part are the sum of two bf16 terms (16 bits), all else is
- *    fp32.  An element of V in the shared part that is not finite may make its column of the
+ *  - Probabilities are not rounded: they go through the tensor cores as three bf16 terms, all
+ *    else is fp32.  An element of V in the shared part that is not finite may make its column of the
  *    group's outputs NaN where it would be infinite.
  *  - The same call gives the same bits.
  * The workspace (sfi_paged_shared_workspace_size, 0 for invalid arguments; it grows with

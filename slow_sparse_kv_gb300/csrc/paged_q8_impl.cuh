@@ -22,6 +22,13 @@
 // 2^4, all stay below 2^15, and it is split into two terms: 22 bits, and what is
 // dropped below is under 2^-35 of the largest product of a row.  Each tile's product starts
 // from zero and is added to o in fp32 (the tensor cores truncate where they add).
+//
+// Measured, 32 / 8 heads of 128 in bf16: 8 x 32768 positions in int8, pages of 64 (0.55 GB), in
+// 92 us, 6.05 TB/s, where a copy reaches 6.78 (pages of 16: 96); 32 sequences of 4096 to 65536 in
+// e4m3 (1.23 GB) in 197 us, 6.2 TB/s, with pages of 16 and 191 with pages of 64: a tile of two pages
+// takes eight copies and not four.  (A copying lane that works its tile's addresses out while it
+// issues the copies: 213.  Scales copied 4 bytes a lane: 220, and 98 for the other.)  One
+// sequence of 700 11.8 us, the two launches.  128 heads (16 a group), 8 x 32768: 118.
 #pragma once
 
 #include <cuda_fp16.h>

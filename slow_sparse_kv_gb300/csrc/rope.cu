@@ -17,6 +17,10 @@
 // for all heads, and once for its query and its key heads the products of weight and cosine
 // or sine, so that a head costs a rotation and a factor: with the weights read and applied head by
 // head the instructions took longer than HBM, 67 us for 16384 rows of 32 + 8 heads of 128.
+//
+// Bound by HBM, 2 e d bytes a head.  Measured: those 16384 rows in bf16 (336 MB) in 56.5 us,
+// 5.94 TB/s, where a copy reaches 6.78; 5001 rows of 12 + 4 heads of 64 in fp32, half of them
+// rotated (41 MB), 12.3; 64 rows of 32 + 8 heads of 128 4.4, a launch and one dependent read.
 #include <cuda_runtime.h>
 
 #include "common.cuh"

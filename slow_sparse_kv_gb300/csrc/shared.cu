@@ -7,18 +7,25 @@
 //   out = sum_w f_w o_w / sum_w f_w l_w,  f_w = 2^(c (m_w - max m)),  c = log2(e) / sqrt(d)
 //
 // The shared part is a matrix product: the group's queries of a KV head, members x G rows,
-// against n0 keys.  A tile is 2 x 128 such rows; all tiles' blocks of 128 keys, KV head by KV
+// against n0 keys.  A tile is 2 x 128 such rows; all tiles' blocks of 48 keys, KV head by KV
 // head, stand in one line, which is cut into a share of equal size for each CTA.  In a CTA, as
 // in prefill.cu: S = Q K^T (tcgen05.mma from shared memory into tensor memory), softmax
 // statistics with a thread for each row, P over S's columns, O += P V; the two halves of
 // a tile alternate, so that the tensor cores work on one while the other's softmax runs.
-// The output is fp32, so P is kept in two bf16 terms (16 bits), at the price of a second
-// product with V.
-// Bytes: 4 d n0 a group and KV head; flops 4 d (6 d with the second term) for each row and key.
-// From 64 rows on about the tensor cores bound it, below HBM does.
+// (A tile of 128 rows or fewer is taken by both halves, each with every other block.)
+// The output is fp32, so P is kept in three bf16 terms (24 bits: nothing is lost), at the price
+// of two more products with V.  (With two terms and a product's sums in tensor memory
+// from a piece's first block to its last the outputs were off by 2e-6 to 5e-6, now by 2.4e-7 to 7.4e-7.)
+// Bytes: 4 d n0 a group and KV head; flops 4 d for each row and key, 8 d with all three terms.
+// From some 100 rows on the tensor cores bound it, below HBM does.
 //
 // Three launches: the shared part, the sequences' own part, and one that joins the states of
-// both.
+// both.  Measured, 32 / 8 heads of 128: 64 sequences behind 32768 positions, 16 to 1024 of
+// their own, 96 us: 61 (0.56 PFLOP/s as the formula counts, 1.13 with the terms; the tensor
+// pipe is active for 55% of the cycles; 7 before the first product, 4 for taking sums out of
+// tensor memory), 19 and 14; that these run one after another is what is left to gain.  5 groups of
+// 9 behind 6000 positions in pages of 24: 62 us (32, 12 and 14).  6 sequences, 8 / 2 heads of 64,
+// behind 600 positions: 18 us (6.5, 4.3 and 5.3).
 #include <cuda_runtime.h>
 
 #include <atomic>
