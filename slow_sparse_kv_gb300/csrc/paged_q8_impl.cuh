@@ -18,9 +18,9 @@
 //
 // fp16 operands: q is scaled by a power of two for each head so that its largest element
 // lies in [2^14, 2^15) (bf16: exact down to 2^-32 of that; fp32: two terms, 22 bits); p sv
-// by one for each tile so that the largest sv counts as [2^10, 2^11) and, p being at most
-// 2^4, all stay below 2^15, and it is split into two terms: 22 bits, and what is
-// dropped below is under 2^-35 of the largest product of a row.  Each tile's product starts
+// by one for each tile and head in the same way, and it is split into two terms: 22 bits, and what
+// is dropped below is under 2^-39 of the tile's largest p sv.  (Scaled by the tile's largest sv
+// alone, a row of large values that the softmax leaves out would cost the others their bits.)  Each tile's product starts
 // from zero and is added to o in fp32 (the tensor cores truncate where they add).
 //
 // Measured, 32 / 8 heads of 128 in bf16: 8 x 32768 positions in int8, pages of 64 (0.55 GB), in
@@ -28,7 +28,7 @@
 // e4m3 (1.23 GB) in 197 us, 6.2 TB/s, with pages of 16 and 191 with pages of 64: a tile of two pages
 // takes eight copies and not four.  (A copying lane that works its tile's addresses out while it
 // issues the copies: 213.  Scales copied 4 bytes a lane: 220, and 98 for the other.)  One
-// sequence of 700 11.8 us, the two launches.  128 heads (16 a group), 8 x 32768: 118.
+// sequence of 700 11.9 us, the two launches.  128 heads (16 a group), 8 x 32768: 126.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -395,18 +395,16 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_q8_kernel(const __g
                 for (int q = NQ - 1; q >= 0; --q) mma_f16_16816(s[mt][h], a0, a1, a2, a3, qb[h][q][kk][0], qb[h][q][kk][1]);
             }
           }
-          // ---- scales: those of the rows r8 + 8 i, and the exponent of the largest of V's
+          // ---- scales: those of the rows r8 + 8 i
           float kscale[4], vscale[4];
-          const uint32_t vtop = __reduce_max_sync(kFull, lane < left ? __float_as_uint(lds32(sc + kTile * 4 + lane * 4)) & 0x7fffffffu : 0u);
-          const int vex = max(int(vtop >> 23), 20);
-          const float vup = pow2(10 + 127 - vex), vdown = pow2(vex - 127 - 10);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int row = r8 + 8 * i;
             kscale[i] = lds32(sc + row * 4);
-            vscale[i] = row < left ? lds32(sc + kTile * 4 + row * 4) * vup : 0.f;
+            vscale[i] = row < left ? lds32(sc + kTile * 4 + row * 4) : 0.f;
           }
           uint32_t pw[NT][2][2][2];  // P^T: [term][positions / 16][half]
+          float down[NT][2];         // what turns the products with V back
 #pragma unroll
           for (int h = 0; h < NT; ++h) {
             float top[2];
@@ -437,10 +435,25 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_q8_kernel(const __g
             const float b0 = m[h][0] == -INFINITY ? 0.f : m[h][0], b1 = m[h][1] == -INFINITY ? 0.f : m[h][1];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float p0 = ex2(s[i >> 1][h][(i & 1) * 2] - b0), p1 = ex2(s[i >> 1][h][(i & 1) * 2 + 1] - b1);
+              float &z0 = s[i >> 1][h][(i & 1) * 2], &z1 = s[i >> 1][h][(i & 1) * 2 + 1];
+              const float p0 = ex2(z0 - b0), p1 = ex2(z1 - b1);
               l[h][0] += p0;
               l[h][1] += p1;
-              const float z0 = p0 * vscale[i], z1 = p1 * vscale[i];
+              z0 = p0 * vscale[i], z1 = p1 * vscale[i];
+            }
+            // the exponents of both heads' largest p sv, as the upper halves of the numbers
+            uint32_t zt = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              zt = __vmaxu2(zt, __byte_perm(__float_as_uint(s[i >> 1][h][(i & 1) * 2]), __float_as_uint(s[i >> 1][h][(i & 1) * 2 + 1]), 0x7632) & 0x7fff7fffu);
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) zt = __vmaxu2(zt, __shfl_xor_sync(kFull, zt, w));
+            const int ex0 = max(int(zt >> 7 & 0xff), 20), ex1 = max(int(zt >> 23), 20);
+            const float up0 = pow2(14 + 127 - ex0), up1 = pow2(14 + 127 - ex1);
+            down[h][0] = pow2(ex0 - 127 - 14), down[h][1] = pow2(ex1 - 127 - 14);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float z0 = s[i >> 1][h][(i & 1) * 2] * up0, z1 = s[i >> 1][h][(i & 1) * 2 + 1] * up1;
               const uint32_t w = pack_f16x2(z0, z1);
               pw[h][0][i >> 1][i & 1] = movmatrix_trans(w);
               pw[h][1][i >> 1][i & 1] = movmatrix_trans(pack_f16x2(z0 - f16_lo(w), z1 - f16_hi(w)));
@@ -478,7 +491,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_q8_kernel(const __g
                   for (int mt = 0; mt < 2; ++mt)
                     mma_f16_16816(d, v[mt][c][0], v[mt][c][1], v[mt][c][2], v[mt][c][3], pw[h][t][mt][0], pw[h][t][mt][1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[c2 * 2 + c][h][e] = fmaf(d[e], vdown, o[c2 * 2 + c][h][e]);
+                for (int e = 0; e < 4; ++e) o[c2 * 2 + c][h][e] = fmaf(d[e], down[h][e & 1], o[c2 * 2 + c][h][e]);
               }
           }
           __syncwarp();

@@ -86,7 +86,7 @@ def tolerance(ref, scale, size, d, n, dtype, top):
     """Elementwise bound: that of an fp32 attention (scores with 8 roundings more: factors and scales),
     queries in two fp16 terms where they are fp32 (2^-21 with both roundings), p in two terms
     (2^-11 each), and of what these drop below their smallest number, 2^-25 on a scale on
-    which the tile's largest value of V counts as 2^10 at least and p as 2^0 at the maximum: 2^-35
+    which the tile's largest p sv counts as 2^14 at least, p being at most 2^4: 2^-35
     of the largest value for each of n positions."""
     if dtype == F32:
         size = size * (1 + 2.0 ** -21 / (2.0 ** -23 * d))
@@ -150,6 +150,32 @@ def test_scales_of_all_sizes(sfi, fmt, dtype):
     for up in (2.0 ** -70, 2.0 ** 60):
         c.lay.scales(c.v).mul_(up)
         c.check(q, *c.run(sfi, q))
+
+
+@pytest.mark.parametrize("up", [20, 40])
+@pytest.mark.parametrize("fmt,dtype", [(I8, BF16), (E4M3, F32)])
+def test_large_values_that_a_head_leaves_out(sfi, fmt, dtype, up):
+    """A position in every tile whose value is 2^up times the others', which the one head of its
+    group leaves out (a score of about -80) and the other attends to alone."""
+    lens = [400, 33]
+    c = Cache(sfi, 4, 2, 128, fmt, 16, lens, spread=0.0)
+    q = normal((2, 4, 128), dtype, 21)
+    q[:, 1::2] = -q[:, ::2]
+    for b, n in enumerate(lens):
+        for i in range(3, n, 32):
+            for g in range(2):
+                at = (int(c.rows[b, i // 16]), g, i % 16)
+                x = q[b, 2 * g].float()
+                c.lay.codes(c.k)[at] = (-40 * torch.sign(x)).to(fmt)
+                c.lay.scales(c.k)[at] = 80 * 128 ** 0.5 / 40 / float(x.abs().sum())
+                c.lay.scales(c.v)[at] *= 2.0 ** up
+    out, lse = c.run(sfi, q)
+    ref, rl, scale, size = P.paged(f64(q), values(c.lay, c.k), values(c.lay, c.v), c.rows, lens)
+    # (as in `tolerance`, but what p in two terms drops is 2^-39 of the largest p sv of a tile and head
+    # for each position; times a code, which is at most twice its row's largest)
+    tol = tolerance(ref, scale, size, 128, 400, dtype, 0.0) + 400 * 2.0 ** -38 * scale.max(-1, keepdims=True)
+    close(f64(out), ref, tol, "out")
+    close_lse(f64(lse), rl, size * (1 + 2.0 ** -21 / (2.0 ** -23 * 128)), 128 + 8)
 
 
 @pytest.mark.parametrize("fmt", [I8, E4M3])
