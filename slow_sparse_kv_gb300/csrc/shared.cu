@@ -710,18 +710,22 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
 // positions too, where each read touches 32 lines: 25 us for 256 rows of 20 pieces.)
 struct State {
   float m = -INFINITY, l = 0.f;
-  // Takes in N states; returns the factors of what it was and of theirs.
+  // Takes in N states; returns the factors of what it was and of theirs.  One that saw only scores of
+  // -infinity, or nothing, adds nothing; any other's factor is above 0, so that its NaNs and
+  // infinities reach the result.
+  static __device__ __forceinline__ float factor(float m, float l, float top, float c) {
+    return m == -INFINITY && l == 0.f ? 0.f : fmaxf(ex2((m - top) * c), 0x1p-126f);
+  }
   template <int N>
   __device__ __forceinline__ float take(const float (&mv)[N], const float (&lv)[N], float (&f)[N], float c) {
     float top = m;
 #pragma unroll
     for (int w = 0; w < N; ++w) top = fmaxf(top, mv[w]);
-    const float was = m == -INFINITY && l == 0.f ? 0.f : ex2((m - top) * c);
+    const float was = factor(m, l, top, c);
     l = was == 0.f ? 0.f : l * was;
 #pragma unroll
     for (int w = 0; w < N; ++w) {
-      // (one that saw only scores of -infinity, or nothing, adds nothing)
-      f[w] = mv[w] == -INFINITY && lv[w] == 0.f ? 0.f : ex2((mv[w] - top) * c);
+      f[w] = factor(mv[w], lv[w], top, c);
       l = f[w] == 0.f ? l : fmaf(f[w], lv[w], l);
     }
     m = top;

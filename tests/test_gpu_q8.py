@@ -218,6 +218,35 @@ def test_bad_pages_and_lengths(sfi):
     assert (out[0] == 0).all() and torch.isneginf(lse[0]).all() and torch.equal(out[1], good[1])
 
 
+@pytest.mark.parametrize("fmt,dtype,page", [(I8, BF16, 32), (E4M3, F32, 16), (I8, F32, 20)])
+def test_wait_limit(sfi, fmt, dtype, page):
+    """A one-clock limit: the waits give up, the status says so, nothing is left in flight.  The
+    cache is larger than L2, so that some wait is always early."""
+    n, hq, hkv, d = 16384, 8, 2, 128
+    per = -(-n // page)
+    n_pages = 64 * per
+    table = torch.randperm(n_pages, device="cuda").view(64, per).int()
+    lay = sfi.PagedLayout(hq, hkv, d, fmt, page, n_pages, table, ints([n] * 64))
+    k, v = (torch.zeros(n_pages, lay.page_bytes, dtype=torch.uint8, device="cuda") for _ in range(2))
+    for pool in (k, v):
+        lay.codes(pool).view(torch.uint8).copy_(torch.randint(0, 100, (1, hkv, page, d), device="cuda", dtype=torch.uint8))
+        lay.scales(pool).fill_(0.01)
+    q = normal((64, hq, d), dtype, 1)
+    ws, good, out = sfi.paged_workspace(lay), *(torch.empty(64, hq, d, device="cuda") for _ in range(2))
+    sfi.sfi_paged_attn_q8(lay, q, k, v, good, None, ws)
+    assert sfi.sfi_read_status(ws) == 0
+    sfi.lib.sfi_set_wait_limit(1)
+    try:
+        for _ in range(2):
+            sfi.sfi_paged_attn_q8(lay, q, k, v, out, None, ws)
+            assert sfi.sfi_read_status(ws) == sfi.SFI_DEV_WAIT_TIMEOUT
+    finally:
+        sfi.lib.sfi_set_wait_limit(0)
+    ws.zero_()
+    sfi.sfi_paged_attn_q8(lay, q, k, v, out, None, ws)
+    assert sfi.sfi_read_status(ws) == 0 and torch.equal(good, out)
+
+
 @pytest.mark.parametrize("fmt,dtype,lens,page", [(I8, BF16, [(i * 7) % 41 for i in range(300)], 16), (E4M3, F32, [1 + i % 3 for i in range(1024)], 20)])
 def test_many_sequences(sfi, fmt, dtype, lens, page):
     c = Cache(sfi, 4, 2, 64, fmt, page, lens)

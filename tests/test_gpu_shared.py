@@ -186,6 +186,32 @@ def test_query_that_is_not_finite_stays_alone(sfi):
     assert torch.equal(out[rest], good[rest]) and torch.equal(lse[rest], gl[rest])
 
 
+@pytest.mark.parametrize("page,own", [(16, [5, 0, 40]), (12, [300, 1, 9])])
+def test_what_is_not_finite_reaches_the_group(sfi, page, own):
+    """Keys of NaN over whole blocks, so that a state holds nothing else; and an element of V that is
+    not finite at a position whose probability is 0 in fp32."""
+    pages = 288 // page  # six blocks of 48, each a share by itself
+    b = Batch(8, 2, 128, page, [(3, pages), (2, pages)], own + [7, 8])
+    good, gl = b.run(sfi)
+    rest = torch.ones(5, 8, dtype=torch.bool, device="cuda")
+    rest[:3, 4:] = False
+    held = b.rows[0, :96 // page].tolist()
+    keep = b.k[held, 1].clone()
+    b.k[held, 1] = float("nan")
+    out, lse = b.run(sfi)
+    assert out[:3, 4:].isnan().all() and lse[:3, 4:].isnan().all()
+    assert torch.equal(out[rest], good[rest]) and torch.equal(lse[rest], gl[rest])
+    b.k[held, 1] = keep
+    # sequence 0's heads 4 to 7 ask for what those keys are not: scores of about -200 and less
+    b.q[0, 4:] = b.q[0, 4:].abs()
+    b.k[held, 1] = -25.0
+    b.v[held[0], 1, 3, 17] = float("nan")
+    out, lse = b.run(sfi)
+    bad = out[0, 4:].isnan()
+    assert bad[:, 17].all() and int(bad.sum()) == 4 and torch.isfinite(lse).all()
+    assert torch.equal(out[rest], good[rest])
+
+
 def test_wrong_groups_share_nothing(sfi):
     """Flagged, and every sequence is attended to by its own row of the table."""
     b = Batch(8, 2, 128, 16, [(3, 4), (2, 3)], [5, 0, 40, 1, 9])
@@ -212,6 +238,26 @@ def test_bad_page_is_flagged(sfi):
         b.table[0, 2] = page
         out, _ = b.run(sfi, status=sfi.SFI_DEV_BAD_INDEX)
         assert torch.equal(out[3:], good[3:])
+
+
+@pytest.mark.parametrize("hq,hkv,d,page", [(8, 2, 128, 16), (4, 2, 64, 32), (8, 2, 128, 20)])
+def test_wait_limit(sfi, hq, hkv, d, page):
+    """A one-clock limit: the waits give up, the status says so, nothing is left in flight; afterwards
+    the default limit gives the bytes from before."""
+    b = Batch(hq, hkv, d, page, [(40, 16000 // page), (3, 4000 // page)], [(i * 37) % 200 for i in range(43)])
+    good, _ = b.run(sfi)
+    ws = sfi.paged_shared_workspace(b.lay)
+    cu, shared, out = ints(b.cu), ints(b.shared), torch.empty_like(good)
+    sfi.lib.sfi_set_wait_limit(1)
+    try:
+        for _ in range(2):
+            sfi.sfi_paged_attn_shared(b.lay, cu, shared, b.q, b.k, b.v, out, None, ws)
+            assert sfi.sfi_read_status(ws) == sfi.SFI_DEV_WAIT_TIMEOUT
+    finally:
+        sfi.lib.sfi_set_wait_limit(0)
+    ws.zero_()
+    again, _ = b.run(sfi, ws=ws)
+    assert torch.equal(good, again)
 
 
 def test_workspace_serves_the_other_calls(sfi):
