@@ -321,7 +321,7 @@ sfi_status sfi_fast_attn_noalloc(const sfi_layout* layout, const sfi_params* par
  *  - q_weight, k_weight: d elements of the rows' type (device; NULL: ones; NULL where norm
  *    is 0).
  *  - rotary_dim: a multiple of 8 in [0, d]; 0 rotates nothing (pos and inv_freq may be NULL).
- *  - inv_freq: host array of rotary_dim / 2 finite numbers, read before the call returns;
+ *  - inv_freq: host array of rotary_dim / 2 numbers up to 2^32, read before the call returns;
  *    whatever scheme makes them (theta^(-2 i / rotary_dim), scaled for longer contexts).
  *    The angle is taken modulo a turn without loss: any int32 position and offset, negative
  *    ones too, is off by less than 2^-24 turns.

@@ -636,6 +636,8 @@ class RotaryLayout:
         r = head_dim if rotary_dim is None else int(rotary_dim)
         if inv_freq is None:
             inv_freq = [float(theta) ** (-2.0 * i / r) for i in range(r // 2)]
+        if not -(1 << 31) <= int(pos_offset) < 1 << 31:
+            raise ValueError(f"pos_offset: {pos_offset} leaves 32 bits")
         if len(inv_freq) != r // 2:
             raise ValueError(f"inv_freq: expected {r // 2} numbers, got {len(inv_freq)}")
         if r > 0:

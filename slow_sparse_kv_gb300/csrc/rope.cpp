@@ -66,8 +66,8 @@ sfi_status sfi_qk_norm_rope(const sfi_rotary_layout* L, const void* q, const voi
   RopeArgs a;
   std::memset(&a, 0, sizeof(a));
   for (int i = 0; i < L->rotary_dim / 2; ++i) {
-    if (!std::isfinite(L->inv_freq[i]))
-      return fail(SFI_ERR_INVALID_ARG, "inv_freq[%d] is not finite", i);
+    if (!(std::fabs(L->inv_freq[i]) <= 0x1p32))  // (beyond, the turns' fraction would lose bits)
+      return fail(SFI_ERR_INVALID_ARG, "inv_freq[%d] (%g) must lie in [-2^32, 2^32]", i, L->inv_freq[i]);
     a.freq[i] = turns_of(L->inv_freq[i]);
   }
   const int unit = L->dtype == SFI_F32 ? 4 : 8;

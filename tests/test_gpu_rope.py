@@ -175,3 +175,5 @@ def test_binding_refusals(sfi):
         sfi.RotaryLayout(2, 1, 64, F32, ints([0]), inv_freq=[1.0])
     with pytest.raises(ValueError):
         sfi.RotaryLayout(2, 1, 64, F32, None)
+    with pytest.raises(ValueError):
+        sfi.RotaryLayout(2, 1, 64, F32, ints([0]), pos_offset=1 << 31)

@@ -32,6 +32,7 @@ def test_rope_refusals(sfi):
                      (dict(rotary_dim=-8), bad), (dict(rotary_dim=72), bad), (dict(rotary_dim=12), bad), (dict(inv_freq=None), bad),
                      (dict(eps=-1.0), bad), (dict(eps=float("nan")), bad), (dict(eps=float("inf")), bad), (dict(norm=0), bad),
                      (dict(norm=0, wq=None), bad), (dict(freq=[float("inf")] * 64), bad), (dict(freq=[float("nan")] * 64), bad),
+                     (dict(freq=[-2.0 ** 33] * 64), bad),
                      (dict(q_stride=511), bad), (dict(q_stride=516), bad), (dict(k_stride=64), bad), (dict(q_out_stride=-512), bad),
                      (dict(k_out_stride=132), bad), (dict(k_stride=1 << 40), cap), (dict(pos=None), bad), (dict(q=None), bad),
                      (dict(k=None), bad), (dict(qo=None), bad), (dict(ko=None), bad), (dict(q=FAKE + 8), bad), (dict(ko=FAKE + 4), bad),
