@@ -440,6 +440,7 @@ class PagedLayout:
         #: elements of a page (bytes of an 8-bit one)
         self.page_bytes = -(-rows * (head_dim + 4) // 16) * 16 if self.q8 else rows * head_dim
         self._pool_shape = (n_pages, self.page_bytes) if self.q8 else (n_pages, n_kv_heads, page_size, head_dim)
+        self._held = torch.uint8 if self.q8 else dtype
         self._page_strides = (1,) if self.q8 else (page_size * head_dim, head_dim, 1)
         code = _POOL_CODES[dtype] if self.q8 else dtype_code(dtype)
         self.c = sfi_paged_layout(self.B, n_q_heads, n_kv_heads, head_dim, code, page_size,
@@ -449,12 +450,11 @@ class PagedLayout:
     def _pool(self, name: str, t: torch.Tensor, layers: int = 0) -> torch.Tensor:
         """Refuse a tensor that is not a pool ([layers,] n_pages, H_kv, page_size, d) of this layout."""
         want = (layers,) + self._pool_shape if layers else self._pool_shape
-        held = torch.uint8 if self.q8 else self.dtype
-        if t.dtype is not held or t.shape != want or t.device != self.device:
-            raise ValueError(f"{name}: expected {held} {want} on {self.device}, "
+        if t.dtype is not self._held or t.shape != want or t.device != self.device:
+            raise ValueError(f"{name}: expected {self._held} {want} on {self.device}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
         apart = self.page_stride or self.page_bytes
-        strides = t.stride()[-len(self._pool_shape):]
+        strides = t.stride()[layers > 0:]
         if strides[1:] != self._page_strides and not t[(0,) * (1 + bool(layers))].is_contiguous():
             raise ValueError(f"{name}: a page must be dense")
         if self.n_pages > 1 and strides[0] != apart:

@@ -124,9 +124,9 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, c
     if (mine) {
       u = unit_at(x, sh.ln, geo.B, H_kv);
       t = int(x - u.begin);
-      n = min(geo.len[u.b], cap) - skipped(geo, u.b) * P;
+      n = min(geo.len[u.b], cap) - skipped<SOLO>(geo, u.b) * P;
     }
-    const int32_t* const row = geo.table + int64_t(u.b) * geo.max_pages + skipped(geo, u.b);
+    const int32_t* const row = geo.table + int64_t(u.b) * geo.max_pages + skipped<SOLO>(geo, u.b);
     if (LD != kCpAsync) {
       bool bad = false;
 #pragma unroll
@@ -160,7 +160,7 @@ __device__ __forceinline__ void copy_tiles(const PagedAttnArgs& a, Shared& sh, c
     auto row_of = [&](int i) {
       const int ut = __shfl_sync(kFull, t, i), ug = __shfl_sync(kFull, u.g, i), un = __shfl_sync(kFull, n, i);
       const int ub = __shfl_sync(kFull, u.b, i);
-      const int32_t* const urow = geo.table + int64_t(ub) * geo.max_pages + skipped(geo, ub);
+      const int32_t* const urow = geo.table + int64_t(ub) * geo.max_pages + skipped<SOLO>(geo, ub);
       const int pos = ut * TR + lane % TR;
       pg = pos < un ? urow[pos / P] : 0;
       in = pos < un ? ug * P + pos % P : -1;
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
   // joining kernel while this one drains; each waits for the results before it)
   pdl_launch();
   pdl_wait();
-  scan_lengths<TR>(geo, sh.ln, blockIdx.x == 0);
+  scan_lengths<TR, SOLO>(geo, sh.ln, blockIdx.x == 0);
   const Line& ln = sh.ln;
   const long long total = ln.pre[B] * H_kv;
 
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_kernel(const __grid
           qf[h][0] = w.x, qf[h][1] = w.y;
         }
       }
-      return min(geo.len[u.b], cap) - skipped(geo, u.b) * geo.P;
+      return min(geo.len[u.b], cap) - skipped<SOLO>(geo, u.b) * geo.P;
     };
     const Run run = SOLO ? warp_run(cut, warp) : Run{from, to};
     constexpr int STEP = SOLO ? 1 : kWarps;

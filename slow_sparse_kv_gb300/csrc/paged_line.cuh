@@ -101,12 +101,13 @@ __device__ __forceinline__ Unit unit_at(long long x, const Line& ln, int B, int 
   return u;
 }
 
-// Pages at the start of sequence b that are left out.
-__device__ __forceinline__ int skipped(const PagedGeo& geo, int b) { return geo.skip ? geo.skip[b] : 0; }
+// Pages at the start of sequence b that are left out (SKIP: geo.skip is set).
+template <bool SKIP>
+__device__ __forceinline__ int skipped(const PagedGeo& geo, int b) { return SKIP ? geo.skip[b] : 0; }
 
 // Fills `ln` (the first kThreads threads of a CTA); `flag` reports lengths out of
 // range.
-template <int TR>
+template <int TR, bool SKIP = false>
 __device__ __forceinline__ void scan_lengths(const PagedGeo& geo, Line& ln, bool flag) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = geo.B, cap = geo.max_pages * geo.P;
@@ -116,7 +117,7 @@ __device__ __forceinline__ void scan_lengths(const PagedGeo& geo, Line& ln, bool
       if (flag) set_status(geo.status, SFI_DEV_LEN_OVER_CAP);
       n = n < 0 ? 0 : cap;
     }
-    if (b < B) n -= skipped(geo, b) * geo.P;
+    if (SKIP && b < B) n -= skipped<SKIP>(geo, b) * geo.P;
     return (n + TR - 1) / TR;
   };
   auto scan = [&](long long x) {
@@ -197,10 +198,10 @@ struct Joined {
   }
 };
 
-// By CTA (bx, by) of nx x ny; `whole`: single pieces too, and no units of which something is left out.
-template <int TR, int D>
-__device__ __forceinline__ void join_units(const PagedAttnArgs& a, const Line& ln, const Cut& cut, bool whole, int bx, int nx,
-                                           int by, int ny) {
+// By CTA (bx, by) of nx x ny; SKIP: single pieces too, and no units of which something is left out.
+template <int TR, int D, bool SKIP = false>
+__device__ __forceinline__ void join_units(const PagedAttnArgs& a, const Line& ln, const Cut& cut, int bx, int nx, int by,
+                                           int ny) {
   constexpr int AHEAD = 8;  // pieces read at a time
   __shared__ float part[3][kWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -211,9 +212,9 @@ __device__ __forceinline__ void join_units(const PagedAttnArgs& a, const Line& l
   for (int unit = bx; unit < B * H_kv; unit += nx) {
     const int b = unit / H_kv, g = unit - b * H_kv;
     const long long nt = ln.pre[b + 1] - ln.pre[b], begin = ln.pre[b] * H_kv + g * nt;
-    if (nt == 0 || skipped(geo, b) > 0) continue;
+    if (nt == 0 || skipped<SKIP>(geo, b) > 0) continue;
     const int first = cut.holder(begin), pieces = cut.holder(begin + nt - 1) - first + 1;
-    if (pieces == 1 && !whole) continue;
+    if (pieces == 1 && !SKIP) continue;
     const int64_t qrow = (int64_t(b) * a.H_q + int64_t(g) * G) * D;
     const float* const p = a.partials + (first + unit) * step;
     if (pieces <= 2 * AHEAD) {
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
   pdl_launch();
   pdl_wait();
   scan_lengths<TR>(a.geo, ln, false);
-  join_units<TR, D>(a, ln, Cut(ln.pre[a.geo.B] * a.geo.H_kv, grid), false, blockIdx.x, gridDim.x, blockIdx.y, gridDim.y);
+  join_units<TR, D>(a, ln, Cut(ln.pre[a.geo.B] * a.geo.H_kv, grid), blockIdx.x, gridDim.x, blockIdx.y, gridDim.y);
 }
 
 // The joining kernel behind a launch of `grid` CTAs: a CTA for each unit, and for each 32

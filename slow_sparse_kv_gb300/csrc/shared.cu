@@ -847,9 +847,9 @@ __global__ void __launch_bounds__(kThreads, kJoinCtas) shared_join_kernel(const 
   }
   if (!alone) return;
   __syncthreads();
-  scan_lengths<kOwnTile>(geo, ln, false);
+  scan_lengths<kOwnTile, true>(geo, ln, false);
   const int nx = gridDim.x / ny;
-  if (int(blockIdx.x) < nx * ny) join_units<kOwnTile, D>(a.own, ln, own, true, blockIdx.x % nx, nx, blockIdx.x / nx, ny);
+  if (int(blockIdx.x) < nx * ny) join_units<kOwnTile, D, true>(a.own, ln, own, blockIdx.x % nx, nx, blockIdx.x / nx, ny);
 }
 
 template <int D, bool TMA>
