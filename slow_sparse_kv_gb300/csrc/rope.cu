@@ -18,9 +18,9 @@
 // or sine, so that a head costs a rotation and a factor: with the weights read and applied head by
 // head the instructions took longer than HBM, 67 us for 16384 rows of 32 + 8 heads of 128.
 //
-// Bound by HBM, 2 e d bytes a head.  Measured: those 16384 rows in bf16 (336 MB) in 56.5 us,
-// 5.94 TB/s, where a copy reaches 6.78; 5001 rows of 12 + 4 heads of 64 in fp32, half of them
-// rotated (41 MB), 12.3; 64 rows of 32 + 8 heads of 128 4.4, a launch and one dependent read.
+// Bound by HBM, 2 e d bytes a head.  Measured: those 16384 rows in bf16 (336 MB) in 58 us,
+// 5.8 TB/s, call behind call, where a copy reaches 6.78; 5001 rows of 12 + 4 heads of 64 in fp32, half of them
+// rotated (41 MB, which L2 holds), 9.7; 64 rows of 32 + 8 heads of 128 4.4, a launch and one dependent read.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -71,9 +71,9 @@ __device__ __forceinline__ void from_pairs(const uint64_t (&u)[2], const uint64_
   }
 }
 
-// FULL: all d dimensions are rotated.
-template <typename T, int D, bool NEXT, bool FULL>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+// FULL: all d dimensions are rotated.  CTAS: on an SM at least.
+template <typename T, int D, bool NEXT, bool FULL, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LPH = D / 8;        // lanes of a head
   constexpr int HPW = 32 / LPH;     // heads of a warp at a time
   __shared__ uint64_t freq[64];
@@ -183,8 +183,13 @@ cudaError_t launch_t(RopeArgs a, cudaStream_t st) {
   a.parts = int(want / a.total < 1 ? 1 : want / a.total < steps ? want / a.total : steps);
   const long long items = (long long)a.total * a.parts;
   const dim3 grid(unsigned((items + kThreads / 32 - 1) / (kThreads / 32)));
-  return a.rot == D ? launch_pdl(rope_kernel<T, D, NEXT, true>, grid, kThreads, 0, st, a)
-                    : launch_pdl(rope_kernel<T, D, NEXT, false>, grid, kThreads, 0, st, a);
+  // bf16 rows are half as long, so more of them have to be on their way: in 64 registers 16384 rows
+  // take 58 us and not 70, call behind call; fp32 rows 109 and not 102, and few rows 3.2 and not 2.8
+  if (sizeof(T) == 2 && a.parts == 1)
+    return a.rot == D ? launch_pdl(rope_kernel<T, D, NEXT, true, sizeof(T) == 2 ? 4 : 1>, grid, kThreads, 0, st, a)
+                      : launch_pdl(rope_kernel<T, D, NEXT, false, sizeof(T) == 2 ? 4 : 1>, grid, kThreads, 0, st, a);
+  return a.rot == D ? launch_pdl(rope_kernel<T, D, NEXT, true, 1>, grid, kThreads, 0, st, a)
+                    : launch_pdl(rope_kernel<T, D, NEXT, false, 1>, grid, kThreads, 0, st, a);
 }
 
 template <typename T>
