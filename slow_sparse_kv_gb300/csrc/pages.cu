@@ -10,8 +10,9 @@
 // 3.7 us, freeing 3.6, a fork's plan 6.0 and its copies 6.6 (16 pages, 8 layers), a
 // compaction's plan 4.6 and its moves of 352 MB 52 (6.77 TB/s), a token's rows for
 // 64 sequences 6.0, a prompt batch's 267 MB 37 to 39.  Into a cache in 8 bits: 37000 positions of 8 heads
-// of 128 in bf16 (231 MB) as e4m3 in 42, 5.5 TB/s (59% of the issue slots are taken: the
-// rounding comes next after HBM), a token's rows for 64 sequences 8.5.
+// of 128 in bf16 (231 MB) as e4m3 in 39.5, 5.8 TB/s (the issue slots are nearly as full: the rounding comes
+// next after HBM), as int8 in 50, bound by the rounding; from fp32 (383 MB) in 60, 6.4 TB/s; a token's
+// rows for 64 sequences 4.8.  (A token's first heads read before its sequence is looked up: 41.3, 52, 62, 5.9.)
 // Free pages are looked for from the lowest on, 4096 counts a round of 0.9 us: extending
 // 64 sequences takes 3.7 us where the first round finds them, 18 with the low 95% of
 // 65000 pages taken, 223 of 10^6 and 4.2 ms of 2^24.
@@ -648,7 +649,11 @@ __device__ __forceinline__ void append_row(const Quant<T, E4M3, D>& a, int b, in
 // would go over its last ones, which may lie in pages that others share, so it is left
 // out.  The last CTA only looks for what is to be flagged.
 template <typename Args>
-__global__ void __launch_bounds__(kCopy) append_kernel(const __grid_constant__ Args a) {
+constexpr int kAppendCtas = 1;  // on an SM at least: registers for more rows on their way
+template <typename T, bool E4M3, int D>
+constexpr int kAppendCtas<Quant<T, E4M3, D>> = sizeof(T) == 2 ? 6 : 5;
+template <typename Args>
+__global__ void __launch_bounds__(kCopy, kAppendCtas<Args>) append_kernel(const __grid_constant__ Args a) {
   constexpr int kWarps = kCopy / 32;
   __shared__ uint32_t mask[kMaxBatch / 32];  // sequences with rows among the CTA's tokens
   static_assert(kMaxBatch / 32 == 32, "a lane for every word");
