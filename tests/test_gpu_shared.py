@@ -278,6 +278,57 @@ def test_workspace_serves_the_other_calls(sfi):
     assert torch.equal(none[0], plain[0])
 
 
+def test_empty_groups(sfi):
+    """1024 groups, of which two have sequences.  Some of the others name more pages than a row of
+    the table has, which is flagged and changes nothing."""
+    b = Batch(8, 2, 64, 16, [(3, 4), (2, 3)], [5, 0, 40, 1, 9])
+    good = b.run(sfi)
+    cu = [0] * 500 + [3] * 300 + [5] * 225
+    shared = [7 * (i % 5) for i in range(1024)]
+    shared[499], shared[799] = 4, 3
+    assert max(shared) > b.rows.shape[1]
+    out, lse = b.run(sfi, status=sfi.SFI_DEV_LEN_OVER_CAP, cu=cu, shared=shared)
+    assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
+
+
+def test_graphs_on_one_workspace(sfi):
+    """Two captured calls of different groups and an eager one, in turn on one workspace and on a
+    stream of the caller's; a replay reads the groups and lengths of its time."""
+    b, c = Batch(8, 2, 128, 16, [(3, 4), (2, 3)], [5, 0, 40, 1, 9]), Batch(8, 2, 128, 20, [(2, 9), (3, 30)], [50, 7, 40, 1, 0], seed=3)
+    sizes = [sfi.paged_shared_workspace(x.lay).numel() for x in (b, c)]
+    ws = torch.zeros(max(sizes), dtype=torch.uint8, device="cuda")
+    want = [b.run(sfi), c.run(sfi)]
+    args, outs, graphs = [], [], []
+    for x in (b, c):
+        args.append((x.lay, ints(x.cu), ints(x.shared), x.q, x.k, x.v))
+        outs.append((torch.zeros(5, 8, 128, device="cuda"), torch.zeros(5, 8, device="cuda")))
+        sfi.sfi_paged_attn_shared(*args[-1], *outs[-1], ws)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            sfi.sfi_paged_attn_shared(*args[-1], *outs[-1], ws)
+    eager = tuple(torch.zeros_like(t) for t in outs[0])
+    st = torch.cuda.Stream()
+    for _ in range(3):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            for g in graphs:
+                g.replay()
+            sfi.sfi_paged_attn_shared(*args[0], *eager, ws)
+        st.synchronize()
+        for got, good in zip(outs + [eager], want + want[:1]):
+            assert torch.equal(got[0], good[0]) and torch.equal(got[1], good[1])
+    args[0][2].copy_(ints([2, 0]))  # fewer pages, and a group that shares nothing
+    b.len[0] -= 3
+    b.lens[0] -= 3
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    b.check(*outs[0])
+    assert sfi.sfi_read_status(ws) == 0
+
+
 def test_forked_sequences_decode(sfi):
     """A prompt, forked; every sequence appends tokens, some of them captured in a graph: the group attends
     as each by itself does."""
