@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) paged_attn_q8_kernel(const __g
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 float& z = s[i >> 1][h][(i & 1) * 2 + e];
-                z = r8 + 8 * i < left ? z * kscale[i] * fac[h][e] : -INFINITY;
+                z = r8 + 8 * i < left ? z * (kscale[i] * fac[h][e]) : -INFINITY;  // (large times small first)
               }
               top[e] = fmaxf(fmaxf(s[0][h][e], s[0][h][2 + e]), fmaxf(s[1][h][e], s[1][h][2 + e]));
 #pragma unroll

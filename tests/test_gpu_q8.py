@@ -152,6 +152,16 @@ def test_scales_of_all_sizes(sfi, fmt, dtype):
         c.check(q, *c.run(sfi, q))
 
 
+@pytest.mark.parametrize("fmt,dtype", [(I8, BF16), (E4M3, F32)])
+@pytest.mark.parametrize("up", [90, -90])
+def test_large_keys_and_small_queries(sfi, fmt, dtype, up):
+    """And the other way round: scores of the usual size."""
+    c = Cache(sfi, 4, 2, 128, fmt, 16, [200, 33])
+    c.lay.scales(c.k).mul_(2.0 ** up)
+    q = (normal((2, 4, 128), F32, 22) * 2.0 ** -up).to(dtype)
+    c.check(q, *c.run(sfi, q))
+
+
 @pytest.mark.parametrize("up", [20, 40])
 @pytest.mark.parametrize("fmt,dtype", [(I8, BF16), (E4M3, F32)])
 def test_large_values_that_a_head_leaves_out(sfi, fmt, dtype, up):
