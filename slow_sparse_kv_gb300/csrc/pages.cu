@@ -11,7 +11,7 @@
 // compaction's plan 4.6 and its moves of 352 MB 52 (6.77 TB/s), a token's rows for
 // 64 sequences 6.0, a prompt batch's 267 MB 37 to 39.  Into a cache in 8 bits: 37000 positions of 8 heads
 // of 128 in bf16 (231 MB) as e4m3 in 39.5, 5.8 TB/s (the issue slots are nearly as full: the rounding comes
-// next after HBM), as int8 in 50, bound by the rounding; from fp32 (383 MB) in 60, 6.4 TB/s; a token's
+// next after HBM), as int8 in 48, bound by the rounding; from fp32 (383 MB) in 60, 6.4 TB/s; a token's
 // rows for 64 sequences 4.8.  (A token's first heads read before its sequence is looked up: 41.3, 52, 62, 5.9.)
 // Free pages are looked for from the lowest on, 4096 counts a round of 0.9 us: extending
 // 64 sequences takes 3.7 us where the first round finds them, 18 with the low 95% of
@@ -567,7 +567,11 @@ __device__ __forceinline__ uint2 quantise(const float (&x)[8], uint32_t top, flo
     }
   } else {
     constexpr float BIG = 12582912.f;
-    const float s = __uint_as_float(top) / 127.f, inv = 1.f / s, half = 0.5f * s;
+    // max / 127 by the rounded reciprocal and one correction by the remainder, which rounds the quotient
+    // correctly (Markstein's theorem; all 2^23 significands were compared).  1 / s may be off.
+    constexpr float kInv = 1.f / 127.f;
+    const float amax = __uint_as_float(top), s0 = amax * kInv, s = fmaf(fmaf(-s0, 127.f, amax), kInv, s0);
+    const float inv = __fdividef(1.f, s), half = 0.5f * s;
     *scale = s;
     float t[8], worst = 0.f;
 #pragma unroll

@@ -393,6 +393,28 @@ def test_append_stores_the_exact_codes(sfi, fmt, dtype, d, hkv, page):
         assert torch.equal(got[:, tail:], was[:, tail:])
 
 
+def test_int8_scales_are_rounded_quotients(sfi):
+    """2^20 rows of fp32 whose largest elements go over the significands and the exponents of both ways to the
+    scale, and of whose other elements one is half of that, next to a tie."""
+    n, hkv, d, page = 1 << 17, 8, 64, 1024
+    lay = sfi.PagedLayout(hkv, hkv, d, I8, page, n // page, ints([list(range(n // page))]), ints([n]))
+    x = torch.zeros(n, hkv, d)
+    at = torch.arange(n * hkv, dtype=torch.int64)
+    bits = (at * 8 + at % 8) % (1 << 23) | (60 + at * 7 % 180) << 23
+    top = bits.int().view(torch.float32).view(n, hkv)
+    x[..., 5], x[..., 9] = top, -0.5 * top
+    k, v = (torch.zeros(n // page, lay.page_bytes, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ws = sfi.paged_workspace(lay)
+    sfi.sfi_paged_append_q8(lay, x.cuda(), -x.cuda(), k, v, ints([0, n]), ws)
+    assert sfi.sfi_read_status(ws) == 0
+    scale = torch.from_numpy(top.numpy() / np.float32(127))
+    half = torch.from_numpy(np.rint(0.5 * top.numpy().astype(np.float64) / scale.numpy())).to(I8)
+    for pool, sign in ((k, 1), (v, -1)):
+        codes, scales = (t.cpu().transpose(1, 2).flatten(0, 1) for t in (lay.codes(pool), lay.scales(pool)))
+        assert torch.equal(scales, scale)
+        assert (codes[..., 5] == sign * 127).all() and torch.equal(codes[..., 9], -sign * half)
+
+
 def test_append_one_row_each_and_idle_slots(sfi):
     lens = [5, 0, 33, 16]
     n_pages, rows = pool_of(lens, 16, 2, 7)
