@@ -710,11 +710,12 @@ __global__ void __launch_bounds__(kSharedThreads, 1) shared_attn_kernel(const __
 // positions too, where each read touches 32 lines: 25 us for 256 rows of 20 pieces.)
 struct State {
   float m = -INFINITY, l = 0.f;
-  // Takes in N states; returns the factors of what it was and of theirs.  One that saw only scores of
-  // -infinity, or nothing, adds nothing; any other's factor is above 0, so that its NaNs and
-  // infinities reach the result.
+  // Takes in N states; returns the factors of what it was and of theirs: -1 for one that saw only
+  // scores of -infinity, or nothing, and adds nothing.  Any other's is its weight, which may be 0 in
+  // fp32: its finite sums then add nothing, and its NaNs and infinities reach the result, since 0
+  // times one is NaN.  (A floor under the weights would let large finite sums through: 2^-126 of 5e37.)
   static __device__ __forceinline__ float factor(float m, float l, float top, float c) {
-    return m == -INFINITY && l == 0.f ? 0.f : fmaxf(ex2((m - top) * c), 0x1p-126f);
+    return m == -INFINITY && l == 0.f ? -1.f : ex2((m - top) * c);
   }
   template <int N>
   __device__ __forceinline__ float take(const float (&mv)[N], const float (&lv)[N], float (&f)[N], float c) {
@@ -722,11 +723,11 @@ struct State {
 #pragma unroll
     for (int w = 0; w < N; ++w) top = fmaxf(top, mv[w]);
     const float was = factor(m, l, top, c);
-    l = was == 0.f ? 0.f : l * was;
+    l = was < 0.f ? 0.f : l * was;
 #pragma unroll
     for (int w = 0; w < N; ++w) {
       f[w] = factor(mv[w], lv[w], top, c);
-      l = f[w] == 0.f ? l : fmaf(f[w], lv[w], l);
+      l = f[w] < 0.f ? l : fmaf(f[w], lv[w], l);
     }
     m = top;
     return was;
@@ -794,9 +795,9 @@ __global__ void __launch_bounds__(kThreads, kJoinCtas) shared_join_kernel(const 
         const float was = st.take(mv, lv, f, c);
 #pragma unroll
         for (int e = 0; e < kJoinCols; ++e) {
-          o[e] = was == 0.f ? 0.f : o[e] * was;
+          o[e] = was < 0.f ? 0.f : o[e] * was;
 #pragma unroll
-          for (int k = 0; k < AHEAD; ++k) o[e] = f[k] == 0.f ? o[e] : fmaf(f[k], v[k][e], o[e]);
+          for (int k = 0; k < AHEAD; ++k) o[e] = f[k] < 0.f ? o[e] : fmaf(f[k], v[k][e], o[e]);
         }
       }
 #pragma unroll
@@ -815,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, kJoinCtas) shared_join_kernel(const 
       st.take(mv, lv, f, c);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
-        if (f[w] != 0.f) o.x = fmaf(f[w], o_sh[w][col][row], o.x), o.y = fmaf(f[w], o_sh[w][col + 1][row], o.y);
+        if (!(f[w] < 0.f)) o.x = fmaf(f[w], o_sh[w][col][row], o.x), o.y = fmaf(f[w], o_sh[w][col + 1][row], o.y);
     }
     const long long nt = own1 - own0, o0 = own0 * H_kv + g * nt;
     if (nt > 0) {
@@ -834,10 +835,10 @@ __global__ void __launch_bounds__(kThreads, kJoinCtas) shared_join_kernel(const 
           v[k] = there ? __ldcg(reinterpret_cast<const float2*>(p + k * step + d0 + col)) : make_float2(0.f, 0.f);
         }
         const float was = st.take(mv, lv, f, c);
-        o.x = was == 0.f ? 0.f : o.x * was, o.y = was == 0.f ? 0.f : o.y * was;
+        o.x = was < 0.f ? 0.f : o.x * was, o.y = was < 0.f ? 0.f : o.y * was;
 #pragma unroll
         for (int k = 0; k < OWN; ++k)
-          if (f[k] != 0.f) o.x = fmaf(f[k], v[k].x, o.x), o.y = fmaf(f[k], v[k].y, o.y);
+          if (!(f[k] < 0.f)) o.x = fmaf(f[k], v[k].x, o.x), o.y = fmaf(f[k], v[k].y, o.y);
       }
     }
     const int64_t to = int64_t(b) * a.own.H_q + g * G + head;
