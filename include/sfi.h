@@ -333,7 +333,9 @@ sfi_status sfi_fast_attn_noalloc(const sfi_layout* layout, const sfi_params* par
  *  - dtype SFI_F32 or SFI_BF16; head_dim 64 or 128; up to 4096 heads each.  n_kv_heads = 0
  *    (or n_q_heads = 0) leaves k (q) out; its pointers are not read.
  *  - total = 0 is a call that does nothing.
- * One launch, no workspace.  A head whose sum of squares leaves fp32 is 0. */
+ * One launch, no workspace.  Finite heads of any size are normed as the formula says, also where
+ * their squares leave fp32 on either side; a head of zeros stays zero, with eps = 0 too.  In a head
+ * with an infinity the norm makes that NaN and the others 0; a NaN makes all of its head NaN. */
 typedef struct {
   int32_t total; /* rows */
   int32_t n_q_heads;

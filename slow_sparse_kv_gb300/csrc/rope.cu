@@ -15,7 +15,7 @@
 // exchanged but the sum of squares (d / 8 lanes a head), and reads and writes the same
 // places, so that a call may work in place.  A row's warp computes its four angles once
 // for all heads, and once for its query and its key heads the products of weight and cosine
-// or sine, so that a head costs a rotation and a factor: with the weights read and applied head by
+// or sine, so that a head costs a factor and a rotation: with the weights read and applied head by
 // head the instructions took longer than HBM, 67 us for 16384 rows of 32 + 8 heads of 128.
 //
 // Bound by HBM, 2 e d bytes a head.  Measured: those 16384 rows in bf16 (336 MB) in 58 us,
@@ -69,6 +69,36 @@ __device__ __forceinline__ void from_pairs(const uint64_t (&u)[2], const uint64_
     x[0] = lo(u[0]), x[1] = hi(u[0]), x[2] = lo(u[1]), x[3] = hi(u[1]);
     y[0] = lo(v[0]), y[1] = hi(v[0]), y[2] = lo(v[1]), y[3] = hi(v[1]);
   }
+}
+
+// The mean of a head's squares, over its d / 8 lanes.
+template <int D>
+__device__ __forceinline__ float mean_squares(const uint64_t (&xu)[2], const uint64_t (&xv)[2]) {
+  const uint64_t q = fma2(xu[0], xu[0], fma2(xu[1], xu[1], fma2(xv[0], xv[0], mul2(xv[1], xv[1]))));
+  float sum = lo(q) + hi(q);
+#pragma unroll
+  for (int w = 1; w < D / 8; w <<= 1) sum += __shfl_xor_sync(kFull, sum, w);
+  return sum * (1.f / D);
+}
+
+// Mean square + eps between which squares are safe: no element is above 2^54, and what its square
+// loses below 2^-126 is less than 2^-26 of the sum.  Beyond, a warp squares its heads times a power of two
+// again; a head's factor r then goes with elements that are scaled too, so that r itself stays
+// a normal number: x / sqrt(v) = (x f) (r).  The heads beside keep their bits (f = 1).
+constexpr float kLeast = 0x1p-100f, kMost = 0x1p100f;
+template <int D>
+__device__ __forceinline__ float far_norm(uint64_t (&xu)[2], uint64_t (&xv)[2], float v, float eps) {
+  const bool large = !(v <= kMost);  // (NaN too)
+  const float up = large ? 0x1p-96f : v < kLeast ? 0x1p96f : 1.f;
+  const uint64_t uu = pair(up, up);
+  const uint64_t su[2] = {mul2(xu[0], uu), mul2(xu[1], uu)}, sv[2] = {mul2(xv[0], uu), mul2(xv[1], uu)};
+  const float z = mean_squares<D>(su, sv) + eps * up * up;
+  const float r = z == 0.f ? 0.f : rsqrtf(z);  // (a head of zeros without eps stays one)
+  const float f = large ? 0x1p-8f : up;
+  const uint64_t ff = pair(f, f);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) xu[e] = mul2(xu[e], ff), xv[e] = mul2(xv[e], ff);
+  return large ? r * 0x1p-88f : r;
 }
 
 // FULL: all d dimensions are rotated.  CTAS: on an SM at least.
@@ -146,21 +176,21 @@ __global__ void __launch_bounds__(kThreads, CTAS) rope_kernel(const __grid_const
         x0[j].get(p), x1[j].get(o);
         uint64_t xu[2], xv[2], yu[2], yv[2];
         to_pairs<NEXT>(p, o, xu, xv);
-        uint64_t rr = pair(1.f, 1.f);
         if (a.norm) {
-          const uint64_t q = fma2(xu[0], xu[0], fma2(xu[1], xu[1], fma2(xv[0], xv[0], mul2(xv[1], xv[1]))));
-          float sum = lo(q) + hi(q);
+          const float v = mean_squares<D>(xu, xv) + a.eps;
+          float r = rsqrtf(v);
+          if (__any_sync(kFull, !(v >= kLeast && v <= kMost))) r = far_norm<D>(xu, xv, v, a.eps);
+          // (before the weights: their product with an element may be more than fp32 holds)
+          const uint64_t rr = pair(r, r);
 #pragma unroll
-          for (int w = 1; w < LPH; w <<= 1) sum += __shfl_xor_sync(kFull, sum, w);
-          const float r = rsqrtf(sum * (1.f / D) + a.eps);
-          rr = pair(r, r);
+          for (int e = 0; e < 2; ++e) xu[e] = mul2(xu[e], rr), xv[e] = mul2(xv[e], rr);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          yu[e] = mul2(fma2(xu[e], wc[e], mul2(xv[e], vs[e])), rr);
-          yv[e] = mul2(fma2(xu[e], ws[e], mul2(xv[e], vc[e])), rr);
+          yu[e] = fma2(xu[e], wc[e], mul2(xv[e], vs[e]));
+          yv[e] = fma2(xu[e], ws[e], mul2(xv[e], vc[e]));
           // (what is not rotated stays as it is, infinities among it)
-          if (!FULL && !turns) yu[e] = mul2(mul2(xu[e], wc[e]), rr), yv[e] = mul2(mul2(xv[e], vc[e]), rr);
+          if (!FULL && !turns) yu[e] = mul2(xu[e], wc[e]), yv[e] = mul2(xv[e], vc[e]);
         }
         if (first + j * HPW >= heads) continue;
         from_pairs<NEXT>(yu, yv, p, o);
