@@ -474,16 +474,17 @@ sfi_status sfi_paged_attn_shared(const sfi_paged_layout* L, int32_t n_groups, co
   if ((s = fill_attn(L, q, k, v, out, lse_out, ws, ws_bytes, w.total, &a.own, &use_tma)) != SFI_OK) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int D = L->head_dim, grid = attn_grid();
-  if (w.max_tiles == 0) {  // nobody shares anything
-    const cudaError_t e = launch_paged_attn(a.own, D, false, use_tma, grid, st);
-    return e == cudaSuccess ? SFI_OK : cuda_fail(e, "paged attention launch");
-  }
-  char* const base = static_cast<char*>(ws);
   a.tok = 128 / a.own.G;
   a.max_tiles = w.max_tiles;
   a.n_groups = n_groups;
   a.cu_group = cu_group;
   a.shared_pages = shared_pages;
+  if (w.max_tiles == 0) {  // nobody shares anything
+    cudaError_t e = n_groups > 0 ? launch_check_groups(a, st) : cudaSuccess;
+    if (e == cudaSuccess) e = launch_paged_attn(a.own, D, false, use_tma, grid, st);
+    return e == cudaSuccess ? SFI_OK : cuda_fail(e, "paged attention launch");
+  }
+  char* const base = static_cast<char*>(ws);
   a.skip = reinterpret_cast<int32_t*>(base + w.skip);
   a.own.geo.skip = a.skip;
   a.plan = reinterpret_cast<SharedPlan*>(base + w.plan);

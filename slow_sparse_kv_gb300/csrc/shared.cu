@@ -178,6 +178,14 @@ __device__ __forceinline__ int make_plan(const SharedArgs& a, SharedMem& sh, boo
   return groups;
 }
 
+// Flags what is wrong with the groups where nothing can be shared (one CTA).
+__global__ void __launch_bounds__(kSharedThreads) check_groups_kernel(const __grid_constant__ SharedArgs a) {
+  __shared__ SharedMem sh;
+  pdl_launch();
+  pdl_wait();
+  make_plan(a, sh, true);
+}
+
 // Leaves the plan for the kernels behind (one warp of the first CTA, beside the others' work).
 __device__ __forceinline__ void publish_plan(const SharedArgs& a, const SharedMem& sh, int groups) {
   const PagedGeo& geo = a.own.geo;
@@ -870,6 +878,10 @@ cudaError_t launch_shared(const SharedArgs& a, bool own_tma, int grid, cudaStrea
 }
 
 }  // namespace
+
+cudaError_t launch_check_groups(const SharedArgs& a, cudaStream_t st) {
+  return launch_pdl(check_groups_kernel, dim3(1), kSharedThreads, 0, st, a);
+}
 
 cudaError_t launch_shared_attn(const SharedArgs& a, int D, bool use_tma, int grid, cudaStream_t st) {
   if (D == 64) return a.box ? launch_shared<64, true>(a, use_tma, grid, st) : launch_shared<64, false>(a, use_tma, grid, st);

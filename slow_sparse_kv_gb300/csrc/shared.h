@@ -43,6 +43,8 @@ struct SharedArgs {
   PagedAttnArgs own;  // the sequences' own positions (geo.skip is set)
 };
 
+// Flags groups that are wrong, and nothing else (a batch of one, where no group can share).
+cudaError_t launch_check_groups(const SharedArgs& a, cudaStream_t st);
 cudaError_t launch_shared_attn(const SharedArgs& a, int D, bool use_tma, int grid, cudaStream_t st);
 
 }  // namespace sfi

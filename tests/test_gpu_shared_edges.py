@@ -1,5 +1,5 @@
 """Attention for sequences that share their first pages (sfi_paged_attn_shared): what the softmax leaves
-out weighs nothing, as in sfi_paged_attn."""
+out weighs nothing, as in sfi_paged_attn; and what is flagged."""
 import pytest
 import torch
 
@@ -71,3 +71,20 @@ def test_large_values_of_a_whole_prefix(sfi, page):
     for seq in range(3):
         leave_out(b, seq, range(288, b.lens[seq]), 1e36)
     check_kept(b, *b.run(sfi))
+
+
+@gpu
+def test_groups_of_a_batch_of_one(sfi):
+    """Nothing can be shared, but what the groups say is looked at all the same."""
+    b = Batch(8, 2, 128, 16, [(1, 4)], [9])
+    good = b.run(sfi)
+    b.check(*good)
+    for cu, shared, status in (([0, 1], [4], 0), ([0, 0], [4], 0), ([1, 1], [4], 0), ([0, 1], [0], 0),
+                               ([0, 2], [4], sfi.SFI_DEV_LEN_OVER_CAP), ([-1, 1], [4], sfi.SFI_DEV_LEN_OVER_CAP),
+                               ([1, 0], [4], sfi.SFI_DEV_LEN_OVER_CAP), ([0, 1, 0], [4, 0], sfi.SFI_DEV_LEN_OVER_CAP),
+                               ([0, 1], [-1], sfi.SFI_DEV_LEN_OVER_CAP), ([0, 1], [1000], sfi.SFI_DEV_LEN_OVER_CAP),
+                               ([0, 1], [5], sfi.SFI_DEV_LEN_OVER_CAP)):
+        out, lse = b.run(sfi, status=status, cu=cu, shared=shared)
+        assert torch.equal(out, good[0]) and torch.equal(lse, good[1]), (cu, shared)
+    none = b.run(sfi, cu=[0], shared=[])
+    assert torch.equal(none[0], good[0]) and torch.equal(none[1], good[1])
