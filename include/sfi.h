@@ -471,6 +471,8 @@ size_t sfi_paged_workspace_size(const sfi_paged_layout* layout);
  * past len[b] may hold anything.  An element of V before it that is not finite makes
  * its column of the outputs that attend to it not finite, and no other: in bf16 it may
  * be NaN where the sum is infinite (a probability is added in terms of both signs).
+ * Sums are divided at the end, their weights being up to 2^8: values of V up to 2^119 / len[b]
+ * stay finite on the way.
  * Two launches: all rows of all sequences are dealt over the SMs, and a small second
  * kernel joins the pieces of each split (sequence, KV head) in a fixed order: the same
  * call gives the same bits, but where a sequence is split, and so the order of its fp32
@@ -493,13 +495,19 @@ sfi_status sfi_paged_attn(const sfi_paged_layout* layout, const void* q, const v
  *    anything; a number of pages outside [0, max_pages], or more than one of the group's
  *    sequences holds, sets it too, and that group shares nothing: each then reads its own
  *    row of the table, and the result is the same.
+ *  - It pays where much is not read again: (sequences - 1) * shared positions * H_kv * d * 4 bytes,
+ *    summed over the groups.  From 0.5 GB on it is faster than sfi_paged_attn; below 0.25 GB
+ *    sfi_paged_attn mostly is, by up to 30 us (groups of 2 to 64 behind 64 to 32768 positions,
+ *    2 x 64 and 8 x 128 a row).  The call does not choose.
  *  - Probabilities are not rounded: they go through the tensor cores as three bf16 terms, all
  *    else is fp32.  An element of V in the shared part that is not finite may make its column of the
  *    group's outputs NaN where it would be infinite.
  *  - The same call gives the same bits.
  * The workspace (sfi_paged_shared_workspace_size, 0 for invalid arguments; it grows with
  * n_groups, and one for more groups serves fewer) holds that of the paged calls and serves them
- * too.  Three launches. */
+ * too.  Most of it are 1 KB * (d + 2) for each KV head of a group (of two sequences at least; larger
+ * ones count once for each 256 / G) and 256 times that: 75 MB for 64 sequences with 8 x 128 a
+ * row and G = 4, 43 MB where n_groups is 1.  Three launches. */
 size_t sfi_paged_shared_workspace_size(const sfi_paged_layout* layout, int32_t n_groups);
 sfi_status sfi_paged_attn_shared(const sfi_paged_layout* layout, int32_t n_groups,
                                  const int32_t* cu_group, const int32_t* shared_pages,
@@ -614,8 +622,10 @@ sfi_status sfi_paged_append_q8(const sfi_paged_layout* layout, int32_t new_dtype
                                void* v, void* ws, size_t ws_bytes, sfi_stream stream);
 
 /* sfi_paged_attn over an 8-bit pool, for q of q_dtype (SFI_F32 or SFI_BF16); out and lse_out
- * fp32.  K and V enter as the numbers that they stand for; scores, softmax and sums are
- * fp32.  Rows at or past len[b] may hold anything.  The rest as there. */
+ * fp32.  K and V enter as the numbers that they stand for; scores, maxima and sums are fp32.
+ * The products take fp16 terms: bf16 queries are exact down to 2^-32 of their head's largest
+ * element; fp32 queries keep 22 bits, or are off by 2^-39 of that largest one, and so are
+ * probabilities times V's scales, the largest being that of a head's 32 positions.  Rows at or past len[b] may hold anything.  The rest as there. */
 sfi_status sfi_paged_attn_q8(const sfi_paged_layout* layout, int32_t q_dtype, const void* q,
                              const void* k, const void* v, float* out, float* lse_out, void* ws,
                              size_t ws_bytes, sfi_stream stream);

@@ -28,7 +28,9 @@
 // e4m3 (1.23 GB) in 197 us, 6.2 TB/s, with pages of 16 and 191 with pages of 64: a tile of two pages
 // takes eight copies and not four.  (A copying lane that works its tile's addresses out while it
 // issues the copies: 213.  Scales copied 4 bytes a lane: 220, and 98 for the other.)  One
-// sequence of 700 11.9 us, the two launches.  128 heads (16 a group), 8 x 32768: 126.
+// sequence of 700 10.5 us, the two launches.  8 x 32768 with fp32 queries: 93.  128 heads (16 a
+// group): 125, with fp32 queries 147: the issue slots.  64 sequences of 1 to 32 with one KV head: 25, since a
+// share is eight tiles and these lie in eight units, one after another.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -25,7 +25,9 @@
 // pipe is active for 55% of the cycles; 7 before the first product, 4 for taking sums out of
 // tensor memory), 19 and 14; that these run one after another is what is left to gain.  5 groups of
 // 9 behind 6000 positions in pages of 24: 62 us (32, 12 and 14).  6 sequences, 8 / 2 heads of 64,
-// behind 600 positions: 18 us (6.5, 4.3 and 5.3).
+// behind 600 positions: 18 us (6.5, 4.3 and 5.3).  sfi_paged_attn on the same sequences is faster where less than
+// 0.25 GB is saved: 2 behind 8192 28 us and 15, 4 behind 32768 60 and 47, 16 behind 8192 29 and 49, 64 behind
+// 512 29 each, behind 32768 86 and 615 (100 own positions each, in a row of calls).
 #include <cuda_runtime.h>
 
 #include <atomic>
